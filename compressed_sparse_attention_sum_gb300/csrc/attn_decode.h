@@ -1,0 +1,93 @@
+// Arguments and split of csa_attn_decode, shared by its kernels and the entry
+// point (internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache_format.cuh"
+
+namespace csa {
+
+constexpr int kDecodeTile = 64;      // slots of one tile of the split
+constexpr int kDecodeSms = 152;      // SMs of a GB300
+
+struct AttnDecodeArgs {
+  const void* q;
+  const uint8_t* cache;
+  const int32_t* raw_table;
+  const int32_t* cmp_table;
+  const int32_t* idx;
+  const float* sink;
+  const int32_t* seq_lens;
+  float scale;
+  void* o;
+  float* lse;
+  float* part_o;       // [b * s_q][splits][H][d], not normalized (splits > 1)
+  float2* part_ml;     // [b * s_q][splits][H]: running maximum (log2 units), sum
+  int b, s_q, H, d, ratio, window, K, P_raw, P_cmp, splits;
+  CacheShape cs;
+  int* status;
+};
+
+// Slots of one query are numbered: the window's `window` positions, then the
+// K index entries (or the visible blocks).  Every slot is looked up on its
+// own, so a split is a range of slots and needs no compaction; masked slots
+// (before position 0, -1 entries) have weight zero.
+struct DecodeRow {
+  int t;        // position of the query; < 0: nothing to attend to
+  int vis;      // visible compressed rows
+  int slots;    // slots of this query
+  int w0;       // position of slot 0 (may be negative)
+};
+
+__device__ __forceinline__ DecodeRow decode_row(const AttnDecodeArgs& a, int bi, int i) {
+  DecodeRow r;
+  int n = a.seq_lens[bi];
+  if (n < 0) {
+    set_status(a.status, kDevCheck, kSiteCacheRange);
+    n = 0;
+  }
+  r.t = n - a.s_q + i;
+  r.vis = r.t >= 0 ? (int)((unsigned)(r.t + 1) / (unsigned)a.ratio) : 0;
+  const long long cap = (long long)a.P_cmp * a.cs.page_size;
+  if (r.vis > cap) {
+    if (a.P_cmp > 0) set_status(a.status, kDevCheck, kSiteCacheRange);
+    r.vis = (int)cap;
+  }
+  r.w0 = r.t - a.window + 1;
+  r.slots = r.t < 0 ? 0 : a.window + (a.idx != nullptr ? a.K : r.vis);
+  return r;
+}
+
+// Byte offsets of slot s of the query (0 <= s < r.slots); false when masked.
+__device__ __forceinline__ bool decode_slot(const AttnDecodeArgs& a, const DecodeRow& r, int bi,
+                                            long long row, int s, long long* code,
+                                            long long* scale) {
+  if (s < a.window) {
+    const int pos = r.w0 + s;
+    if (pos < 0) return false;
+    const int slot = (int)((unsigned)pos % (unsigned)(a.P_raw * a.cs.page_size));
+    return cache_row(a.cs, a.raw_table + (long long)bi * a.P_raw, slot, code, scale, a.status);
+  }
+  const int k = s - a.window;
+  const int j = a.idx != nullptr ? a.idx[row * a.K + k] : k;
+  if (j < 0 || j >= r.vis) return false;
+  return cache_row(a.cs, a.cmp_table + (long long)bi * a.P_cmp, j, code, scale, a.status);
+}
+
+// Splits of each query's slots over CTAs: enough CTAs to fill the GPU twice
+// over, at most one per tile.
+inline int decode_splits(long long rows, int H_groups, long long slots) {
+  const long long tiles = (slots + kDecodeTile - 1) / kDecodeTile;
+  long long s = (2ll * kDecodeSms) / (rows * H_groups);
+  s = s < 1 ? 1 : s;
+  return (int)(s < tiles ? s : (tiles < 1 ? 1 : tiles));
+}
+
+// Combines the splits of every (row, head): o and lse.
+cudaError_t launch_attn_decode_combine(const AttnDecodeArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_attn_decode_simt(const AttnDecodeArgs& a, bool bf16, int bits,
+                                    cudaStream_t st);
+
+}  // namespace csa

@@ -1,0 +1,605 @@
+"""The serving calls on the GPU against the fp64 oracle: the quantised paged
+cache (byte for byte), the single-token indexer (exact sets) and the
+single-token attention (bounds derived below), their streams and graphs, and a
+decode loop that uses all of them together."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_sparse_attention_sum_gb300 import csa, serve
+from oracle import serve_oracle as orc
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, I32, U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+DEVICE_CHECK, SITE_PAGE, SITE_RANGE = 6, 0x71, 0x72
+POISON = 0xFF        # NaN codes and an infinite scale: no row that is not visible may matter
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from compressed_sparse_attention_sum_gb300 import build
+    build.build()
+    serve.load_library()
+    csa.csa_get_device_status()
+    yield
+    assert csa.csa_get_device_status() == 0
+
+
+def dev(x, dtype=None):
+    t = x if isinstance(x, torch.Tensor) else torch.as_tensor(np.asarray(x))
+    return t.to(dtype) .cuda() if dtype is not None else t.cuda()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def empty_cache(n_pages, page, d, bits, fill=POISON):
+    return torch.full((n_pages, serve.csa_cache_page_bytes(page, d, bits)), fill, dtype=U8,
+                      device="cuda")
+
+
+def tables(rng, b, *widths, spare=2):
+    """Page tables over one pool in random order; returns (n_pages, tables)."""
+    total = b * sum(widths)
+    ids = rng.permutation(total + spare)[:total]
+    out, at = [], 0
+    for w in widths:
+        out.append(ids[at:at + b * w].reshape(b, w).astype(np.int32))
+        at += b * w
+    return total + spare, out
+
+
+# ------------------------------------------------------------------ cache
+
+def special_rows(rng, shape, dtype):
+    """N(0, 1) rows with rounding ties, exact group maxima, zeros and extreme magnitudes."""
+    x = rng.standard_normal(shape).astype(np.float32)
+    flat = x.reshape(-1, 32)
+    n = len(flat)
+    flat[0 % n, :8] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0]
+    flat[0 % n, 8:] = np.clip(flat[0 % n, 8:], -6, 6)
+    flat[1 % n] = 0.0
+    flat[2 % n] *= np.float32(2.0 ** 100)
+    flat[3 % n] *= np.float32(2.0 ** -118)       # below the smallest scale
+    flat[4 % n, 3] = -448.0
+    flat[5 % n, 0] = np.float32(-6.0000005)
+    flat[6 % n] = -0.0
+    return torch.from_numpy(x).to(dtype)
+
+
+CACHE_CASES = [
+    # bits, dtype, d, page, b, s, P, pos0 (first), ragged
+    (4, BF, 128, 64, 3, 5, 2, 61, False),
+    (4, F32, 32, 16, 2, 17, 2, 0, True),
+    (4, BF, 512, 16, 2, 33, 4, 7, True),
+    (8, BF, 128, 48, 3, 50, 2, 40, True),
+    (8, F32, 64, 16, 1, 1, 1, 1000003, False),
+    (8, F32, 320, 16, 2, 40, 1, 11, False),      # more rows than the ring holds
+    (4, BF, 96, 16, 4, 70, 2, 2147483000, True),
+]
+
+
+@pytest.mark.parametrize("case", CACHE_CASES, ids=lambda c: f"{c[0]}bit_d{c[2]}_s{c[5]}_P{c[6]}")
+def test_write_bytes_and_read_back(case):
+    bits, dtype, d, page, b, s, P, first, ragged = case
+    rng = np.random.default_rng(d + s)
+    n_pages, (table,) = tables(rng, b, P)
+    pos0 = np.array([first + 3 * i for i in range(b)], np.int32)
+    counts = np.array([s] + [int(rng.integers(0, s + 1)) for _ in range(b - 1)] if ragged else [s] * b)
+    if ragged:
+        counts[-1] = 0 if b > 1 else s
+    x = special_rows(rng, (b, s, d), dtype)
+    # rows and batches at strides of their own, the gaps holding NaN
+    pitch, gap = d + 16, 24
+    buf = torch.full((b, s * pitch + gap), float("nan"), dtype=dtype, device="cuda")
+    xs = buf[:, :s * pitch].unflatten(1, (s, pitch))[..., :d]
+    xs.copy_(x)
+    cache = empty_cache(n_pages, page, d, bits)
+    before = cache.cpu().numpy()
+    got = serve.csa_cache_write(xs, cache, dev(table), dev(pos0), page, bits,
+                                counts=dev(counts, I32) if ragged else None)
+    assert got is cache
+    want = orc.write(before, f64(x), table, pos0, counts, page, bits)
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+    # read the newest rows that the ring still holds
+    ring = P * page
+    start = np.array([max(0, c - ring) for c in counts])
+    n = min(s, ring)
+    left = np.minimum(counts - start, n)
+    for out_dtype in (BF, F32):
+        out = torch.full((b, n, d + 8), 7.0, dtype=out_dtype, device="cuda")
+        serve.csa_cache_read(cache, dev(table), dev((pos0 + start).astype(np.int32)), out[..., :d], page,
+                             bits, counts=dev(left, I32))
+        got = f64(out)
+        assert (got[..., d:] == 7.0).all()
+        for i in range(b):
+            for r in range(n):
+                want_row = (orc.held_rows(f64(x)[i, start[i] + r][None], bits)[0] if r < left[i]
+                            else np.full(d, 7.0))
+                assert np.array_equal(got[i, r, :d], want_row), (i, r)
+
+
+def test_bad_pages_and_counts_are_skipped_and_recorded():
+    bits, d, page = 4, 64, 16
+    rng = np.random.default_rng(0)
+    x = torch.from_numpy(rng.standard_normal((3, 20, d))).to(BF)
+    table = np.array([[0, 5], [2, -1], [4, 3]], np.int32)          # 6 pages: 5 is inside, -1 and 99 are not
+    table_bad = table.copy()
+    table_bad[0, 1] = 99
+    cache = empty_cache(6, page, d, bits)
+    before = cache.cpu().numpy()
+    zeros = dev(np.zeros(3, np.int32))
+    serve.csa_cache_write(x.cuda(), cache, dev(table_bad), zeros, page, bits)
+    assert csa.csa_get_device_status(with_site=True) == (DEVICE_CHECK, SITE_PAGE)
+    want = orc.write(before, f64(x), table, [0, 0, 0], [16, 16, 20], page, bits)
+    assert np.array_equal(cache.cpu().numpy(), want)
+    out = torch.full((3, 20, d), 7.0, dtype=BF, device="cuda")
+    serve.csa_cache_read(cache, dev(table_bad), zeros, out, page, bits)
+    assert csa.csa_get_device_status(with_site=True) == (DEVICE_CHECK, SITE_PAGE)
+    held = orc.held_rows(f64(x), bits)
+    held[:2, 16:] = 0.0                                            # rows of the bad pages
+    assert np.array_equal(f64(out), held)
+    # counts outside [0, s] are clamped, a negative position moves nothing
+    cache = empty_cache(6, page, d, bits)
+    table[1, 1] = 1
+    serve.csa_cache_write(x.cuda(), cache, dev(table), dev(np.array([0, -4, 2], np.int32)), page, bits,
+                          counts=dev(np.array([-3, 20, 99], np.int32)))
+    assert csa.csa_get_device_status(with_site=True) == (DEVICE_CHECK, SITE_RANGE)
+    want = orc.write(before, f64(x), table, [0, 0, 2], [0, 0, 20], page, bits)
+    assert np.array_equal(cache.cpu().numpy(), want)
+
+
+def test_offsets_beyond_32_bits():
+    """A cache of 5.1 GB: pages whose byte offsets pass 2^32, for all four calls."""
+    bits, d, page = 8, 512, 64
+    page_bytes = serve.csa_cache_page_bytes(page, d, bits)
+    n_pages = (5 << 30) // page_bytes + 1
+    cache = torch.empty(n_pages, page_bytes, dtype=U8, device="cuda")
+    rng = np.random.default_rng(5)
+    raw_t, cmp_t = [[n_pages - 1, n_pages - 2]], [[n_pages - 5, 3]]
+    raw = torch.from_numpy(rng.standard_normal((1, 100, d))).to(BF)
+    cmp = torch.from_numpy(rng.standard_normal((1, 100, d))).to(BF)
+    zero = dev(np.zeros(1, np.int32))
+    for x, t in ((raw, raw_t), (cmp, cmp_t)):
+        serve.csa_cache_write(x.cuda(), cache, dev(t, I32), zero, page, bits)
+        out = torch.zeros(1, 100, d, dtype=F32, device="cuda")
+        serve.csa_cache_read(cache, dev(t, I32), zero, out, page, bits)
+        assert np.array_equal(f64(out), orc.held_rows(f64(x), bits))
+    q = torch.from_numpy(rng.standard_normal((1, 1, 64, d))).to(BF)
+    lens = dev(np.array([100], np.int32))
+    o, lse = serve.csa_attn_decode(q.cuda(), cache, dev(raw_t, I32), dev(cmp_t, I32), None, None, lens,
+                                   d ** -0.5, 1, 33, page, bits)
+    r, c = orc.held_rows(f64(raw[0]), bits), orc.held_rows(f64(cmp[0]), bits)
+    check_row(o[0, 0], lse[0, 0], f64(q)[0, 0], lambda p: r[p], lambda j: c[j], None, None, d ** -0.5, 99,
+              1, 33, BF)
+    del cache
+    d = 128
+    page_bytes = serve.csa_cache_page_bytes(page, d, bits)
+    n_pages = (5 << 30) // page_bytes + 1
+    cache = torch.empty(n_pages, page_bytes, dtype=U8, device="cuda")
+    keys = torch.from_numpy(rng.standard_normal((1, 100, d))).to(BF)
+    serve.csa_cache_write(keys.cuda(), cache, dev(cmp_t, I32) * 0 + dev([[n_pages - 1, n_pages - 4]], I32),
+                          zero, page, bits)
+    qi = torch.from_numpy(rng.standard_normal((1, 1, 64, d))).to(BF)
+    w = torch.from_numpy(rng.standard_normal((1, 1, 64))).float()
+    got = serve.csa_indexer_topk_decode(qi.cuda(), cache, dev([[n_pages - 1, n_pages - 4]], I32), w.cuda(),
+                                        lens, 20, 1, page, bits)
+    want = orc.index_row(f64(qi)[0, 0], f64(w)[0, 0], orc.held_rows(f64(keys[0]), bits), 99, 1, 20)
+    assert np.array_equal(got.cpu().numpy()[0, 0], want)
+
+
+# ---------------------------------------------------------------- indexer
+
+def index_case(rng, b, s_q, H, d, ratio, lens, bits, page, dtype, keys=None):
+    n = max(1, max(lens) // ratio)
+    P = -(-n // page)
+    n_pages, (table,) = tables(rng, b, P)
+    if keys is None:
+        keys = torch.from_numpy(rng.standard_normal((b, n, d))).to(BF)
+    cache = empty_cache(n_pages, page, d, bits)
+    serve.csa_cache_write(keys.cuda(), cache, dev(table), dev(np.zeros(b, np.int32)), page, bits)
+    q = torch.from_numpy(rng.standard_normal((b, s_q, H, d))).to(dtype)
+    w = torch.from_numpy(rng.standard_normal((b, s_q, H)) / 2).float()
+    return cache, table, keys, q, w
+
+
+def index_oracle(q, w, keys, lens, ratio, topk, bits):
+    b, s_q = q.shape[:2]
+    out = np.empty((b, s_q, topk), np.int64)
+    for s in range(b):
+        held = orc.held_rows(f64(keys[s]), bits)
+        for i in range(s_q):
+            out[s, i] = orc.index_row(f64(q)[s, i], f64(w)[s, i], held, lens[s] - s_q + i, ratio, topk)
+    return out
+
+
+INDEX_CASES = [
+    # b, s_q, H, d, ratio, lens, topk, bits, page, dtype
+    (1, 1, 64, 128, 4, [1200], 64, 4, 64, BF),
+    (4, 1, 64, 128, 4, [0, 1, 3, 2051], 100, 4, 16, BF),
+    (3, 2, 64, 128, 4, [1, 777, 1025], 33, 8, 48, BF),
+    (2, 3, 32, 128, 1, [300, 129], 128, 4, 64, BF),
+    (2, 1, 32, 64, 4, [1100, 515], 7, 8, 16, BF),
+    (2, 2, 8, 64, 2, [700, 2], 1, 4, 32, BF),
+    (1, 1, 3, 32, 4, [999], 17, 4, 16, BF),
+    (1, 2, 70, 96, 4, [640], 50, 8, 16, BF),
+    (2, 1, 4, 256, 4, [803, 90], 30, 8, 64, BF),
+    (2, 1, 64, 128, 4, [900, 37], 50, 4, 64, F32),
+    (1, 2, 5, 64, 3, [500], 20, 8, 16, F32),
+    (1, 1, 16, 128, 128, [40000], 512, 4, 64, BF),      # topk above the visible blocks
+]
+
+
+@pytest.mark.parametrize("case", INDEX_CASES, ids=lambda c: f"b{c[0]}s{c[1]}H{c[2]}d{c[3]}k{c[6]}_{c[7]}bit")
+def test_indexer_matches_oracle(case):
+    b, s_q, H, d, ratio, lens, topk, bits, page, dtype = case
+    rng = np.random.default_rng(H * d + topk)
+    cache, table, keys, q, w = index_case(rng, b, s_q, H, d, ratio, lens, bits, page, dtype)
+    got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev(lens, I32), topk, ratio,
+                                        page, bits)
+    assert np.array_equal(got.cpu().numpy(), index_oracle(q, w, keys, lens, ratio, topk, bits))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("kind", ["equal", "zero", "few", "swapped", "zero_w"])
+def test_indexer_ties_go_to_the_lower_block(kind, bits):
+    """Many blocks with exactly equal scores.  "swapped": a block's channels are
+    exchanged where q has equal values, so that the exact scores are equal while
+    sums of rounded numbers in channel order need not be."""
+    rng = np.random.default_rng(11)
+    H, d, ratio, page, n, topk = 64, 128, 1, 64, 700, 211
+    base = rng.integers(-6, 7, (5, d)).astype(np.float64)
+    q = np.repeat(rng.standard_normal((1, 1, H, d // 2)), 2, axis=-1)
+    keys = base[rng.integers(0, 5, n)]
+    if kind == "equal":
+        keys = np.repeat(base[:1], n, 0)
+    elif kind == "zero":
+        keys = np.zeros((n, d))
+    elif kind == "swapped":
+        flip = rng.random((n, d // 2)) < 0.5
+        pairs = np.repeat(base[:1], n, 0).reshape(n, d // 2, 2)
+        keys = np.where(flip[..., None], pairs[..., ::-1], pairs).reshape(n, d)
+    keys = torch.from_numpy(keys[None]).to(BF)
+    cache, table, keys, _, w = index_case(rng, 1, 1, H, d, ratio, [n], bits, page, BF, keys=keys)
+    q = torch.from_numpy(q).to(BF)
+    if kind == "zero_w":
+        w = w * 0
+    got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev([n], I32), topk, ratio,
+                                        page, bits).cpu().numpy()[0, 0]
+    held = orc.held_rows(f64(keys[0]), bits)
+    if kind == "few":
+        want = orc.index_row(f64(q)[0, 0], f64(w)[0, 0], held, n - 1, ratio, topk)
+    else:
+        want = np.arange(topk)
+    assert np.array_equal(got, want)
+
+
+def test_indexer_scores_closer_than_fp32():
+    """Blocks whose exact scores differ by far less than fp32 resolves: two
+    large channels cancel, a small third one decides."""
+    rng = np.random.default_rng(12)
+    n, d, H, topk = 300, 128, 32, 40
+    keys = np.zeros((n, d))
+    keys[:, 0], keys[:, 32] = 6.0, -6.0
+    keys[:, 64] = 6.0                                   # the group's scale is 1
+    tiny = rng.choice([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0], n)
+    keys[:, 65] = tiny
+    keys = torch.from_numpy(keys[None]).to(BF)
+    q = np.zeros((1, 1, H, d))
+    q[..., 0], q[..., 32] = 2.0 ** 20, 2.0 ** 20
+    q[..., 64], q[..., 65] = 1.0, 2.0 ** -12
+    cache, table, keys, _, w = index_case(rng, 1, 1, H, d, 1, [n], 4, 64, BF, keys=keys)
+    w = w.abs() + 0.1
+    got = serve.csa_indexer_topk_decode(torch.from_numpy(q).to(BF).cuda(), cache, dev(table), w.cuda(),
+                                        dev([n], I32), topk, 1, 64, 4).cpu().numpy()[0, 0]
+    assert np.array_equal(got, np.sort(np.argsort(-tiny, kind="stable")[:topk]))
+
+
+def test_indexer_does_not_depend_on_the_batch():
+    rng = np.random.default_rng(13)
+    lens = [2000, 1500, 1999]
+    cache, table, keys, q, w = index_case(rng, 3, 2, 64, 128, 4, lens, 4, 64, BF)
+    whole = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev(lens, I32), 99, 4, 64, 4)
+    for s in range(3):
+        alone = serve.csa_indexer_topk_decode(q[s:s + 1].cuda(), cache, dev(table[s:s + 1]), w[s:s + 1].cuda(),
+                                              dev(lens[s:s + 1], I32), 99, 4, 64, 4)
+        assert torch.equal(alone[0], whole[s])
+
+
+def test_indexer_long_row():
+    """One row over many tiles and several thousand places, against fp64 torch."""
+    rng = np.random.default_rng(14)
+    for bits, n, topk in ((4, 70001, 1024), (8, 30000, 5000)):
+        d, H, page = 128, 64, 64
+        keys = torch.from_numpy(rng.standard_normal((1, n, d)).astype(np.float32)).to(BF)
+        cache, table, keys, q, w = index_case(rng, 1, 1, H, d, 1, [n], bits, page, BF, keys=keys)
+        held = torch.zeros(1, n, d, dtype=F32, device="cuda")
+        serve.csa_cache_read(cache, dev(table), dev(np.zeros(1, np.int32)), held, page, bits)
+        score = ((held[0].double() @ q[0, 0].cuda().double().T).clamp(min=0)
+                 * w[0, 0].cuda().double()).sum(1)
+        want = score.sort(descending=True, stable=True).indices[:topk].sort().values
+        got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev([n], I32), topk, 1,
+                                            page, bits)
+        assert torch.equal(got[0, 0].long(), want)
+
+
+def test_indexer_bad_page_and_length():
+    rng = np.random.default_rng(15)
+    n, page = 200, 16
+    cache, table, keys, q, w = index_case(rng, 2, 1, 16, 64, 1, [n, n], 4, page, BF)
+    table = table.copy()
+    table[1, 3] = cache.shape[0]                        # keys 48..63 of sequence 1 score as zero keys
+    got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev([n, n], I32), 30, 1, page,
+                                        4).cpu().numpy()
+    assert csa.csa_get_device_status(with_site=True) == (DEVICE_CHECK, SITE_PAGE)
+    held = [orc.held_rows(f64(keys[s]), 4) for s in range(2)]
+    held[1][48:64] = 0.0
+    for s in range(2):
+        assert np.array_equal(got[s, 0], orc.index_row(f64(q)[s, 0], f64(w)[s, 0], held[s], n - 1, 1, 30))
+    # a length beyond the table is clamped to its slots, a negative one is empty
+    got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table * 0 + np.arange(13), I32), w.cuda(),
+                                        dev([-5, 100000], I32), 208, 1, page, 4).cpu().numpy()
+    assert csa.csa_get_device_status(with_site=True) == (DEVICE_CHECK, SITE_RANGE)
+    assert (got[0] == -1).all() and np.array_equal(got[1, 0], np.arange(208))
+
+
+# --------------------------------------------------------------- attention
+
+def check_row(o, lse, q, raw, cmp, idx, sink, scale, t, ratio, window, dtype):
+    """Bounds: a logit's fp32 dot errs by at most d 2^-23 of sum |q k| (products
+    summed in fp32, every sum rounded once), and e^x - 1 ~ x.  bf16 attention
+    may round each probability to bf16 (half a step: 2^-8 relative, with their
+    sum 2^-8 more) and rounds o once (2^-8); fp32 rounds nothing to fewer bits."""
+    want, want_lse, spread = orc.attend_row(q, raw, cmp, idx, sink, scale, t, ratio, window)
+    d = q.shape[-1]
+    big = 0.0
+    if t >= 0:
+        top = max(np.abs(raw(p)).max() for p in range(max(0, t - window + 1), t + 1))
+        js = range((t + 1) // ratio) if idx is None else [j for j in idx if 0 <= j < (t + 1) // ratio]
+        for j in js:
+            top = max(top, np.abs(cmp(int(j))).max())
+        big = np.abs(q).sum(-1).max() * top * scale
+    logit = 2 * d * 2.0 ** -23 * big + 2.0 ** -20
+    rel = logit + (2 * 2.0 ** -8 if dtype == BF else 0.0)
+    tol = rel * spread + (2.0 ** -8 if dtype == BF else 2.0 ** -23) * np.abs(want) + 1e-30
+    got = f64(o)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
+    got_lse = f64(lse)
+    inf = np.isinf(want_lse)
+    assert np.array_equal(got_lse[inf], want_lse[inf])
+    assert (np.abs(got_lse[~inf] - want_lse[~inf]) <= logit + 2.0 ** -22 * np.abs(want_lse[~inf])).all()
+
+
+ATTN_CASES = [
+    # b, s_q, H, d, ratio, window, lens, K (0: idx None; -1: no compressed rows), bits, page, dtype, sink
+    (1, 1, 32, 128, 4, 128, [700], 64, 4, 64, BF, True),
+    (5, 1, 32, 128, 4, 31, [0, 1, 5, 300, 1029], 100, 8, 64, BF, True),
+    (2, 3, 32, 128, 128, 128, [2, 1500], 0, 4, 64, BF, False),
+    (2, 1, 64, 512, 4, 128, [900, 77], 130, 4, 16, BF, True),
+    (2, 2, 64, 512, 4, 65, [515, 1], 33, 8, 48, BF, True),
+    (3, 1, 16, 64, 4, 16, [200, 16, 64], 17, 4, 16, BF, False),
+    (1, 2, 8, 64, 1, 7, [333], 0, 8, 16, BF, True),
+    (2, 1, 64, 256, 4, 100, [401, 640], 50, 4, 64, BF, True),
+    (1, 1, 3, 96, 2, 40, [150], 20, 8, 16, BF, False),
+    (1, 1, 128, 128, 4, 64, [260], 300, 4, 16, BF, True),
+    (2, 2, 32, 128, 4, 50, [90, 300], -1, 4, 16, BF, True),
+    (2, 1, 64, 512, 1, 1, [600, 1], 0, 4, 64, BF, False),
+    (2, 1, 8, 128, 4, 33, [500, 3], 40, 4, 16, F32, True),
+    (1, 2, 5, 160, 4, 12, [320], 0, 8, 32, F32, False),
+    (1, 1, 32, 512, 4, 128, [1000], 64, 4, 64, F32, True),
+]
+
+
+def attn_case(rng, case):
+    b, s_q, H, d, ratio, window, lens, K, bits, page, dtype, with_sink = case
+    n_c = max(1, max(lens) // ratio)
+    P_raw = -(-(window + s_q - 1) // page)
+    P_cmp = -(-n_c // page)
+    n_pages, (raw_t, cmp_t) = tables(rng, b, P_raw, P_cmp)
+    cache = empty_cache(n_pages, page, d, bits)
+    raw = torch.from_numpy(rng.standard_normal((b, max(max(lens), 1), d))).to(BF)
+    cmp = torch.from_numpy(rng.standard_normal((b, n_c, d))).to(BF)
+    serve.csa_cache_write(raw.cuda(), cache, dev(raw_t), dev(np.zeros(b, np.int32)), page, bits,
+                          counts=dev(lens, I32))
+    serve.csa_cache_write(cmp.cuda(), cache, dev(cmp_t), dev(np.zeros(b, np.int32)), page, bits,
+                          counts=dev([n // ratio for n in lens], I32))
+    idx = None
+    if K > 0:
+        # repeats, -1 and entries that are not visible yet, in no order
+        idx = rng.integers(-1, n_c + 3, (b, s_q, K)).astype(np.int32)
+        idx[0, 0, :] = -1 if lens[0] > 200 else idx[0, 0]
+        idx[-1, -1, K // 2:] = -1
+    q = torch.from_numpy(rng.standard_normal((b, s_q, H, d))).to(dtype)
+    sink = rng.standard_normal(H).astype(np.float32) if with_sink else None
+    return cache, raw_t, (None if K < 0 else cmp_t), raw, cmp, idx, q, sink
+
+
+def run_attn(case, parts, **kw):
+    b, s_q, H, d, ratio, window, lens, K, bits, page, dtype, _ = case
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = parts
+    return serve.csa_attn_decode(q.cuda(), cache, dev(raw_t), None if cmp_t is None else dev(cmp_t),
+                                 None if idx is None else dev(idx), None if sink is None else dev(sink),
+                                 dev(lens, I32), d ** -0.5, ratio, window, page, bits, **kw)
+
+
+@pytest.mark.parametrize("case", ATTN_CASES, ids=lambda c: f"b{c[0]}s{c[1]}H{c[2]}d{c[3]}r{c[4]}K{c[7]}_{c[8]}bit")
+def test_attention_matches_oracle(case):
+    b, s_q, H, d, ratio, window, lens, K, bits, page, dtype, _ = case
+    rng = np.random.default_rng(H + d + window)
+    parts = attn_case(rng, case)
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = parts
+    o, lse = run_attn(case, parts)
+    assert o.dtype == dtype and o.shape == q.shape and lse.dtype == F32
+    assert csa.csa_get_device_status() == 0
+    for s in range(b):
+        r = orc.held_rows(f64(raw[s, :max(1, lens[s])]), bits)
+        c = orc.held_rows(f64(cmp[s]), bits)
+        for i in range(s_q):
+            rows = [] if K < 0 else None if idx is None else idx[s, i]
+            check_row(o[s, i], lse[s, i], f64(q)[s, i], lambda p: r[p], lambda j: c[j], rows, sink,
+                      d ** -0.5, lens[s] - s_q + i, ratio, window, dtype)
+
+
+def test_attention_large_logits_and_dominant_sink():
+    """Logits of several hundred: the running maximum carries them; a sink far
+    above them leaves o near zero, far below it changes nothing."""
+    case = (1, 1, 32, 128, 4, 64, [400], 80, 8, 16, BF, True)
+    rng = np.random.default_rng(21)
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = attn_case(rng, case)
+    q = q * 30
+    r, c = orc.held_rows(f64(raw[0]), 8), orc.held_rows(f64(cmp[0]), 8)
+    for level in (-1000.0, 1000.0):
+        s = np.full(32, level, np.float32)
+        o, lse = run_attn(case, (cache, raw_t, cmp_t, raw, cmp, idx, q, s))
+        check_row(o[0, 0], lse[0, 0], f64(q)[0, 0], lambda p: r[p], lambda j: c[j], idx[0, 0], s, 128 ** -0.5,
+                  399, 4, 64, BF)
+
+
+def test_attention_bad_page_is_masked():
+    case = (2, 1, 16, 64, 1, 16, [100, 100], 0, 4, 16, BF, True)
+    rng = np.random.default_rng(22)
+    parts = list(attn_case(rng, case))
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = parts
+    cmp_t = cmp_t.copy()
+    cmp_t[1, 2] = -7                                    # blocks 32..47 of sequence 1
+    parts[2] = cmp_t
+    o, lse = run_attn(case, parts)
+    assert csa.csa_get_device_status(with_site=True) == (DEVICE_CHECK, SITE_PAGE)
+    for s in range(2):
+        r, c = orc.held_rows(f64(raw[s]), 4), orc.held_rows(f64(cmp[s]), 4)
+        rows = [j for j in range(100) if s == 0 or not 32 <= j < 48]
+        check_row(o[s, 0], lse[s, 0], f64(q)[s, 0], lambda p: r[p], lambda j: c[j], rows, sink, 0.125, 99, 1,
+                  16, BF)
+
+
+def test_attention_is_the_same_bits_every_time():
+    case = (2, 1, 64, 512, 4, 128, [900, 1700], 300, 4, 64, BF, True)
+    parts = attn_case(np.random.default_rng(23), case)
+    o, lse = run_attn(case, parts)
+    for _ in range(3):
+        o2, lse2 = run_attn(case, parts)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+# ---------------------------------------------- streams, graphs, together
+
+def test_calls_on_a_side_stream_and_in_two_graphs_that_share_workspaces():
+    rng = np.random.default_rng(31)
+    case = (2, 1, 32, 128, 4, 64, [500, 300], 50, 4, 16, BF, True)
+    parts = attn_case(rng, case)
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = parts
+    icache, itable, keys, qi, w = index_case(rng, 2, 1, 64, 128, 4, [500, 300], 4, 16, BF)
+    args = [dev(raw_t), dev(cmp_t), dev(sink), dev([500, 300], I32), dev(itable), qi.cuda(), w.cuda(), q.cuda()]
+    rt, ct, sk, lens, it, qi_d, w_d, q_d = args
+    ws_i = torch.empty(serve.csa_indexer_topk_decode_workspace_size(2, 1, 64, 128, it.shape[1] * 16), dtype=U8,
+                       device="cuda")
+    ws_a = torch.empty(serve.csa_attn_decode_workspace_size(2, 1, 32, 128, 64, 50), dtype=U8, device="cuda")
+
+    def step(out_idx, o, lse):
+        serve.csa_indexer_topk_decode(qi_d, icache, it, w_d, lens, 50, 4, 16, 4, workspace=ws_i, out_idx=out_idx)
+        serve.csa_attn_decode(q_d, cache, rt, ct, out_idx, sk, lens, 128 ** -0.5, 4, 64, 16, 4, workspace=ws_a,
+                              out=o, lse=lse)
+
+    def bufs():
+        return (torch.zeros(2, 1, 50, dtype=I32, device="cuda"), torch.zeros_like(q_d),
+                torch.zeros(2, 1, 32, device="cuda"))
+
+    ref = bufs()
+    step(*ref)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = bufs()
+    with torch.cuda.stream(side):
+        step(*got)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(ref, got))
+
+    graphs = []
+    for _ in range(2):
+        out = bufs()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(*out)
+        graphs.append((g, out))
+    for (g, out) in graphs:
+        for t in out:
+            t.zero_()
+        g.replay()
+        g.replay()
+    torch.cuda.synchronize()
+    for _, out in graphs:
+        assert all(torch.equal(x, y) for x, y in zip(ref, out))
+    # a replay reads the buffers as they are then: shorter sequences
+    lens.copy_(dev([77, 12], I32))
+    want = bufs()
+    step(*want)
+    graphs[0][0].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, graphs[0][1]))
+    assert not torch.equal(want[1], ref[1])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_decode_loop_matches_the_whole_sequence_calls(bits):
+    """Token by token: append the raw row; at the end of a block pool it
+    (csa_compress) and append the pooled row and the block's index key; select;
+    attend.  The whole-sequence calls on the rows read back select the same
+    blocks and give the same output up to both sides' rounding."""
+    g = torch.Generator().manual_seed(41)
+    b, n, H, d, H_I, d_I, ratio, window, topk, page = 2, 75, 32, 128, 64, 128, 4, 20, 6, 16
+    kv = torch.randn(b, n, d, generator=g).to(BF).cuda()
+    score = (torch.randn(b, n, d, generator=g) * 0.5).to(BF).cuda()
+    keys = torch.randn(b, n // ratio, d_I, generator=g).to(BF).cuda()
+    q = torch.randn(b, n, H, d, generator=g).to(BF).cuda()
+    q_I = torch.randn(b, n, H_I, d_I, generator=g).to(BF).cuda()
+    w = (torch.randn(b, n, H_I, generator=g) / 2).cuda()
+    sink = torch.randn(H, generator=g).cuda()
+    n_c = n // ratio
+    rng = np.random.default_rng(42)
+    P_all, P_cmp = -(-n // page), -(-n_c // page)
+    n_pages, (raw_t, cmp_t) = tables(rng, b, P_all, P_cmp)
+    i_pages, (key_t,) = tables(rng, b, P_cmp)
+    raw_t, cmp_t, key_t = dev(raw_t), dev(cmp_t), dev(key_t)
+    cache, icache = empty_cache(n_pages, page, d, bits), empty_cache(i_pages, page, d_I, bits)
+    O = torch.zeros(b, n, H, d, dtype=BF, device="cuda")
+    L = torch.zeros(b, n, H, device="cuda")
+    idx = torch.full((b, n, topk), -1, dtype=I32, device="cuda")
+    for t in range(n):
+        at = torch.full((b,), t, dtype=I32, device="cuda")
+        serve.csa_cache_write(kv[:, t:t + 1], cache, raw_t, at, page, bits)
+        if (t + 1) % ratio == 0:
+            blk = (t + 1) // ratio - 1
+            jj = torch.full((b,), blk, dtype=I32, device="cuda")
+            pooled = csa.csa_compress(kv[:, t + 1 - ratio:t + 1].contiguous(),
+                                      score[:, t + 1 - ratio:t + 1].contiguous(), ratio)
+            serve.csa_cache_write(pooled, cache, cmp_t, jj, page, bits)
+            serve.csa_cache_write(keys[:, blk:blk + 1], icache, key_t, jj, page, bits)
+        lens = at + 1
+        idx[:, t:t + 1] = serve.csa_indexer_topk_decode(q_I[:, t:t + 1].contiguous(), icache, key_t,
+                                                        w[:, t:t + 1].contiguous(), lens, topk, ratio, page, bits)
+        o, l = serve.csa_attn_decode(q[:, t:t + 1].contiguous(), cache, raw_t, cmp_t,
+                                     idx[:, t:t + 1].contiguous(), sink, lens, d ** -0.5, ratio, window, page,
+                                     bits)
+        O[:, t:t + 1], L[:, t:t + 1] = o, l
+    zero = torch.zeros(b, dtype=I32, device="cuda")
+    kv_full = torch.empty(b, n + n_c, d, dtype=BF, device="cuda")
+    serve.csa_cache_read(cache, raw_t, zero, kv_full[:, :n], page, bits)
+    serve.csa_cache_read(cache, cmp_t, zero, kv_full[:, n:], page, bits)
+    k_I = serve.csa_cache_read(icache, key_t, zero, torch.empty(b, n_c, d_I, dtype=BF, device="cuda"), page, bits)
+    ref_idx = csa.csa_indexer_topk(q_I, k_I, w, topk, ratio)
+    assert torch.equal(idx[..., :ref_idx.shape[2]], ref_idx)
+    ref_o, ref_l = csa.csa_attn_fwd(q, kv_full, idx, sink, d ** -0.5, ratio, window)
+    # each side: probabilities and their sum rounded to bf16 (2 x 2^-8) and o rounded once (2^-8), of at
+    # most the largest |v| of the row's slots
+    top = kv_full.float().abs().max().item()
+    assert (O.float() - ref_o.float()).abs().max().item() <= 2 * 3 * 2.0 ** -8 * top
+    rel = (O.float() - ref_o.float()).norm() / ref_o.float().norm()
+    assert rel.item() <= 2 * 3 * 2.0 ** -8
+    assert (L - ref_l).abs().max().item() <= 1e-4
+    assert csa.csa_get_device_status() == 0
