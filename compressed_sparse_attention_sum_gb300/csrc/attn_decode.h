@@ -9,7 +9,7 @@
 
 namespace csa {
 
-constexpr int kDecodeTile = 64;      // slots of one tile of the split
+constexpr int kDecodeTile = 64;      // slots of one tile of the split (CUDA cores)
 constexpr int kDecodeSms = 152;      // SMs of a GB300
 
 struct AttnDecodeArgs {
@@ -76,18 +76,50 @@ __device__ __forceinline__ bool decode_slot(const AttnDecodeArgs& a, const Decod
   return cache_row(a.cs, a.cmp_table + (long long)bi * a.P_cmp, j, code, scale, a.status);
 }
 
-// Splits of each query's slots over CTAs: enough CTAs to fill the GPU twice
-// over, at most one per tile.
-inline int decode_splits(long long rows, int H_groups, long long slots) {
-  const long long tiles = (slots + kDecodeTile - 1) / kDecodeTile;
-  long long s = (2ll * kDecodeSms) / (rows * H_groups);
-  s = s < 1 ? 1 : s;
-  return (int)(s < tiles ? s : (tiles < 1 ? 1 : tiles));
+// How a call is cut into CTAs: queries of one sequence that share a CTA (and
+// their groups), head groups, and splits of the slots.
+struct DecodePlan {
+  int cols, per_group, groups, head_groups, splits;
+};
+
+// Splits for `ctas` CTAs over `tiles` tiles each: as many as fit the GPU
+// `resident` times over, at most one per tile.
+inline int decode_splits(long long ctas, long long tiles, int resident) {
+  long long s = (long long)resident * kDecodeSms / ctas;
+  if (s > tiles) s = tiles;
+  return s < 1 ? 1 : (int)s;
+}
+
+inline DecodePlan decode_plan_simt(int b, int s_q, int H, int window, long long cmp_rows) {
+  DecodePlan p{8, 1, s_q, (H + 7) / 8, 1};
+  p.splits = decode_splits((long long)b * s_q * p.head_groups,
+                           (window + cmp_rows + kDecodeTile - 1) / kDecodeTile, 2);
+  return p;
+}
+
+inline bool decode_tc_width(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
+
+// Without an index list the queries of a sequence see the same rows (all but
+// the newest), so as many of them as fit 64 columns share a CTA.  Narrow
+// widths leave room for three CTAs on an SM, 512 for one.
+inline DecodePlan decode_plan_tc(int b, int s_q, int H, int d, int window, int K, bool dense,
+                                 long long cmp_cap) {
+  DecodePlan p{};
+  p.per_group = dense && H % 16 == 0 && H <= 32 ? 64 / H : 1;
+  if (p.per_group > s_q) p.per_group = s_q;
+  p.groups = (s_q + p.per_group - 1) / p.per_group;
+  p.cols = p.per_group * H <= 32 ? 32 : 64;
+  p.head_groups = p.per_group > 1 ? 1 : (H + p.cols - 1) / p.cols;
+  const long long slots = window + p.per_group - 1 + (dense ? cmp_cap : K);
+  p.splits = decode_splits((long long)b * p.groups * p.head_groups, (slots + 127) / 128,
+                           d <= 128 ? 3 : 1);
+  return p;
 }
 
 // Combines the splits of every (row, head): o and lse.
 cudaError_t launch_attn_decode_combine(const AttnDecodeArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_attn_decode_simt(const AttnDecodeArgs& a, bool bf16, int bits,
                                     cudaStream_t st);
+cudaError_t launch_attn_decode_tc(const AttnDecodeArgs& a, int bits, cudaStream_t st);
 
 }  // namespace csa

@@ -14,10 +14,12 @@ from typing import Optional, Tuple
 import torch
 
 from . import csa
-from .csa import CSAError, _dt, _need, _ptr  # noqa: F401  (CSAError: re-exported)
+from .csa import CSA_BF16, CSA_FP32, CSAError  # noqa: F401  (CSAError: re-exported)
 
 _c_int, _c_ll, _c_p, _c_f, _c_sz = (ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p,
                                     ctypes.c_float, ctypes.c_size_t)
+_DT = {torch.bfloat16: CSA_BF16, torch.float32: CSA_FP32}
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 SIGNATURES = {
     "csa_cache_page_bytes": (_c_sz, [_c_int] * 3),
@@ -32,6 +34,7 @@ SIGNATURES = {
 }
 
 _declared = None
+_page_bytes = {}
 
 
 def load_library():
@@ -47,74 +50,103 @@ def load_library():
     return lib
 
 
-def _same_device(first: torch.Tensor, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+# A decode step makes these calls for every layer and token, each with kernels
+# of a few microseconds: the checks below are written to cost little where
+# nothing is wrong (one condition a tensor; the message is made on failure).
+
+def _check(t, name, dtype, shape, dev):
+    """A contiguous CUDA tensor of this dtype and shape on device dev."""
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.get_device() == dev):
+        _refuse(t, name, dtype, shape, dev)
 
 
-def _call(name: str, t: torch.Tensor, stream, *args):
-    """Call an entry point with t's device current, on `stream` or on that device's current one."""
-    lib = load_library()
-    with torch.cuda.device(t.device):
-        s = stream if stream is not None else torch.cuda.current_stream(t.device)
-        csa._check(name, getattr(lib, name)(*args, s.cuda_stream))
-
-
-def _cache_args(cache, page_size, bits, d):
-    """Check the cache tensor [n_pages, page bytes] and return n_pages."""
-    _need(cache, "cache", dtype=torch.uint8)
-    want = csa_cache_page_bytes(page_size, d, bits)
-    if cache.dim() != 2 or cache.shape[1] != want:
-        raise ValueError(f"cache must be [n_pages, {want}] for pages of {page_size} rows of {d} "
-                         f"channels in {bits} bits, got {tuple(cache.shape)}")
-    return cache.shape[0]
-
-
-def _int_tensor(t, name, shape, optional=False):
-    if t is None and optional:
-        return
-    _need(t, name, dtype=torch.int32)
-    if tuple(t.shape) != tuple(shape):
+def _refuse(t, name, dtype, shape, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _table(t, name, b):
-    _need(t, name, dtype=torch.int32)
-    if t.dim() != 2 or t.shape[0] != b or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [{b}, P] with P >= 1, got {tuple(t.shape)}")
-    return t.shape[1]
+def _first(t, name, dims):
+    """The device index and dtype code of a call's main tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dt = _DT.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
+    if t.dim() != len(dims):
+        raise ValueError(f"{name} must be [{', '.join(dims)}]")
+    return t.get_device(), dt
+
+
+def _table(t, name, b, dev):
+    """P of a page table [b, P]."""
+    P = t.shape[1] if t.dim() == 2 else 0
+    _check(t, name, _I32, (b, max(P, 1)), dev)
+    return P
+
+
+def _pages(cache, page_size, bits, d, dev):
+    """n_pages of a cache tensor [n_pages, page bytes]."""
+    want = csa_cache_page_bytes(page_size, d, bits)
+    n = cache.shape[0] if cache.dim() == 2 else 0
+    _check(cache, "cache", _U8, (n, want), dev)
+    return n
 
 
 def _workspace(ws, nbytes, dev):
+    """Pointer and size of the workspace; the tensor is returned to be kept alive."""
     if ws is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    _need(ws, "workspace")
-    return ws
+        ws = torch.empty(max(nbytes, 16), dtype=_U8, device=f"cuda:{dev}")
+    elif not (ws.is_cuda and ws.is_contiguous() and ws.get_device() == dev):
+        _refuse(ws, "workspace", ws.dtype, ws.shape, dev)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _call(name, dev, stream, *args):
+    """Call an entry point with device dev current, on `stream` or on dev's current stream."""
+    fn = getattr(_declared or load_library(), name)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    code = fn(*args, s)
+    if code != 0:
+        raise CSAError(name, code)
 
 
 def csa_cache_page_bytes(page_size: int, d: int, bits: int) -> int:
     """Bytes of one page of `page_size` rows of d channels in 4 or 8 bits."""
-    n = int(load_library().csa_cache_page_bytes(int(page_size), int(d), int(bits)))
-    if n == 0:
-        raise ValueError(f"no cache format with pages of {page_size} rows, {d} channels and "
-                         f"{bits} bits (page_size % 16 == 0, d % 32 == 0, d <= 512, bits 4 or 8)")
+    key = (page_size, d, bits)
+    n = _page_bytes.get(key)
+    if n is None:
+        n = int(load_library().csa_cache_page_bytes(int(page_size), int(d), int(bits)))
+        if n == 0:
+            raise ValueError(f"no cache format with pages of {page_size} rows, {d} channels and "
+                             f"{bits} bits (page_size % 16 == 0, d % 32 == 0, d <= 512, bits 4 "
+                             "or 8)")
+        _page_bytes[key] = n
     return n
 
 
 def _rows_args(x, name, cache, table, pos0, page_size, bits, counts):
-    _need(x, name, contiguous=False)
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be [b, s, d]")
+    dev, dt = _first(x, name, ("b", "s", "d"))
     b, s, d = x.shape
-    if x.numel() and x.stride(2) != 1:
+    bs, rs, cs = x.stride()
+    if cs != 1 and b and s:
         raise ValueError(f"{name} rows must be contiguous")
-    n_pages = _cache_args(cache, page_size, bits, d)
-    P = _table(table, "table", b) if b else 1
-    _int_tensor(pos0, "pos0", (b,))
-    _int_tensor(counts, "counts", (b,), optional=True)
-    _same_device(x, cache=cache, table=table, pos0=pos0, counts=counts)
-    return b, s, d, P, n_pages
+    n_pages = _pages(cache, page_size, bits, d, dev)
+    P = _table(table, "table", b, dev)
+    _check(pos0, "pos0", _I32, (b,), dev)
+    if counts is not None:
+        _check(counts, "counts", _I32, (b,), dev)
+    return dev, dt, b, s, d, bs, rs, P, n_pages
 
 
 def csa_cache_write(x: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, pos0: torch.Tensor,
@@ -128,11 +160,11 @@ def csa_cache_write(x: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, p
     [b, P] int32 page ids, pos0 and counts [b] int32.  Positions run through
     the P * page_size slots as through a ring.  Returns cache.
     """
-    b, s, d, P, n_pages = _rows_args(x, "x", cache, table, pos0, page_size, bits, counts)
-    if b and s:
-        _call("csa_cache_write", x, stream, x.data_ptr(), x.stride(0), x.stride(1), _dt(x),
-              table.data_ptr(), pos0.data_ptr(), _ptr(counts), cache.data_ptr(), b, s, d, P,
-              n_pages, page_size, bits)
+    dev, dt, b, s, d, bs, rs, P, n_pages = _rows_args(x, "x", cache, table, pos0, page_size, bits,
+                                                      counts)
+    _call("csa_cache_write", dev, stream, x.data_ptr(), bs, rs, dt, table.data_ptr(),
+          pos0.data_ptr(), None if counts is None else counts.data_ptr(), cache.data_ptr(), b, s,
+          d, P, n_pages, page_size, bits)
     return cache
 
 
@@ -142,11 +174,11 @@ def csa_cache_read(cache: torch.Tensor, table: torch.Tensor, pos0: torch.Tensor,
     """Read the rows at positions pos0[s] .. pos0[s] + counts[s] - 1 into
     out [b, s, d] (bf16 or fp32, rows contiguous), exactly as the codes stand
     for them; rows past counts[s] are left as they were.  Returns out."""
-    b, s, d, P, n_pages = _rows_args(out, "out", cache, table, pos0, page_size, bits, counts)
-    if b and s:
-        _call("csa_cache_read", out, stream, cache.data_ptr(), table.data_ptr(), pos0.data_ptr(),
-              _ptr(counts), out.data_ptr(), out.stride(0), out.stride(1), _dt(out), b, s, d, P,
-              n_pages, page_size, bits)
+    dev, dt, b, s, d, bs, rs, P, n_pages = _rows_args(out, "out", cache, table, pos0, page_size,
+                                                      bits, counts)
+    _call("csa_cache_read", dev, stream, cache.data_ptr(), table.data_ptr(), pos0.data_ptr(),
+          None if counts is None else counts.data_ptr(), out.data_ptr(), bs, rs, dt, b, s, d, P,
+          n_pages, page_size, bits)
     return out
 
 
@@ -168,29 +200,25 @@ def csa_indexer_topk_decode(q_I: torch.Tensor, cache: torch.Tensor, table: torch
     pages (block j at position j).  Returns idx [b, s_q, topk] int32:
     ascending, -1 behind the min(topk, vis) blocks.
     """
-    _need(q_I, "q_I")
-    if q_I.dim() != 4:
-        raise ValueError("q_I must be [b, s_q, H_I, d_I]")
-    b, s_q, H, d = q_I.shape
-    n_pages = _cache_args(cache, page_size, bits, d)
-    P = _table(table, "table", b)
-    _need(w, "w", dtype=torch.float32)
-    if tuple(w.shape) != (b, s_q, H):
-        raise ValueError(f"w must be {(b, s_q, H)}, got {tuple(w.shape)}")
-    _int_tensor(seq_lens, "seq_lens", (b,))
+    dev, dt = _first(q_I, "q_I", ("b", "s_q", "H_I", "d_I"))
+    b, s_q, H, d = shape = q_I.shape
+    _check(q_I, "q_I", q_I.dtype, shape, dev)
+    n_pages = _pages(cache, page_size, bits, d, dev)
+    P = _table(table, "table", b, dev)
+    _check(w, "w", _F32, (b, s_q, H), dev)
+    _check(seq_lens, "seq_lens", _I32, (b,), dev)
+    if topk < 1:
+        raise ValueError("topk must be at least 1")
     if out_idx is None:
-        out_idx = torch.empty(b, s_q, max(topk, 0), dtype=torch.int32, device=q_I.device)
-    _int_tensor(out_idx, "out_idx", (b, s_q, topk))
-    if workspace is None:
-        nbytes = csa_indexer_topk_decode_workspace_size(b, s_q, H, d, P * page_size)
-        workspace = _workspace(None, nbytes, q_I.device)
-    _need(workspace, "workspace")
-    _same_device(q_I, cache=cache, table=table, w=w, seq_lens=seq_lens, out_idx=out_idx,
-                 workspace=workspace)
-    _call("csa_indexer_topk_decode", q_I, stream, q_I.data_ptr(), cache.data_ptr(),
+        out_idx = torch.empty((b, s_q, topk), dtype=_I32, device=q_I.device)
+    else:
+        _check(out_idx, "out_idx", _I32, (b, s_q, topk), dev)
+    nbytes = (csa_indexer_topk_decode_workspace_size(b, s_q, H, d, P * page_size)
+              if workspace is None else 0)
+    keep, ws, nbytes = _workspace(workspace, nbytes, dev)
+    _call("csa_indexer_topk_decode", dev, stream, q_I.data_ptr(), cache.data_ptr(),
           table.data_ptr(), w.data_ptr(), seq_lens.data_ptr(), out_idx.data_ptr(), b, s_q, H, d,
-          ratio, topk, P, n_pages, page_size, bits, _dt(q_I), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          ratio, topk, P, n_pages, page_size, bits, dt, ws, nbytes)
     return out_idx
 
 
@@ -214,43 +242,35 @@ def csa_attn_decode(q: torch.Tensor, cache: torch.Tensor, raw_table: torch.Tenso
     (None: every visible block), sink [H] fp32 or None, seq_lens [b] int32.
     Returns (O [b, s_q, H, d], lse [b, s_q, H] fp32).
     """
-    _need(q, "q")
-    if q.dim() != 4:
-        raise ValueError("q must be [b, s_q, H, d]")
-    b, s_q, H, d = q.shape
-    n_pages = _cache_args(cache, page_size, bits, d)
-    P_raw = _table(raw_table, "raw_table", b)
-    P_cmp = 0 if cmp_table is None else _table(cmp_table, "cmp_table", b)
+    dev, dt = _first(q, "q", ("b", "s_q", "H", "d"))
+    b, s_q, H, d = shape = q.shape
+    _check(q, "q", q.dtype, shape, dev)
+    n_pages = _pages(cache, page_size, bits, d, dev)
+    P_raw = _table(raw_table, "raw_table", b, dev)
+    P_cmp = 0 if cmp_table is None else _table(cmp_table, "cmp_table", b, dev)
     K = 0
     if idx is not None:
-        _need(idx, "idx", dtype=torch.int32)
-        if idx.dim() != 3 or tuple(idx.shape[:2]) != (b, s_q):
-            raise ValueError(f"idx must be [{b}, {s_q}, K], got {tuple(idx.shape)}")
-        K = idx.shape[2]
+        K = idx.shape[2] if idx.dim() == 3 else 0
+        _check(idx, "idx", _I32, (b, s_q, K), dev)
         if K == 0 or cmp_table is None:
             raise ValueError("idx needs at least one entry a row, and cmp_table")
     if sink is not None:
-        _need(sink, "sink", dtype=torch.float32)
-        if tuple(sink.shape) != (H,):
-            raise ValueError(f"sink must be [{H}]")
-    _int_tensor(seq_lens, "seq_lens", (b,))
+        _check(sink, "sink", _F32, (H,), dev)
+    _check(seq_lens, "seq_lens", _I32, (b,), dev)
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _check(out, "out", q.dtype, shape, dev)
     if lse is None:
-        lse = torch.empty(b, s_q, H, dtype=torch.float32, device=q.device)
-    _need(out, "out", dtype=q.dtype)
-    _need(lse, "lse", dtype=torch.float32)
-    if out.shape != q.shape or tuple(lse.shape) != (b, s_q, H):
-        raise ValueError("out must have q's shape and lse [b, s_q, H]")
-    if workspace is None:
-        nbytes = csa_attn_decode_workspace_size(b, s_q, H, d, window, K or P_cmp * page_size)
-        workspace = _workspace(None, nbytes, q.device)
-    _need(workspace, "workspace")
-    _same_device(q, cache=cache, raw_table=raw_table, cmp_table=cmp_table, idx=idx, sink=sink,
-                 seq_lens=seq_lens, out=out, lse=lse, workspace=workspace)
-    _call("csa_attn_decode", q, stream, q.data_ptr(), cache.data_ptr(), raw_table.data_ptr(),
-          _ptr(cmp_table), _ptr(idx), _ptr(sink), seq_lens.data_ptr(), float(scale),
-          out.data_ptr(), lse.data_ptr(), b, s_q, H, d, ratio, window, K, P_raw, P_cmp, n_pages,
-          page_size, bits, _dt(q), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+        lse = torch.empty((b, s_q, H), dtype=_F32, device=q.device)
+    else:
+        _check(lse, "lse", _F32, (b, s_q, H), dev)
+    nbytes = (csa_attn_decode_workspace_size(b, s_q, H, d, window, K or P_cmp * page_size)
+              if workspace is None else 0)
+    keep, ws, nbytes = _workspace(workspace, nbytes, dev)
+    _call("csa_attn_decode", dev, stream, q.data_ptr(), cache.data_ptr(), raw_table.data_ptr(),
+          None if cmp_table is None else cmp_table.data_ptr(),
+          None if idx is None else idx.data_ptr(), None if sink is None else sink.data_ptr(),
+          seq_lens.data_ptr(), scale, out.data_ptr(), lse.data_ptr(), b, s_q, H, d, ratio, window,
+          K, P_raw, P_cmp, n_pages, page_size, bits, dt, ws, nbytes)
     return out, lse
