@@ -15,12 +15,9 @@
 // The codes of a tile are fetched into registers while the tile before is in
 // the softmax, expanded to bf16 (exact: a code has at most four significant
 // bits) and stored once, 128-byte swizzled: read K-major the tile is the A
-// operand of S^T, read MN-major that of O^T.  A code's exponent and mantissa
-// bits, shifted under bf16's, are its value times 2^-126 (e2m1) or 2^-120
-// (e4m3); one product with the group's scale times that power makes them
-// right.  A shift places two codes of a 32-bit word at once, four (or two)
-// codes apart, so the channels of a row lie permuted within each eight: Q is
-// permuted alike, and O is put back where it is stored.
+// operand of S^T, read MN-major that of O^T.  The expansion leaves a row's
+// channels permuted within each eight (cache_expand.cuh): Q is permuted alike,
+// and O is put back where it is stored.
 //
 // What bounds it: at 64 heads x 512 the conversion of the codes (about three
 // instructions a value) and the tensor core are alike in cost; at 32 x 128 the
@@ -29,6 +26,7 @@
 // bf16, their sum and the running maximum in fp32, rescaling only when a
 // column's maximum grows by more than 2^8.
 #include "attn_decode.h"
+#include "cache_expand.cuh"
 #include "tcgen05.cuh"
 
 namespace csa {
@@ -89,42 +87,6 @@ __device__ __forceinline__ float lane_reduce16(float (&v)[16]) {
   return kMax ? fmaxf(v[0], other) : v[0] + other;
 }
 
-// The channel at position p of a row's permuted order (within eight).
-template <int BITS>
-__device__ __forceinline__ int channel_of(int p) {
-  return BITS == 4 ? (p & ~7) | ((p >> 1) & 3) | ((p & 1) << 2)
-                   : (p & ~3) | ((p >> 1) & 1) | ((p & 1) << 1);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Eight codes -> four words of two bf16, not yet scaled, in permuted order.
-__device__ __forceinline__ void expand8_e2m1(uint32_t w, uint32_t (&o)[4]) {
-  constexpr uint32_t S = 0x80008000u, M = 0x01C001C0u;
-  o[0] = ((w << 12) & S) | ((w << 6) & M);
-  o[1] = ((w << 8) & S) | ((w << 2) & M);
-  o[2] = ((w << 4) & S) | ((w >> 2) & M);
-  o[3] = (w & S) | ((w >> 6) & M);
-}
-__device__ __forceinline__ void expand8_e4m3(uint32_t w0, uint32_t w1, uint32_t (&o)[4]) {
-  constexpr uint32_t S = 0x80008000u, M = 0x07F007F0u;
-  o[0] = ((w0 << 8) & S) | ((w0 << 4) & M);
-  o[1] = (w0 & S) | ((w0 >> 4) & M);
-  o[2] = ((w1 << 8) & S) | ((w1 << 4) & M);
-  o[3] = (w1 & S) | ((w1 >> 4) & M);
-}
-
-// One scale group (32 channels) of a slot as fetched.
-template <int BITS>
-struct Codes {
-  uint4 w[BITS / 4];
-  uint32_t scale;
-};
-
 template <int D, int NC, int BITS>
 __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
     const AttnDecodeArgs a, int per_group, int groups, int head_groups) {
@@ -159,6 +121,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
   const DecodeRow last = decode_row(a, bi, i0 + nq - 1);
   const int wext = a.window + nq - 1;
   const int w0 = last.t - wext + 1;
+  const int ring = a.P_raw * a.cs.page_size;
+  const int ring0 = w0 >= 0 ? w0 % ring : ring - 1 - (int)((unsigned)(-1 - w0) % (unsigned)ring);
   const int slots = last.t < 0 ? 0 : wext + (a.idx != nullptr ? a.K : last.vis);
   const int tiles = (slots + kSlots - 1) / kSlots;
   const int it0 = (int)((long long)tiles * split / a.splits);
@@ -184,21 +148,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
     if (qi < nq && h < heads)
       v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
                                           ((row0 + qi) * a.H + h0 + h) * D + ch * 8);
-    // into the channel order of the expanded codes
-    uint4 p;
-    if constexpr (BITS == 4) {
-      p.x = __byte_perm(v.x, v.z, 0x5410);     // channels 0, 4
-      p.y = __byte_perm(v.x, v.z, 0x7632);     // 1, 5
-      p.z = __byte_perm(v.y, v.w, 0x5410);     // 2, 6
-      p.w = __byte_perm(v.y, v.w, 0x7632);     // 3, 7
-    } else {
-      p.x = __byte_perm(v.x, v.y, 0x5410);     // 0, 2
-      p.y = __byte_perm(v.x, v.y, 0x7632);     // 1, 3
-      p.z = __byte_perm(v.z, v.w, 0x5410);
-      p.w = __byte_perm(v.z, v.w, 0x7632);
-    }
     *reinterpret_cast<uint4*>(sm + C::Q + (ch >> 3) * C::kQBlk + c * 128 +
-                              (((ch & 7) ^ (c & 7)) << 4)) = p;
+                              (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(v);
   }
   fence_proxy_async_smem();
   fence_before();
@@ -275,10 +226,11 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
         if (it < n && cslot + k * C::kPass < kSlots && s < slots) {
           if (s < wext) {
             const int pos = w0 + s;
+            int slot = ring0 + s;                          // ring0 + s < 2 ring
+            slot -= slot >= ring ? ring : 0;
             if (pos >= 0)
-              ok = cache_row(a.cs, a.raw_table + (long long)bi * a.P_raw,
-                             (int)((unsigned)pos % (unsigned)(a.P_raw * a.cs.page_size)), &code,
-                             &scale, a.status);
+              ok = cache_row(a.cs, a.raw_table + (long long)bi * a.P_raw, slot, &code, &scale,
+                             a.status);
           } else {
             const int j = a.idx != nullptr ? a.idx[row0 * a.K + s - wext] : s - wext;
             if (j >= 0 && j < last.vis)
@@ -296,18 +248,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
 #pragma unroll
         for (int m = 0; m < C::kMT; ++m) {
           Codes<BITS>& c = cd[k * C::kMT + m];
-          c.scale = 0;
-#pragma unroll
-          for (int e = 0; e < BITS / 4; ++e) c.w[e] = make_uint4(0u, 0u, 0u, 0u);
-          if (scale_p[k] != nullptr) {
-            c.scale = __ldg(scale_p[k] + m * 4);
-            if constexpr (BITS == 4) {
-              c.w[0] = __ldg(reinterpret_cast<const uint4*>(code_p[k] + m * 64));
-            } else {
-              c.w[0] = __ldg(reinterpret_cast<const uint4*>(code_p[k] + m * 128));
-              c.w[1] = __ldg(reinterpret_cast<const uint4*>(code_p[k] + m * 128 + 16));
-            }
-          }
+          c.clear();
+          if (scale_p[k] != nullptr) c.load(code_p[k] + m * (16 * BITS), scale_p[k] + m * 4);
         }
     };
     // Expands the fetched codes of tile it into the KV buffer; M tile m's
@@ -327,30 +269,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
           const int s = cslot + k * C::kPass;
           if (s >= kSlots) continue;
           const Codes<BITS>& c = cd[k * C::kMT + m];
-          // exponent of scale * 2^126 (2^120): beyond bf16's largest it takes a second factor
-          constexpr int kUp = BITS == 4 ? 126 : 120;
-          const int e = (int)c.scale + kUp;                // biased by 127
-          const uint32_t f1 = (uint32_t)min(e, 254) * 0x00800080u;
-          const uint32_t blk = (uint32_t)(m * 2 + (cg >> 1)) * kKvBlk + s * 128;
-          const uint32_t words[8] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w,
-                                     c.w[BITS / 4 - 1].x, c.w[BITS / 4 - 1].y,
-                                     c.w[BITS / 4 - 1].z, c.w[BITS / 4 - 1].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {                    // eight channels each
-            uint32_t o[4];
-            if constexpr (BITS == 4) expand8_e2m1(words[j], o);
-            else expand8_e4m3(words[2 * j], words[2 * j + 1], o);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f1);
-            if (e > 254) {
-              const uint32_t f2 = (uint32_t)(e - 254 + 127) * 0x00800080u;
-#pragma unroll
-              for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f2);
-            }
-            const uint32_t ch = (cg & 1) * 4 + j;
-            *reinterpret_cast<uint4*>(sm + C::KV + blk + ((ch ^ (s & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          unsigned char* dst = sm + C::KV + (uint32_t)(m * 2 + (cg >> 1)) * kKvBlk + s * 128;
+          expand_group<BITS>(c, dst, (cg & 1) * 4, s & 7);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bar_kv[m]);

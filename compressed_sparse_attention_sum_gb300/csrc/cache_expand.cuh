@@ -1,0 +1,115 @@
+// Codes of the cache to bf16 tiles in shared memory, the operands of the
+// tensor-core kernels of the serving calls.
+//
+// A code's exponent and mantissa bits, moved under bf16's, are its value times
+// 2^-126 (e2m1) or 2^-120 (e4m3), subnormal codes included; one product with
+// the group's scale times that power makes it right, exactly (a code has at
+// most four significant bits).  A shift of a 32-bit word moves two codes at
+// once, four (e2m1) or two (e4m3) codes apart, so a row's channels come out
+// permuted within each eight: position p holds channel channel_of(p).  The
+// other operand of a product over channels is permuted alike (permute8).
+#pragma once
+
+#include "cache_format.cuh"
+
+namespace csa {
+
+template <int BITS>
+__device__ __forceinline__ int channel_of(int p) {
+  return BITS == 4 ? (p & ~7) | ((p >> 1) & 3) | ((p & 1) << 2)
+                   : (p & ~3) | ((p >> 1) & 1) | ((p & 1) << 1);
+}
+
+// Eight bf16 channels into the expanded codes' order.
+template <int BITS>
+__device__ __forceinline__ uint4 permute8(uint4 v) {
+  if constexpr (BITS == 4)
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                      __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+  else
+    return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                      __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One scale group (32 channels) of a row as fetched.
+template <int BITS>
+struct Codes {
+  uint4 w[BITS / 4];
+  uint32_t scale;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < BITS / 4; ++e) w[e] = make_uint4(0u, 0u, 0u, 0u);
+    scale = 0;
+  }
+  __device__ __forceinline__ void load(const uint8_t* code, const uint8_t* s) {
+#pragma unroll
+    for (int e = 0; e < BITS / 4; ++e) w[e] = __ldg(reinterpret_cast<const uint4*>(code) + e);
+    scale = __ldg(s);
+  }
+};
+
+// Eight codes -> four words of two bf16, not yet scaled, in permuted order.
+template <int BITS>
+__device__ __forceinline__ void expand8(uint32_t w0, uint32_t w1, uint32_t (&o)[4]) {
+  constexpr uint32_t S = 0x80008000u;
+  if constexpr (BITS == 4) {
+    constexpr uint32_t M = 0x01C001C0u;
+    o[0] = ((w0 << 12) & S) | ((w0 << 6) & M);
+    o[1] = ((w0 << 8) & S) | ((w0 << 2) & M);
+    o[2] = ((w0 << 4) & S) | ((w0 >> 2) & M);
+    o[3] = (w0 & S) | ((w0 >> 6) & M);
+  } else {
+    constexpr uint32_t M = 0x07F007F0u;
+    o[0] = ((w0 << 8) & S) | ((w0 << 4) & M);
+    o[1] = (w0 & S) | ((w0 >> 4) & M);
+    o[2] = ((w1 << 8) & S) | ((w1 << 4) & M);
+    o[3] = (w1 & S) | ((w1 >> 4) & M);
+  }
+}
+
+// A scale group -> four 16-byte chunks (ch0 .. ch0 + 3) of a row of 128 bytes
+// in the 128-byte swizzle (row & 7 = sw).  With NORM returns the sum of its
+// squares, added in bf16 (16 to an accumulator: within 4% below and above).
+template <int BITS, bool NORM = false>
+__device__ __forceinline__ float expand_group(const Codes<BITS>& c, unsigned char* row, int ch0,
+                                              int sw) {
+  __nv_bfloat162 sq = __floats2bfloat162_rn(0.f, 0.f);
+  // scale * 2^126 (2^120) as bf16 bits; where that is beyond bf16 (a scale
+  // above 2^1, 2^7) a second factor carries the rest
+  const int e = (int)c.scale + (BITS == 4 ? 126 : 120);
+  const uint32_t f1 = (uint32_t)min(e, 254) * 0x00800080u;
+  const uint32_t words[8] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w,
+                             c.w[BITS / 4 - 1].x, c.w[BITS / 4 - 1].y, c.w[BITS / 4 - 1].z,
+                             c.w[BITS / 4 - 1].w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t o[4];
+    if constexpr (BITS == 4) expand8<4>(words[j], 0u, o);
+    else expand8<8>(words[2 * j], words[2 * j + 1], o);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f1);
+    if (e > 254) {
+      const uint32_t f2 = (uint32_t)(e - 254 + 127) * 0x00800080u;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f2);
+    }
+    *reinterpret_cast<uint4*>(row + (((ch0 + j) ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+    if constexpr (NORM) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&o[x]);
+        sq = __hfma2(v, v, sq);
+      }
+    }
+  }
+  const float2 f = __bfloat1622float2(sq);
+  return f.x + f.y;
+}
+
+}  // namespace csa

@@ -22,37 +22,64 @@ constexpr int kCacheMinExp = -110;
 // sequence length, position or count outside its range.
 constexpr int kSiteCachePage = 0x71, kSiteCacheRange = 0x72;
 
+// Slots of a sequence (P * page_size) and rows of a page: below these, a
+// division by page_size is one multiplication, and all offsets within a page
+// fit 32 bits.
+constexpr long long kMaxSlots = 1ll << 24;
+constexpr int kMaxPageSize = 32768;
+
 struct CacheShape {
-  long long page_bytes;
-  long long scale_off;     // of a page's scale bytes
+  uint32_t page_bytes;
+  uint32_t scale_off;      // of a page's scale bytes
+  uint32_t code_row, scale_row;   // bytes of a row
   int page_size, n_pages;
-  int code_row, scale_row; // bytes of a row
+  uint32_t recip;          // ceil(2^31 / (page_size / 16))
 };
 
 inline CacheShape cache_shape(int page_size, int n_pages, int d, int bits) {
   CacheShape c;
   c.page_size = page_size;
   c.n_pages = n_pages;
-  c.code_row = d * bits / 8;
-  c.scale_row = d / kCacheGroup;
-  c.scale_off = (long long)page_size * c.code_row;
-  c.page_bytes = c.scale_off + (long long)page_size * c.scale_row;
+  c.code_row = (uint32_t)(d * bits / 8);
+  c.scale_row = (uint32_t)(d / kCacheGroup);
+  c.scale_off = (uint32_t)page_size * c.code_row;
+  c.page_bytes = c.scale_off + (uint32_t)page_size * c.scale_row;
+  const uint32_t g = (uint32_t)page_size / 16;
+  c.recip = (uint32_t)(((1ull << 31) + g - 1) / g);
   return c;
+}
+
+// slot / page_size for 0 <= slot < 2^24: with g = page_size / 16 < 2^11 + 1 and
+// n = slot / 16 < 2^20, recip exceeds 2^31 / g by less than 1, so n * recip /
+// 2^31 exceeds n / g by less than 2^20 / 2^31 <= 1 / g: the floor is the same.
+__device__ __forceinline__ int page_index(const CacheShape& c, int slot) {
+  return (int)__umulhi(((uint32_t)slot >> 4) << 1, c.recip);
+}
+
+// Byte offset of a page, and of a row's codes and scales in it.
+__device__ __forceinline__ long long page_base(const CacheShape& c, int page) {
+  return (long long)((unsigned long long)(uint32_t)page * c.page_bytes);
+}
+__device__ __forceinline__ uint32_t row_code(const CacheShape& c, int row) {
+  return (uint32_t)row * c.code_row;
+}
+__device__ __forceinline__ uint32_t row_scale(const CacheShape& c, int row) {
+  return c.scale_off + (uint32_t)row * c.scale_row;
 }
 
 // Byte offsets of the row in `slot` of a sequence whose page ids are `pages`;
 // false (and the status word set) when the page id is outside the cache.
 __device__ __forceinline__ bool cache_row(const CacheShape& c, const int32_t* pages, int slot,
                                           long long* code, long long* scale, int* status) {
-  const int pi = slot / c.page_size, row = slot - pi * c.page_size;
+  const int pi = page_index(c, slot), row = slot - pi * c.page_size;
   const int page = pages[pi];
   if ((unsigned)page >= (unsigned)c.n_pages) {
     set_status(status, kDevCheck, kSiteCachePage);
     return false;
   }
-  const long long base = (long long)page * c.page_bytes;
-  *code = base + (long long)row * c.code_row;
-  *scale = base + c.scale_off + (long long)row * c.scale_row;
+  const long long base = page_base(c, page);
+  *code = base + row_code(c, row);
+  *scale = base + row_scale(c, row);
   return true;
 }
 

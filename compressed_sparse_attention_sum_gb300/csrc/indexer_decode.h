@@ -23,7 +23,8 @@ struct IndexDecodeArgs {
   float* scores;       // [b * s_q][slots]
   double* exact;       // [b * s_q][slots]: exact scores of the row's close candidates
   int32_t* list;       // [b * s_q][slots]: their blocks, ascending
-  int32_t* tile_scale; // [b][tiles]: largest scale byte of a tile's keys
+  float* tile_norm;    // [b * s_q][tiles]: bound on |k_j| of a tile's keys
+  float err;           // bound of a score's error over sum_h |w_h| |q_h| times |k_j|
   int b, s_q, H, d, ratio, topk, P, slots, tiles;
   CacheShape cs;
   int* status;
@@ -55,12 +56,14 @@ inline size_t index_decode_layout(IndexDecodeArgs* a, unsigned char* ws) {
   a->exact = (double*)take(n * sizeof(double));
   a->scores = (float*)take(n * sizeof(float));
   a->list = (int32_t*)take(n * sizeof(int32_t));
-  a->tile_scale = (int32_t*)take((size_t)a->b * a->tiles * sizeof(int32_t));
+  a->tile_norm = (float*)take(rows * (size_t)a->tiles * sizeof(float));
   return at;
 }
 
 cudaError_t launch_index_scores_simt(const IndexDecodeArgs& a, bool bf16, int bits,
                                      cudaStream_t st);
+bool index_decode_tc_supported(int H, int d);
+cudaError_t launch_index_scores_tc(const IndexDecodeArgs& a, int bits, cudaStream_t st);
 cudaError_t launch_index_select(const IndexDecodeArgs& a, bool bf16, int bits, cudaStream_t st);
 
 }  // namespace csa

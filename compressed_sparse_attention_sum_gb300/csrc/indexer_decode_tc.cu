@@ -1,0 +1,249 @@
+// Indexer scores of csa_indexer_topk_decode on the 5th-generation tensor
+// cores (tcgen05 + TMEM): bf16 queries, d_I 64 or 128.
+//
+// One token meets thousands of keys, so the keys are M:
+//   S^T [keys, (query, head)] = K [128, d_I] . Q^T [cols, d_I]
+// A CTA keeps the Q of up to 128 columns of one sequence (all heads of one
+// query, or of several) in shared memory and walks every gridDim.x-th tile of
+// 128 keys.  The codes of the next tile are fetched into registers while the
+// present one is multiplied; a tile is expanded to bf16 once for all heads
+// (exactly, cache_expand.cuh).  A thread then owns a key: it reads its row of
+// S^T from TMEM and adds w_h ReLU(s) over the heads, and a warp stores 32
+// consecutive scores.
+//
+// What bounds it: expanding the codes and the weighted ReLU, both on the
+// integer and FMA pipes; four CTAs on an SM hide each other's latency.  The
+// tile's largest |k| goes to the select.
+#include "cache_expand.cuh"
+#include "indexer_decode.h"
+#include "tcgen05.cuh"
+
+namespace csa {
+namespace idt {
+
+using namespace csa::umma;
+
+constexpr int kThreads = 128;
+constexpr int kSiteIndex = 0x74;
+constexpr uint32_t kBlk = kIdxTile * 128;
+constexpr float kNormSlack = 1.05f;       // the squares are summed 16 at a time in bf16
+
+template <int D, int NC>
+struct Cfg {
+  static constexpr int kGroups = D / 32;                 // scale groups of a key
+  static constexpr int kKeys = 8 * (32 / (8 * kGroups)); // keys a warp expands at once
+  static constexpr int kPass = kKeys * (kThreads / 32);
+  static constexpr int kKpt = kIdxTile / kPass;          // keys of a thread
+  static constexpr uint32_t kQBlk = NC * 128;
+  static constexpr uint32_t K = (D / 64) * kQBlk;
+  static constexpr uint32_t W = K + (D / 64) * kBlk;     // [NC] head weights
+  static constexpr uint32_t BAR = W + NC * 4;
+  static constexpr uint32_t MISC = BAR + 8;              // TMEM slot, dead
+  static constexpr uint32_t BND = MISC + 8;              // [4]
+  static constexpr uint32_t kBytes = BND + 16;
+};
+
+template <int D, int NC, int BITS>
+__global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDecodeArgs a,
+                                                                   int per_group, int hpad) {
+  using C = Cfg<D, NC>;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* w_s = reinterpret_cast<float*>(sm + C::W);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::MISC);
+  volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
+  float* bnd = reinterpret_cast<float*>(sm + C::BND);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int bi = blockIdx.y, i0 = blockIdx.z * per_group;
+  const int nq = min(per_group, a.s_q - i0);
+  const long long row0 = (long long)bi * a.s_q + i0;
+  int most = 0;                                          // keys any query needs scores of
+  for (int i = 0; i < nq; ++i) {
+    const int v = index_vis(a, bi, i0 + i);
+    if (v > a.topk) most = max(most, v);
+  }
+  const int tiles = (most + kIdxTile - 1) / kIdxTile;
+  if ((int)blockIdx.x >= tiles) return;                  // CTA-uniform
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *dead = 0;
+  }
+  if (warp == 0) tmem_alloc(tmem_slot, NC);
+
+  const int32_t* pages = a.table + (long long)bi * a.P;
+  const int cg = (lane >> 3) % C::kGroups;
+  const int ckey = warp * C::kKeys + (lane / (8 * C::kGroups)) * 8 + (lane & 7);
+  // Page ids are read two tiles ahead and codes one, all of a step at once: a
+  // dependent read of global memory takes as long as a tile's arithmetic.
+  Codes<BITS> cd[C::kKpt];
+  int page[C::kKpt];
+  auto fetch_pages = [&](int tile) {
+#pragma unroll
+    for (int k = 0; k < C::kKpt; ++k) {
+      const int j = tile * kIdxTile + ckey + k * C::kPass;
+      page[k] = j < most ? __ldg(pages + page_index(a.cs, j)) : 0;
+    }
+  };
+  auto fetch_codes = [&](int tile) {
+#pragma unroll
+    for (int k = 0; k < C::kKpt; ++k) {
+      const int j = tile * kIdxTile + ckey + k * C::kPass;
+      cd[k].clear();
+      if (j >= most) continue;
+      if ((unsigned)page[k] < (unsigned)a.cs.n_pages) {
+        const int r = j - page_index(a.cs, j) * a.cs.page_size;
+        const uint8_t* base = a.cache + page_base(a.cs, page[k]);
+        cd[k].load(base + row_code(a.cs, r) + cg * (4 * BITS), base + row_scale(a.cs, r) + cg);
+      } else {
+        set_status(a.status, kDevCheck, kSiteCachePage);
+      }
+    }
+  };
+  // Q: column c is query c / hpad, head c % hpad; the others are zero
+  constexpr int kQChunks = NC * (D / 8) / kThreads;
+  uint4 qv[kQChunks];
+#pragma unroll
+  for (int x = 0; x < kQChunks; ++x) {
+    const int e = tid + x * kThreads, c = e / (D / 8), ch = e - c * (D / 8);
+    const int qi = c / hpad, h = c - qi * hpad;
+    qv[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (qi < nq && h < a.H)
+      qv[x] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                   ((row0 + qi) * a.H + h) * D + ch * 8));
+  }
+  fetch_pages(blockIdx.x);
+  fetch_codes(blockIdx.x);
+  fetch_pages(blockIdx.x + gridDim.x);
+#pragma unroll
+  for (int x = 0; x < kQChunks; ++x) {
+    const int e = tid + x * kThreads, c = e / (D / 8), ch = e - c * (D / 8);
+    *reinterpret_cast<uint4*>(sm + (ch >> 3) * C::kQBlk + c * 128 +
+                              (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(qv[x]);
+  }
+  for (int c = tid; c < NC; c += kThreads) {
+    const int qi = c / hpad, h = c - qi * hpad;
+    w_s[c] = qi < nq && h < a.H ? a.w[(row0 + qi) * a.H + h] : 0.f;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+
+  uint32_t parity = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    // ---- expand ----------------------------------------------------------------
+    float norm2 = 0.f;                                   // |k|^2, largest of this thread's keys
+#pragma unroll
+    for (int k = 0; k < C::kKpt; ++k) {
+      const int key = ckey + k * C::kPass;
+      float s = expand_group<BITS, true>(cd[k], sm + C::K + (cg >> 1) * kBlk + key * 128,
+                                         (cg & 1) * 4, key & 7);
+      // squares of groups below 2^-40 may underflow
+      if (cd[k].scale < 87u) s = fmaxf(s, 32.f * (BITS == 4 ? 36.f : 448.f * 448.f) * 0x1p-80f);
+#pragma unroll
+      for (int o = 8; o < 8 * C::kGroups; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      norm2 = fmaxf(norm2, s);
+    }
+    norm2 = warp_max(norm2);
+    if (lane == 0) bnd[warp] = norm2;
+    fence_proxy_async_smem();
+    fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      fence_after();
+      constexpr uint32_t idesc = idesc_bf16_f32_major(kIdxTile, NC, 0, 0);
+      const uint32_t ka = smem_addr(sm + C::K), qa = smem_addr(sm);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        mma_bf16_ss(tmem, sw128_desc(ka + (k >> 2) * kBlk + (k & 3) * 32),
+                    sw128_desc(qa + (k >> 2) * C::kQBlk + (k & 3) * 32), idesc, k > 0 ? 1u : 0u);
+      mma_commit(bar);
+    }
+    if (tid < nq)
+      a.tile_norm[(row0 + tid) * a.tiles + tile] =
+          sqrtf(fmaxf(fmaxf(bnd[0], bnd[1]), fmaxf(bnd[2], bnd[3]))) * kNormSlack;
+    if (tile + (int)gridDim.x < tiles) {
+      fetch_codes(tile + gridDim.x);
+      fetch_pages(tile + 2 * gridDim.x);
+    }
+    if (!mbar_wait(bar, parity)) *dead = 1;
+    parity ^= 1;
+    fence_after();
+    // ---- sum_h w_h ReLU(s_h) for this thread's key ------------------------------
+    const int j = tile * kIdxTile + tid;
+#pragma unroll 1
+    for (int q = 0; q < nq; ++q) {
+      float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
+#pragma unroll 1
+      for (int c0 = q * hpad; c0 < (q + 1) * hpad; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16_wait(tmem + lane_base + c0, v);
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          const float4 w4 = *reinterpret_cast<const float4*>(w_s + c0 + c);
+          t0 = fmaf(w4.x, fmaxf(__uint_as_float(v[c]), 0.f), t0);
+          t1 = fmaf(w4.y, fmaxf(__uint_as_float(v[c + 1]), 0.f), t1);
+          t2 = fmaf(w4.z, fmaxf(__uint_as_float(v[c + 2]), 0.f), t2);
+          t3 = fmaf(w4.w, fmaxf(__uint_as_float(v[c + 3]), 0.f), t3);
+        }
+      }
+      if (j < most && !*dead) a.scores[(row0 + q) * a.slots + j] = (t0 + t1) + (t2 + t3);
+    }
+    fence_before();
+    __syncthreads();                                     // K, S and bnd are free
+    if (*dead) break;
+  }
+  if (tid == 0 && *dead) set_status(a.status, kDevTimeout, kSiteIndex);
+  if (warp == 0) {
+    fence_after();
+    tmem_dealloc(tmem, NC);
+  }
+}
+
+template <int D, int NC, int BITS>
+cudaError_t launch(const IndexDecodeArgs& a, int per_group, int hpad, cudaStream_t st) {
+  using C = Cfg<D, NC>;
+  const size_t smem = 1024 + C::kBytes;
+  auto k = index_scores_tc_kernel<D, NC, BITS>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int groups = (a.s_q + per_group - 1) / per_group;
+  // CTAs of a sequence: over all sequences twice the four that fit an SM, as
+  // those of shorter sequences find no tile
+  long long g = (8ll * 152 + (long long)a.b * groups - 1) / ((long long)a.b * groups);
+  g = g > a.tiles ? a.tiles : g;
+  k<<<dim3((unsigned)g, a.b, groups), kThreads, smem, st>>>(a, per_group, hpad);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace idt
+
+bool index_decode_tc_supported(int H, int d) { return (d == 64 || d == 128) && H <= 128; }
+
+cudaError_t launch_index_scores_tc(const IndexDecodeArgs& a, int bits, cudaStream_t st) {
+  const int hpad = (a.H + 15) / 16 * 16;
+  // as many queries of a sequence as fit 128 columns share the expanded keys
+  int pg = 128 / hpad;
+  pg = pg > a.s_q ? a.s_q : pg;
+  const bool wide = pg * hpad > 64;
+#define CSA_IDX(D, NC)                                                                           \
+  return bits == 4 ? idt::launch<D, NC, 4>(a, pg, hpad, st) : idt::launch<D, NC, 8>(a, pg, hpad, st)
+  if (a.d == 64) {
+    if (wide) CSA_IDX(64, 128);
+    CSA_IDX(64, 64);
+  }
+  if (wide) CSA_IDX(128, 128);
+  CSA_IDX(128, 64);
+#undef CSA_IDX
+}
+
+}  // namespace csa

@@ -1,0 +1,675 @@
+// The exact top-k of csa_indexer_topk_decode from its fp32 scores.
+//
+// The set has to be that of the exact scores, so blocks whose score lies
+// within the possible error of the K-th largest, T, are scored again.  With
+// eps a bound on the error of every fp32 score of the row, a block above
+// T + 2 eps belongs to the exact top-k and one below T - 2 eps does not; those
+// between are close.  eps = err * sum_h |w_h| |q_h| * max |k_j|, with |k_j|
+// bounded by the keys' group scales and err by the roundings of the sums:
+//   CUDA cores: d_I products and H_I heads added one by one, each addition
+//     rounding by 2^-24 of the sum so far: (d_I + H_I + 16) 2^-24;
+//   tensor cores: d_I / 16 steps that add 16 products at once, each cutting
+//     off at most 2^-23 of the sum so far, and H_I / 4 heads one by one in each
+//     of four chains: (d_I / 8 + H_I / 4 + 8) 2^-24.  Measured at most 3.6
+//     2^-24 where that is 56 2^-24 (128 heads x 128 channels, all terms
+//     positive), 0.1 2^-24 on N(0, 1) inputs.
+// A close block's dot products are accumulated as pairs of fp32 (the rounding
+// error of every addition is itself summed, which leaves about 2^-40) and
+// added over the heads in fp64; the best fill the places that the blocks above
+// T + 2 eps leave, ties to the lower block.
+//
+// A cluster of up to eight CTAs takes a row, each a contiguous part of its
+// scores, kept in shared memory as ordered integers.  A histogram of 1024 bins
+// over the range of scores, whose counts the CTAs read from each other, gives
+// the bin that T lies in (where outliers leave more than 512 scores in it,
+// histograms over the bits of the keys, four rounds at most, narrow it down).
+// The keys of that bin and of 2 eps around it are gathered in every CTA; T and the close blocks follow from ranks among them.  The heads
+// of the close blocks' exact scores are dealt over the CTAs.  A row with more than 512 keys there (ties) is
+// finished by the first CTA alone, by radix selects over global lists.
+// Latency bounds it: cluster barriers, reads of the other CTAs' shared memory
+// (all of a step are in flight at once) and the chain of dependent additions of
+// a dot product (d_I / 4 long: four threads share a head).
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "indexer_decode.h"
+
+namespace csa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kSel = 512;            // threads of a CTA
+constexpr int kSelWarps = kSel / 32;
+constexpr int kBins = 2 * kSel;
+constexpr int kBinBits = 10;
+constexpr int kNarrow = 256;         // keys of the bin around T
+constexpr int kList = kSel;          // keys around T that are ranked directly: one a thread
+constexpr int kMaxCluster = 8;
+constexpr int kMaxStaged = 40960;    // scores a CTA keeps in shared memory
+
+// Unsigned keys in the order of the floats they come from (-0 as +0).
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ unsigned long long order_key(double x) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
+  return (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+
+struct __align__(16) SelShared {
+  // read by the other CTAs of the cluster
+  int hist[2][kBins];                // a round's counts; two, so that a round needs one barrier
+  uint32_t list_key[kList];
+  int list_j[kList];
+  float2 exact[kList];               // close blocks' exact scores over this CTA's heads
+  uint32_t range[2];                 // smallest and largest key of this part
+  int n[2];                          // keys in the list, keys above it
+  // this CTA's own
+  uint32_t all_key[kList];
+  int all_j[kList];
+  int close_j[kList];
+  unsigned long long all_exact[kList];
+  int warp_n[kSelWarps];
+  int warp_m[kSelWarps];
+  float part[kSelWarps];
+  float2 pair[kSelWarps];
+  int bin, above, in_bin;
+  uint32_t tkey;
+  int digit, radix_above;            // the lone CTA's radix select
+};
+
+template <int CS>
+__device__ __forceinline__ void cluster_sync() {
+  if constexpr (CS > 1) cg::this_cluster().sync();
+  else __syncthreads();
+}
+template <int CS, typename V>
+__device__ __forceinline__ const V* peer(V* p, int rank) {
+  if constexpr (CS > 1) return cg::this_cluster().map_shared_rank(p, rank);
+  else return p;
+}
+
+__device__ __forceinline__ int block_count(SelShared& sh, int c) {
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) sh.warp_n[threadIdx.x >> 5] = c;
+  __syncthreads();
+  int t = 0;
+  for (int k = 0; k < kSelWarps; ++k) t += sh.warp_n[k];
+  __syncthreads();
+  return t;
+}
+
+// Ordered compaction: emit(j, rank) for every j in [0, n) with pred(j), ranks
+// in ascending j.  Returns their number.  Warp v owns the v-th contiguous part.
+template <typename P, typename E>
+__device__ int compact(SelShared& sh, int n, P pred, E emit) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = ((n + kSel - 1) / kSel) * 32;
+  const int j0 = min(warp * part, n), j1 = min(j0 + part, n);
+  int c = 0;
+  for (int j = j0 + lane; j - lane < j1; j += 32)
+    c += __popc(__ballot_sync(0xffffffffu, j < j1 && pred(j)));
+  if (lane == 0) sh.warp_n[warp] = c;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int v = 0; v < kSelWarps; ++v) {
+    if (v < warp) before += sh.warp_n[v];
+    total += sh.warp_n[v];
+  }
+  for (int j = j0 + lane; j - lane < j1; j += 32) {
+    const bool p = j < j1 && pred(j);
+    const unsigned m = __ballot_sync(0xffffffffu, p);
+    if (p) emit(j, before + __popc(m & ((1u << lane) - 1u)));
+    before += __popc(m);
+  }
+  __syncthreads();
+  return total;
+}
+
+// Numbers held as an unevaluated sum hi + lo of two fp32, about 2^-46.
+__device__ __forceinline__ float2 pair_add(float2 a, float2 b) {
+  const float s = __fadd_rn(a.x, b.x), t = __fsub_rn(s, a.x);
+  const float e = __fadd_rn(__fsub_rn(a.x, __fsub_rn(s, t)), __fsub_rn(b.x, t));
+  const float lo = __fadd_rn(e, __fadd_rn(a.y, b.y)), hi = __fadd_rn(s, lo);
+  return make_float2(hi, __fsub_rn(lo, __fsub_rn(hi, s)));
+}
+__device__ __forceinline__ float2 pair_mul(float2 a, float w) {
+  const float p = __fmul_rn(a.x, w);
+  const float e = __fmaf_rn(a.y, w, __fmaf_rn(a.x, w, -p));
+  const float hi = __fadd_rn(p, e);
+  return make_float2(hi, __fsub_rn(e, __fsub_rn(hi, p)));
+}
+__device__ __forceinline__ float2 pair_shfl(float2 a, int o) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, a.x, o), __shfl_xor_sync(0xffffffffu, a.y, o));
+}
+__device__ __forceinline__ unsigned long long pair_key(float2 a) {
+  return order_key((double)a.x + (double)a.y);
+}
+
+// Part `part` of four of the dot product of q and k over d channels: a product
+// is split by an fma (exact already for bf16 q), a sum by the exact error of an
+// addition.
+template <typename T>
+__device__ __forceinline__ float2 dot_pair(const T* q, const float* k, int d, int part) {
+  float hi = 0.f, lo = 0.f;
+  const int c1 = (part + 1) * (d / 4);
+  for (int c0 = part * (d / 4); c0 < c1; c0 += 8) {
+    float qv[8];
+    load8(q + c0, qv);
+    const float4 k0 = *reinterpret_cast<const float4*>(k + c0);
+    const float4 k1 = *reinterpret_cast<const float4*>(k + c0 + 4);
+    const float kv[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = __fmul_rn(qv[e], kv[e]);
+      if (sizeof(T) == 4) lo += __fmaf_rn(qv[e], kv[e], -p);
+      const float s = __fadd_rn(hi, p), t = __fsub_rn(s, hi);
+      lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t));
+      hi = s;
+    }
+  }
+  return pair_add(make_float2(hi, 0.f), make_float2(lo, 0.f));
+}
+
+// Sums over the heads [h0, h0 + nh) of the exact scores of blocks block(0) ..
+// block(m - 1), each given to store(e, sum).  Four threads a (block, head);
+// scratch k_s holds the dequantised keys of a round (up to 16 of them).  Called
+// by the whole CTA.
+template <typename T, int BITS, typename B, typename S>
+__device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long row, int bi,
+                            float* k_s, int m, int h0, int nh, B block, S store) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* q = (const T*)a.q + (row * a.H + h0) * a.d;
+  const int32_t* pages = a.table + (long long)bi * a.P;
+  const int wpb = max(1, (nh + 7) / 8);                  // warps of a block
+  const int per = kSelWarps / wpb;
+  const int mine = warp / wpb, h = (warp - mine * wpb) * 8 + (lane >> 2), part = lane & 3;
+  const float w = h < nh ? a.w[row * a.H + h0 + h] : 0.f;
+  for (int e0 = 0; e0 < m; e0 += per) {
+    const int n = min(per, m - e0);
+    for (int x = tid; x < n * (a.d / 8); x += kSel) {
+      const int s = x / (a.d / 8), c0 = (x - s * (a.d / 8)) * 8;
+      long long code, scale;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (cache_row(a.cs, pages, block(e0 + s), &code, &scale, a.status))
+        cache_load8<BITS>(a.cache + code, scale_value(a.cache[scale + c0 / 32]), c0, v);
+      store8(k_s + s * a.d + c0, v);
+    }
+    __syncthreads();
+    if (mine < n) {                                      // warp-uniform
+      float2 x = make_float2(0.f, 0.f);
+      if (h < nh) x = dot_pair(q + h * a.d, k_s + mine * a.d, a.d, part);
+      x = pair_add(x, pair_shfl(x, 1));
+      x = pair_add(x, pair_shfl(x, 2));
+      x = x.x > 0.f ? pair_mul(x, w) : make_float2(0.f, 0.f);   // hi carries the sum's sign
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) x = pair_add(x, pair_shfl(x, o));
+      if (lane == 0) sh.pair[warp] = x;
+    }
+    __syncthreads();
+    if (tid < n) {
+      float2 x = sh.pair[tid * wpb];
+      for (int k = 1; k < wpb; ++k) x = pair_add(x, sh.pair[tid * wpb + k]);
+      store(e0 + tid, x);
+    }
+    __syncthreads();
+  }
+}
+
+// The k-th largest of the keys key(0) .. key(n - 1) (1 <= k <= n), and in
+// *equal how many keys equal to it belong to the k largest.  One CTA.
+template <typename F>
+__device__ unsigned long long radix_select(SelShared& sh, int n, int k, F key, int* equal) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned long long prefix = 0, mask = 0;
+  for (int shift = 56; shift >= 0; shift -= 8) {
+    for (int e = tid; e < 256; e += kSel) sh.hist[0][e] = 0;
+    __syncthreads();
+    for (int j = tid; j < n; j += kSel) {
+      const unsigned long long x = key(j);
+      if ((x & mask) == prefix) atomicAdd(&sh.hist[0][(int)(x >> shift) & 255], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int c[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        c[e] = sh.hist[0][255 - lane * 8 - e];
+        sum += c[e];
+      }
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      before -= sum;
+      if (before < k && before + sum >= k) {             // exactly one lane
+        int at = before;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (at < k && at + c[e] >= k) {
+            sh.digit = 255 - lane * 8 - e;
+            sh.radix_above = at;
+          }
+          at += c[e];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= (unsigned long long)sh.digit << shift;
+    mask |= 255ull << shift;
+    k -= sh.radix_above;
+    __syncthreads();
+  }
+  *equal = k;
+  return prefix;
+}
+
+// How many of all_key[0, m) are above x and equal to it (the entries up to the
+// next multiple of four are 0, below every key but -NaN's).
+__device__ __forceinline__ void count_keys(const SelShared& sh, int m, uint32_t x, int* above,
+                                           int* equal) {
+  int g = 0, q = 0;
+#pragma unroll 4
+  for (int e = 0; e < m; e += 4) {
+    const uint4 y = *reinterpret_cast<const uint4*>(sh.all_key + e);
+    g += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
+    q += (y.x == x) + (y.y == x) + (y.z == x) + (y.w == x);
+  }
+  *above = g;
+  *equal = q;
+}
+
+template <typename T, int BITS, int CS>
+__global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArgs a,
+                                                            int staged_cap) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ SelShared sh;
+  uint32_t* staged = reinterpret_cast<uint32_t*>(dyn);
+  float* k_s = reinterpret_cast<float*>(dyn + (size_t)staged_cap * 4);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
+  const long long row = blockIdx.x / CS;
+  const int bi = (int)(row / a.s_q), i = (int)(row - (long long)bi * a.s_q);
+  const int vis = index_vis(a, bi, i), K = a.topk;
+  int32_t* out = a.out + row * K;
+  if (vis <= K) {                                        // every block, whatever the scores
+    for (int k = rank * kSel + tid; k < K; k += CS * kSel) out[k] = k < vis ? k : -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+
+  // error of a score per unit of |k_j|, from the row's own q and w: eight lanes a head
+  const T* q = (const T*)a.q + row * a.H * a.d;
+  float aw = 0.f;
+  for (int h0 = warp * 4; h0 < a.H; h0 += kSelWarps * 4) {
+    const int h = h0 + (lane >> 3);
+    float n2 = 0.f;
+    if (h < a.H) {
+#pragma unroll 2
+      for (int c = (lane & 7) * 8; c < a.d; c += 64) {
+        float v[8];
+        load8(q + h * a.d + c, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n2 = fmaf(v[e], v[e], n2);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+    if (h < a.H && (lane & 7) == 0) aw += fabsf(a.w[row * a.H + h]) * sqrtf(n2);
+  }
+  aw = warp_sum(aw);
+  if (lane == 0) sh.part[warp] = aw;
+  for (int e = tid; e < kBins; e += kSel) sh.hist[0][e] = 0;
+  __syncthreads();
+  aw = 0.f;
+  for (int k = 0; k < kSelWarps; ++k) aw += sh.part[k];
+  __syncthreads();
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");     // the scores
+
+  const int seg = (vis + CS - 1) / CS;
+  const int j0 = min(rank * seg, vis), n = min(seg, vis - j0);
+  float* score = a.scores + row * a.slots;
+  const bool is_staged = seg <= staged_cap;              // the same in every CTA
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  const float* norms = a.tile_norm + row * a.tiles;
+  float kmax = tid * kIdxTile < vis ? norms[tid] : 0.f;  // in flight with the scores
+#pragma unroll 4
+  for (int j = tid; j < n; j += kSel) {
+    const uint32_t k = order_key(score[j0 + j]);
+    if (is_staged) staged[j] = k;
+    lo = min(lo, k);
+    hi = max(hi, k);
+  }
+  for (int t = tid + kSel; t * kIdxTile < vis; t += kSel) kmax = fmaxf(kmax, norms[t]);
+  kmax = warp_max(kmax);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    sh.part[warp] = kmax;
+    sh.warp_n[warp] = (int)lo;
+    sh.warp_m[warp] = (int)hi;
+  }
+  __syncthreads();
+  kmax = 0.f;
+  for (int k = 0; k < kSelWarps; ++k) {
+    kmax = fmaxf(kmax, sh.part[k]);
+    lo = min(lo, (uint32_t)sh.warp_n[k]);
+    hi = max(hi, (uint32_t)sh.warp_m[k]);
+  }
+  if (CS > 1) {
+    if (tid == 0) {
+      sh.range[0] = lo;
+      sh.range[1] = hi;
+    }
+    cluster_sync<CS>();
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      const uint32_t* p = peer<CS>(sh.range, r);
+      lo = min(lo, p[0]);
+      hi = max(hi, p[1]);
+    }
+  } else {
+    __syncthreads();
+  }
+  auto key = [&](int j) { return is_staged ? staged[j] : order_key(score[j0 + j]); };
+  const float eps2 = 2.f * a.err * aw * kmax;
+
+  // ---- narrow [lo, hi] to a bin that holds the k-th largest key ------------------
+  // Counts of the other CTAs' bins and this one's; returns the bin of the k-th
+  // largest (from the top), how many lie above it and in it.
+  int buf = 0;
+  auto find_bin = [&](int k) {
+    cluster_sync<CS>();
+    // bins from the top: thread t holds two of them, of all CTAs
+    const int b0 = kBins - 2 - 2 * tid;
+    int2 c = make_int2(0, 0), pc[CS];
+#pragma unroll
+    for (int r = 0; r < CS; ++r)
+      pc[r] = *reinterpret_cast<const int2*>(peer<CS>(sh.hist[buf], r) + b0);
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      c.x += pc[r].x;
+      c.y += pc[r].y;
+    }
+    // the other histogram was last read before this barrier
+    *reinterpret_cast<int2*>(sh.hist[buf ^ 1] + b0) = make_int2(0, 0);
+    const int sum = c.x + c.y;
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += v;
+    }
+    if (lane == 31) sh.warp_n[warp] = before;
+    __syncthreads();
+    for (int v = 0; v < warp; ++v) before += sh.warp_n[v];
+    before -= sum;
+    if (before < k && before + sum >= k) {               // exactly one thread
+      const bool second = before + c.y < k;
+      sh.bin = second ? b0 : b0 + 1;
+      sh.above = second ? before + c.y : before;
+      sh.in_bin = second ? c.x : c.y;
+    }
+    __syncthreads();
+    buf ^= 1;
+  };
+  // First by value, 1024 bins between the smallest and largest score.  The bin
+  // is then widened by what rounding may have moved a score across its edge.
+  const uint32_t lo0 = lo, hi0 = hi;
+  bool by_value = false;
+  if (vis > kNarrow && lo < hi) {
+    const float mn = order_value(lo), mx = order_value(hi), range = mx - mn;
+    const float inv = (float)kBins / range;
+    if (range < 3e38f && inv < 3e38f && inv > 0.f) {     // finite, not NaN
+      int* hist = sh.hist[buf];
+#pragma unroll 4
+      for (int j = tid; j < n; j += kSel)
+        atomicAdd(&hist[min((int)((order_value(key(j)) - mn) * inv), kBins - 1)], 1);
+      find_bin(K);
+      const float w = range / (float)kBins, slack = 0.01f * w + fmaxf(fabsf(mn), fabsf(mx)) * 0x1p-21f;
+      lo = max(lo0, order_key(mn + (float)sh.bin * w - slack));
+      hi = sh.bin == kBins - 1 ? hi0 : min(hi0, order_key(mn + (float)(sh.bin + 1) * w + slack));
+      by_value = true;
+    }
+  }
+  int k = K, in_range = vis;
+  int m = 0, above = 0, before_me = 0;
+  uint32_t list_hi = 0;
+  for (int limit = by_value ? vis : kNarrow;;) {
+    if (in_range > limit && lo < hi) {
+      const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);   // (hi - lo) >> shift < 1024
+      int* hist = sh.hist[buf];
+#pragma unroll 4
+      for (int j = tid; j < n; j += kSel) {
+        const uint32_t x = key(j);
+        if (x >= lo && x <= hi) atomicAdd(&hist[(x - lo) >> shift], 1);
+      }
+      find_bin(k);
+      k -= sh.above;
+      in_range = sh.in_bin;
+      lo += (uint32_t)sh.bin << shift;
+      hi = min(hi, lo + ((1u << shift) - 1u));
+      continue;
+    }
+    // ---- the keys of the bin and of 2 eps around it, in every CTA ---------------
+    const uint32_t list_lo = min(lo, order_key(order_value(lo) - eps2));
+    list_hi = max(hi, order_key(order_value(hi) + eps2));
+    if (tid == 0) sh.n[0] = 0;
+    __syncthreads();
+    int c = 0;
+#pragma unroll 4
+    for (int j = tid; j < n; j += kSel) {
+      const uint32_t x = key(j);
+      c += x > list_hi;
+      if (x >= list_lo && x <= list_hi) {
+        const int at = atomicAdd(&sh.n[0], 1);
+        if (at < kList) {
+          sh.list_key[at] = x;
+          sh.list_j[at] = j0 + j;
+        }
+      }
+    }
+    c = block_count(sh, c);
+    if (tid == 0) sh.n[1] = c;
+    cluster_sync<CS>();
+    int2 pn[CS];
+#pragma unroll
+    for (int r = 0; r < CS; ++r) pn[r] = *reinterpret_cast<const int2*>(peer<CS>(sh.n, r));
+    m = above = before_me = 0;
+    int at = 0, from = -1;                               // entry tid: of CTA `from`, its entry `at`
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      if (tid >= m && tid < m + pn[r].x) {
+        from = r;
+        at = tid - m;
+      }
+      m += pn[r].x;
+      above += pn[r].y;
+      if (r < rank) before_me += pn[r].y;
+    }
+    if (m <= kList) {
+      sh.all_key[tid] = from >= 0 ? peer<CS>(sh.list_key, max(from, 0))[at] : 0u;
+      sh.all_j[tid] = from >= 0 ? peer<CS>(sh.list_j, max(from, 0))[at] : -1;
+      __syncthreads();
+      break;
+    }
+    if (lo == hi) break;                                 // a row of ties
+    // too many: narrow by keys, from the whole range, and at last to one key
+    limit = by_value ? kNarrow : 0;
+    if (by_value) {
+      lo = lo0;
+      hi = hi0;
+    }
+    by_value = false;
+    cluster_sync<CS>();                                  // sh.n is read
+  }
+
+  if (m <= kList) {
+    // ---- T by rank, then the close blocks ----------------------------------------
+    const uint32_t x = sh.all_key[tid];
+    const int j = sh.all_j[tid];
+    int gt = 0, eq = 0;
+    if (tid < m) {
+      count_keys(sh, m, x, &gt, &eq);
+      if (above + gt < K && above + gt + eq >= K) sh.tkey = x;
+    }
+    __syncthreads();
+    const uint32_t tkey = sh.tkey;
+    const float tval = order_value(tkey);
+    const uint32_t clo = min(tkey, order_key(tval - eps2)), chi = max(tkey, order_key(tval + eps2));
+    const bool sure = tid < m && x > chi, close = tid < m && x >= clo && x <= chi;
+    const unsigned sm = __ballot_sync(0xffffffffu, sure), cm = __ballot_sync(0xffffffffu, close);
+    if (lane == 0) {
+      sh.warp_n[warp] = __popc(sm);
+      sh.warp_m[warp] = __popc(cm);
+    }
+    __syncthreads();
+    int need = K - above, mc = 0, place = 0;
+    for (int v = 0; v < kSelWarps; ++v) {
+      need -= sh.warp_n[v];
+      if (v < warp) place += sh.warp_m[v];
+      mc += sh.warp_m[v];
+    }
+    place += __popc(cm & ((1u << lane) - 1u));
+    if (close) sh.close_j[place] = j;
+    __syncthreads();
+    bool in = sure;
+    if (need < mc && eps2 > 0.f) {
+      // every CTA scores all close blocks over its share of the heads
+      const int share = (a.H + CS - 1) / CS, h0 = min(rank * share, a.H);
+      score_exact<T, BITS>(sh, a, row, bi, k_s, mc, h0, min(share, a.H - h0),
+                           [&](int e) { return sh.close_j[e]; },
+                           [&](int e, float2 v) { sh.exact[e] = v; });
+      cluster_sync<CS>();
+      if (tid < mc) {
+        float2 v[CS];
+#pragma unroll
+        for (int r = 0; r < CS; ++r) v[r] = peer<CS>(sh.exact, r)[tid];
+#pragma unroll
+        for (int r = 1; r < CS; ++r) v[0] = pair_add(v[0], v[r]);
+        sh.all_exact[tid] = pair_key(v[0]);
+      }
+    } else {
+      // all of them, or blocks whose scores are exactly equal
+      if (tid < mc) sh.all_exact[tid] = 0;
+    }
+    __syncthreads();
+    if (close) {
+      const unsigned long long v = sh.all_exact[place];
+      int better = 0;
+      for (int e = 0; e < mc; ++e) {
+        const unsigned long long y = sh.all_exact[e];
+        better += y > v || (y == v && sh.close_j[e] < j);
+      }
+      in = better < need;
+    }
+    // this CTA's place: behind the chosen blocks of the parts before it
+    before_me += block_count(sh, in && j < j0 ? 1 : 0);
+    // the list's blocks of this part: chosen ones as the largest key, the others as the smallest
+    if (tid < m && j >= j0 && j < j0 + n) {
+      if (is_staged) staged[j - j0] = in ? 0xffffffffu : 0u;
+      else score[j] = in ? INFINITY : -INFINITY;
+    }
+    if (list_hi == 0xffffffffu) list_hi = 0xfffffffeu;
+    __syncthreads();
+    compact(sh, n, [&](int y) { return key(y) > list_hi; },
+            [&](int y, int pos) { if (before_me + pos < K) out[before_me + pos] = j0 + y; });
+    cluster_sync<CS>();                                  // no CTA leaves while another reads it
+    return;
+  }
+  cluster_sync<CS>();
+  if (rank != 0) return;
+
+  // ---- a row of ties (T = lo = hi): one CTA, lists in global memory --------------
+  const int need = K - above;
+  const uint32_t list_lo = min(lo, order_key(order_value(lo) - eps2));
+  int32_t* list = a.list + row * a.slots;
+  compact(sh, vis,
+          [&](int j) {
+            const uint32_t x = order_key(score[j]);
+            return x >= list_lo && x <= list_hi;
+          },
+          [&](int j, int at) { list[at] = j; });
+  if (need < m && eps2 > 0.f) {
+    double* ex = a.exact + row * a.slots;
+    score_exact<T, BITS>(sh, a, row, bi, k_s, m, 0, a.H, [&](int e) { return list[e]; },
+                         [&](int e, float2 v) { ex[e] = (double)v.x + (double)v.y; });
+    int eq = 0;
+    const unsigned long long bar =
+        radix_select(sh, m, need, [&](int e) { return order_key(ex[e]); }, &eq);
+    compact(sh, m, [&](int e) { return order_key(ex[e]) == bar; },
+            [&](int e, int at) { score[list[e]] = at < eq ? INFINITY : -INFINITY; });
+    for (int e = tid; e < m; e += kSel) {
+      const unsigned long long x = order_key(ex[e]);
+      if (x != bar) score[list[e]] = x > bar ? INFINITY : -INFINITY;
+    }
+  } else {
+    for (int e = tid; e < m; e += kSel) score[list[e]] = e < need ? INFINITY : -INFINITY;
+  }
+  __syncthreads();
+  const uint32_t top = min(list_hi, order_key(INFINITY) - 1);
+  compact(sh, vis, [&](int j) { return order_key(score[j]) > top; },
+          [&](int j, int at) { if (at < K) out[at] = j; });
+}
+
+template <typename T, int BITS, int CS>
+cudaError_t launch_select_cs(const IndexDecodeArgs& a, cudaStream_t st) {
+  int cap = ((a.slots + CS - 1) / CS + 3) / 4 * 4;
+  cap = cap < kMaxStaged ? cap : kMaxStaged;
+  const size_t smem = (size_t)cap * 4 + (size_t)kSelWarps * a.d * sizeof(float);
+  auto k = index_select_kernel<T, BITS, CS>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.b * a.s_q * CS));
+  cfg.blockDim = dim3(kSel);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)CS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CS > 1 ? 2 : 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&cfg, k, a, cap);
+}
+
+// CTAs of a row: one for every 256 slots, up to eight, as long as the rows
+// together leave SMs for them.
+template <typename T, int BITS>
+cudaError_t launch_select(const IndexDecodeArgs& a, cudaStream_t st) {
+  const long long rows = (long long)a.b * a.s_q;
+  int cs = 1;
+  while (cs < kMaxCluster && a.slots > cs * 256 && rows * cs * 2 <= 152) cs *= 2;
+  switch (cs) {
+    case 1: return launch_select_cs<T, BITS, 1>(a, st);
+    case 2: return launch_select_cs<T, BITS, 2>(a, st);
+    case 4: return launch_select_cs<T, BITS, 4>(a, st);
+    default: return launch_select_cs<T, BITS, 8>(a, st);
+  }
+}
+
+}  // namespace
+
+// Launched as a programmatic dependent of the score kernel: its CTAs compute
+// the rows' error scale, and write the rows that take every block, beside it.
+cudaError_t launch_index_select(const IndexDecodeArgs& a, bool bf16, int bits, cudaStream_t st) {
+  if (bf16)
+    return bits == 4 ? launch_select<__nv_bfloat16, 4>(a, st) : launch_select<__nv_bfloat16, 8>(a, st);
+  return bits == 4 ? launch_select<float, 4>(a, st) : launch_select<float, 8>(a, st);
+}
+
+}  // namespace csa

@@ -24,11 +24,10 @@ cudaError_t launch_cache_read(const void* cache, const int32_t* table, const int
 namespace {
 
 using csa::aligned16;
+using csa::kMaxSlots;
 
-constexpr int kMaxPage = 65536;
 constexpr int kMaxDecodeH = 128;
 constexpr int kMaxRows = 65535;           // queries of one call
-constexpr long long kMaxSlots = 1ll << 24;   // index entries or blocks of one query
 
 csa_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 
@@ -36,7 +35,7 @@ bool valid_dtype(csa_dtype_t dt) { return dt == CSA_FP32 || dt == CSA_BF16; }
 
 bool valid_format(int page_size, int d, int bits) {
   return (bits == 4 || bits == 8) && page_size >= 16 && page_size % 16 == 0 &&
-         page_size <= kMaxPage && d >= 32 && d <= 512 && d % 32 == 0;
+         page_size <= csa::kMaxPageSize && d >= 32 && d <= 512 && d % 32 == 0;
 }
 
 // P pages of page_size rows: slots are counted in 31 bits.
@@ -63,7 +62,7 @@ csa_status_t check_cache_rows(const void* x, long long bs, long long rs, csa_dty
     return CSA_ERR_INVALID_ARG;
   if (!aligned16(cache) || !valid_rows(x, bs, rs, dt, d, s, b)) return CSA_ERR_INVALID_ARG;
   if (n_pages < 1 || !valid_table(P, page_size)) return CSA_ERR_INVALID_ARG;
-  if (b > kMaxRows) return CSA_ERR_UNSUPPORTED;
+  if (b > kMaxRows || (long long)P * page_size > kMaxSlots) return CSA_ERR_UNSUPPORTED;
   return CSA_OK;
 }
 
@@ -166,7 +165,11 @@ csa_status_t csa_indexer_topk_decode(const void* q_I, const void* cache, const i
     return CSA_ERR_WORKSPACE;
   a.status = csa::device_status_word();
   const cudaStream_t s = (cudaStream_t)stream;
-  const cudaError_t e = csa::launch_index_scores_simt(a, dt == CSA_BF16, bits, s);
+  const bool tc = dt == CSA_BF16 && csa::index_decode_tc_supported(H_I, d_I);
+  // see indexer_select.cu: fp32 sums on the tensor cores and on CUDA cores
+  a.err = (tc ? (float)(d_I / 8 + H_I / 4 + 8) : (float)(d_I + H_I + 16)) * 0x1p-24f;
+  const cudaError_t e = tc ? csa::launch_index_scores_tc(a, bits, s)
+                           : csa::launch_index_scores_simt(a, dt == CSA_BF16, bits, s);
   if (e != cudaSuccess) return CSA_ERR_CUDA;
   return from_cuda(csa::launch_index_select(a, dt == CSA_BF16, bits, s));
 }
@@ -210,8 +213,8 @@ csa_status_t csa_attn_decode(const void* q, const void* cache, const int32_t* ra
   if ((long long)P_raw * page_size < (long long)window + s_q - 1) return CSA_ERR_INVALID_ARG;
   if (!(scale == scale)) return CSA_ERR_INVALID_ARG;
   const long long cmp_rows = K > 0 ? K : (long long)P_cmp * page_size;
-  if (H > kMaxDecodeH || (long long)b * s_q > kMaxRows || window > kMaxSlots ||
-      cmp_rows > kMaxSlots)
+  if (H > kMaxDecodeH || (long long)b * s_q > kMaxRows || K > kMaxSlots ||
+      (long long)P_raw * page_size > kMaxSlots || (long long)P_cmp * page_size > kMaxSlots)
     return CSA_ERR_UNSUPPORTED;
   csa::AttnDecodeArgs a{};
   a.q = q;

@@ -42,7 +42,8 @@
  * clamped and recorded (site 0x72).
  *
  * Limits: 32 <= d <= 512 and d % 32 == 0; page_size a multiple of 16, at most
- * 65536; bits 4 or 8; positions below 2^31.  NaN and infinite inputs give
+ * 32768; bits 4 or 8; P * page_size at most 2^24 (UNSUPPORTED above);
+ * positions below 2^31.  NaN and infinite inputs give
  * unspecified values in their own rows.
  */
 #ifndef CSA_SERVE_H_
