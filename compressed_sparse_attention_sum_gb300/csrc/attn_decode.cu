@@ -1,5 +1,5 @@
 // csa_attn_decode on CUDA cores, for any head count and width, and the
-// kernel that joins the splits of a query.
+// kernel that joins the parts of a query.
 //
 // A CTA takes one (query, group of 8 heads, split of the query's slots).  Tile
 // by tile, the slots' rows are dequantised into shared memory as fp32 (one
@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_decode.h"
+#include "tcgen05.cuh"
 
 namespace csa {
 namespace {
@@ -20,6 +21,7 @@ constexpr int kTile = 32;            // slots of a shared-memory tile
 
 template <typename T, int BITS, int ND>   // ND = 32-channel groups held per warp (d <= 32 ND)
 __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(const AttnDecodeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(16) float kv_s[];   // [kTile][d]
   __shared__ long long s_code[kTile], s_scale[kTile];
   __shared__ int s_ok[kTile];
@@ -31,8 +33,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(const AttnDe
   const bool has_head = h < a.H;
   const DecodeRow r = decode_row(a, bi, i);
   const int tiles = (r.slots + kDecodeTile - 1) / kDecodeTile;
-  const int s_begin = (int)((long long)tiles * split / a.splits) * kDecodeTile;
-  const int s_end = min((int)((long long)tiles * (split + 1) / a.splits) * kDecodeTile, r.slots);
+  const int s_begin = (int)((long long)tiles * split / a.parts) * kDecodeTile;
+  const int s_end = min((int)((long long)tiles * (split + 1) / a.parts) * kDecodeTile, r.slots);
 
   float qv[ND], acc[ND];
 #pragma unroll
@@ -83,8 +85,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(const AttnDe
     }
   }
   if (!has_head) return;
-  if (a.splits > 1) {
-    const long long at = (row * a.splits + split) * a.H + h;
+  if (a.parts > 1) {
+    const long long at = (row * a.parts + split) * a.H + h;
 #pragma unroll
     for (int k = 0; k < ND; ++k)
       if (k < ng) a.part_o[at * d + k * 32 + lane] = acc[k];
@@ -105,8 +107,9 @@ __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(const AttnDe
   if (lane == 0) a.lse[row * a.H + h] = out_l;
 }
 
-// One warp per (row, head): the splits' (m, l) give each split's weight, then
-// the lanes add the splits' O over the channels.
+// One warp per (row, head): the parts' (m, l) give each part's weight, then the
+// lanes add the parts' O, four channels each.  Launched as a programmatic
+// dependent of the kernel that writes the parts.
 template <typename T>
 __global__ void __launch_bounds__(128) attn_decode_combine_kernel(const AttnDecodeArgs a) {
   const int lane = threadIdx.x & 31;
@@ -114,46 +117,56 @@ __global__ void __launch_bounds__(128) attn_decode_combine_kernel(const AttnDeco
   if (rh >= (long long)a.b * a.s_q * a.H) return;
   const long long row = rh / a.H;
   const int h = (int)(rh - row * a.H);
-  const float2* ml = a.part_ml + row * a.splits * a.H + h;
   const float sink2 = a.sink != nullptr ? a.sink[h] * kLog2e : -INFINITY;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float2* ml = a.part_ml + row * a.parts * a.H + h;
   float m = sink2;
-  for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, ml[(long long)s * a.H].x);
+  for (int s = lane; s < a.parts; s += 32) m = fmaxf(m, ml[(long long)s * a.H].x);
   m = warp_max(m);
   float total = 0.f;
-  if (m > -INFINITY) {
-    for (int s = lane; s < a.splits; s += 32) {
-      const float2 v = ml[(long long)s * a.H];
-      total = fmaf(v.y, exp2f(v.x - m), total);
-    }
+  for (int s = lane; s < a.parts; s += 32) {
+    const float2 v = ml[(long long)s * a.H];
+    if (v.y > 0.f) total = fmaf(v.y, exp2f(v.x - m), total);
   }
   total = warp_sum(total);
-  if (m > -INFINITY) total += exp2f(sink2 - m);
+  if (sink2 > -INFINITY) total += exp2f(sink2 - m);
   const float inv = total > 0.f ? 1.f / total : 0.f;
   for (int c = lane * 4; c < a.d; c += 128) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < a.splits; ++s) {
-      const float2 v = ml[(long long)s * a.H];
-      if (v.y == 0.f) continue;          // an empty split: its O is not read
-      const float f = exp2f(v.x - m) * inv;
-      const float4 o = *reinterpret_cast<const float4*>(
-          a.part_o + ((row * a.splits + s) * a.H + h) * a.d + c);
-      acc.x = fmaf(f, o.x, acc.x);
-      acc.y = fmaf(f, o.y, acc.y);
-      acc.z = fmaf(f, o.z, acc.z);
-      acc.w = fmaf(f, o.w, acc.w);
+    for (int s0 = 0; s0 < a.parts; s0 += 4) {            // four parts' reads in flight
+      float f[4];
+      float4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int s = min(s0 + k, a.parts - 1);
+        const float2 v = ml[(long long)s * a.H];
+        f[k] = s0 + k < a.parts && v.y > 0.f ? exp2f(v.x - m) * inv : 0.f;
+        o[k] = *reinterpret_cast<const float4*>(a.part_o + ((row * a.parts + s) * a.H + h) * a.d + c);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (f[k] > 0.f) {                                // an empty part's O was never written
+          acc.x = fmaf(f[k], o[k].x, acc.x);
+          acc.y = fmaf(f[k], o[k].y, acc.y);
+          acc.z = fmaf(f[k], o[k].z, acc.z);
+          acc.w = fmaf(f[k], o[k].w, acc.w);
+        }
+      }
     }
     T* dst = (T*)a.o + (row * a.H + h) * a.d + c;
-    dst[0] = from_f<T>(acc.x);
-    dst[1] = from_f<T>(acc.y);
-    dst[2] = from_f<T>(acc.z);
-    dst[3] = from_f<T>(acc.w);
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(umma::pack_bf16x2(acc.x, acc.y),
+                                                  umma::pack_bf16x2(acc.z, acc.w));
+    } else {
+      *reinterpret_cast<float4*>(dst) = acc;
+    }
   }
   if (lane == 0) a.lse[rh] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
 }
 
 template <typename T, int BITS>
 cudaError_t launch_simt(const AttnDecodeArgs& a, cudaStream_t st) {
-  const dim3 grid((unsigned)(a.b * a.s_q), a.splits, (a.H + kWarps - 1) / kWarps);
+  const dim3 grid((unsigned)(a.b * a.s_q), a.parts, (a.H + kWarps - 1) / kWarps);
   const size_t smem = (size_t)kTile * a.d * sizeof(float);
 #define CSA_DEC(ND)                                                                              \
   do {                                                                                           \
@@ -176,11 +189,18 @@ cudaError_t launch_simt(const AttnDecodeArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_decode_combine(const AttnDecodeArgs& a, bool bf16, cudaStream_t st) {
   const long long rh = (long long)a.b * a.s_q * a.H;
-  const unsigned grid = (unsigned)((rh + 3) / 4);
-  if (bf16) attn_decode_combine_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
-  else attn_decode_combine_kernel<float><<<grid, 128, 0, st>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rh + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   count_launches(1);
-  return cudaGetLastError();
+  return bf16 ? cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel<__nv_bfloat16>, a)
+              : cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel<float>, a);
 }
 
 cudaError_t launch_attn_decode_simt(const AttnDecodeArgs& a, bool bf16, int bits,
@@ -189,7 +209,7 @@ cudaError_t launch_attn_decode_simt(const AttnDecodeArgs& a, bool bf16, int bits
                                           : launch_simt<__nv_bfloat16, 8>(a, st))
                              : (bits == 4 ? launch_simt<float, 4>(a, st)
                                           : launch_simt<float, 8>(a, st));
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || a.parts == 1) return e;
   return launch_attn_decode_combine(a, bf16, st);
 }
 

@@ -23,9 +23,10 @@ struct AttnDecodeArgs {
   float scale;
   void* o;
   float* lse;
-  float* part_o;       // [b * s_q][splits][H][d], not normalized (splits > 1)
-  float2* part_ml;     // [b * s_q][splits][H]: running maximum (log2 units), sum
-  int b, s_q, H, d, ratio, window, K, P_raw, P_cmp, splits;
+  float* part_o;       // [b * s_q][parts][H][d], not normalized (parts > 1)
+  float2* part_ml;     // [b * s_q][parts][H]: running maximum (log2 units), sum
+  int b, s_q, H, d, ratio, window, K, P_raw, P_cmp;
+  int parts;           // partial results of a query
   CacheShape cs;
   int* status;
 };
@@ -77,31 +78,31 @@ __device__ __forceinline__ bool decode_slot(const AttnDecodeArgs& a, const Decod
 }
 
 // How a call is cut into CTAs: queries of one sequence that share a CTA (and
-// their groups), head groups, and splits of the slots.
+// their groups), head groups, CTAs of a cluster that join a part of the slots
+// among themselves, and parts, which a second kernel joins.
 struct DecodePlan {
-  int cols, per_group, groups, head_groups, splits;
+  int cols, per_group, groups, head_groups, cluster, parts;
 };
 
-// Splits for `ctas` CTAs over `tiles` tiles each: as many as fit the GPU
-// `resident` times over, at most one per tile.
-inline int decode_splits(long long ctas, long long tiles, int resident) {
-  long long s = (long long)resident * kDecodeSms / ctas;
-  if (s > tiles) s = tiles;
-  return s < 1 ? 1 : (int)s;
-}
-
 inline DecodePlan decode_plan_simt(int b, int s_q, int H, int window, long long cmp_rows) {
-  DecodePlan p{8, 1, s_q, (H + 7) / 8, 1};
-  p.splits = decode_splits((long long)b * s_q * p.head_groups,
-                           (window + cmp_rows + kDecodeTile - 1) / kDecodeTile, 2);
+  DecodePlan p{8, 1, s_q, (H + 7) / 8, 1, 1};
+  // enough CTAs to fill the GPU twice over, at most one per tile
+  const long long tiles = (window + cmp_rows + kDecodeTile - 1) / kDecodeTile;
+  long long n = 2ll * kDecodeSms / ((long long)b * s_q * p.head_groups);
+  n = n > tiles ? tiles : n;
+  p.parts = n < 1 ? 1 : (int)n;
   return p;
 }
 
 inline bool decode_tc_width(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
 
+// CTAs of the tensor-core kernel that fit an SM (registers: 9 or 17 warps).
+constexpr int decode_tc_resident(int d, int cols) { return d <= 128 && cols == 32 ? 2 : 1; }
+
 // Without an index list the queries of a sequence see the same rows (all but
-// the newest), so as many of them as fit 64 columns share a CTA.  Narrow
-// widths leave room for three CTAs on an SM, 512 for one.
+// the newest), so as many of them as fit 64 columns share a CTA.  The slots go
+// to one CTA per tile of 128 as long as the GPU holds them at once: up to eight
+// in a cluster, more in several clusters.
 inline DecodePlan decode_plan_tc(int b, int s_q, int H, int d, int window, int K, bool dense,
                                  long long cmp_cap) {
   DecodePlan p{};
@@ -111,15 +112,20 @@ inline DecodePlan decode_plan_tc(int b, int s_q, int H, int d, int window, int K
   p.cols = p.per_group * H <= 32 ? 32 : 64;
   p.head_groups = p.per_group > 1 ? 1 : (H + p.cols - 1) / p.cols;
   const long long slots = window + p.per_group - 1 + (dense ? cmp_cap : K);
-  p.splits = decode_splits((long long)b * p.groups * p.head_groups, (slots + 127) / 128,
-                           d <= 128 ? 3 : 1);
+  const long long tiles = (slots + 127) / 128;
+  long long n = (long long)decode_tc_resident(d, p.cols) * kDecodeSms / ((long long)b * p.groups * p.head_groups);
+  n = n > tiles ? tiles : n;
+  p.cluster = 1;
+  while (p.cluster < 8 && p.cluster < n) p.cluster *= 2;
+  p.parts = n < 16 ? 1 : (int)(n / 8);
   return p;
 }
 
-// Combines the splits of every (row, head): o and lse.
+// Combines the parts of every (row, head): o and lse.
 cudaError_t launch_attn_decode_combine(const AttnDecodeArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_attn_decode_simt(const AttnDecodeArgs& a, bool bf16, int bits,
                                     cudaStream_t st);
-cudaError_t launch_attn_decode_tc(const AttnDecodeArgs& a, int bits, cudaStream_t st);
+cudaError_t launch_attn_decode_tc(const AttnDecodeArgs& a, const DecodePlan& p, int bits,
+                                  cudaStream_t st);
 
 }  // namespace csa

@@ -9,22 +9,29 @@
 //   O^T [d, cols]    += KV^T [d, slots] . P^T        M = 128 channels a tile
 // A CTA takes NC = 32 or 64 columns: the heads of one query or, when the
 // queries of a sequence share their slots (no index list), of several.  Its
-// slots come in tiles of 128; the split of a query's tiles over CTAs and their
-// combination are those of attn_decode.cu.
+// slots come in tiles of 128; a query's tiles are split over the CTAs of a
+// cluster, which join their results through each other's shared memory, and
+// over several clusters where a row is long (attn_decode.cu joins those).
 //
 // The codes of a tile are fetched into registers while the tile before is in
-// the softmax, expanded to bf16 (exact: a code has at most four significant
-// bits) and stored once, 128-byte swizzled: read K-major the tile is the A
-// operand of S^T, read MN-major that of O^T.  The expansion leaves a row's
-// channels permuted within each eight (cache_expand.cuh): Q is permuted alike,
-// and O is put back where it is stored.
+// the softmax (its index entries and page ids one and two tiles earlier: each
+// is a dependent read of global memory), expanded to bf16 (exact: a code has
+// at most four significant bits) and stored once, 128-byte swizzled: read
+// K-major the tile is the A operand of S^T, read MN-major that of O^T.  The
+// expansion leaves a row's channels permuted within each eight
+// (cache_expand.cuh): Q is permuted alike, and O is put back where it is
+// stored.
 //
-// What bounds it: at 64 heads x 512 the conversion of the codes (about three
-// instructions a value) and the tensor core are alike in cost; at 32 x 128 the
-// latency of the chain fetch - convert - S - softmax - O, which several CTAs
-// on an SM overlap.  The arithmetic follows attn_fwd_tc512: probabilities in
-// bf16, their sum and the running maximum in fp32, rescaling only when a
-// column's maximum grows by more than 2^8.
+// What bounds it: at 64 heads x 512 the shared memory (a tile is written once
+// and read twice by the tensor core, whose N = 64 leaves A's reads 1.5 times
+// as long as the products); at 32 x 128 the latency of the chain index - page
+// - codes - S - softmax - O - join.  The arithmetic follows attn_fwd_tc512:
+// probabilities in bf16 (a weight of the values, which the sum of 2^-9
+// relative errors of both signs moves by less than the rounding of o), their
+// sum and the running maximum in fp32, rescaling only when a column's maximum
+// grows by more than 2^8.
+#include <cooperative_groups.h>
+
 #include "attn_decode.h"
 #include "cache_expand.cuh"
 #include "tcgen05.cuh"
@@ -33,6 +40,7 @@ namespace csa {
 namespace adt {
 
 using namespace csa::umma;
+namespace cg = cooperative_groups;
 
 constexpr int kSlots = 128;
 constexpr float kRescale = 8.f;
@@ -59,12 +67,13 @@ struct Cfg {
   static constexpr uint32_t KV = (D / 64) * kQBlk;
   static constexpr uint32_t P = KV + kBlocks * kKvBlk;
   static constexpr uint32_t BARS = P + kSlots * 128;       // s, p, kv[kMT], o[kMT]
-  static constexpr uint32_t MISC = BARS + (2 + 2 * kMT) * 8;   // TMEM slot, dead, rescale
-  static constexpr uint32_t RED = MISC + 16;               // [4][NC]
-  static constexpr uint32_t MRUN = RED + 4 * NC * 4;
-  static constexpr uint32_t FAC = MRUN + NC * 4;
-  static constexpr uint32_t OKS = FAC + NC * 4;            // [2][kSlots] bytes
+  static constexpr uint32_t MISC = BARS + (2 + 2 * kMT) * 8;   // TMEM slot, dead
+  static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][4][NC] column maxima
+  static constexpr uint32_t MRUN = RED + 8 * NC * 4;       // [2][NC]
+  static constexpr uint32_t ML = MRUN + 2 * NC * 4;        // [NC] (maximum, sum) of this CTA
+  static constexpr uint32_t OKS = ML + NC * 8;             // [2][kSlots] bytes
   static constexpr uint32_t kBytes = OKS + 2 * kSlots;
+  static constexpr uint32_t STAGE = KV;                    // [NC][D] fp32: O, after the last tile
 };
 
 // Transposing butterfly: v[c] holds this lane's value of column c; afterwards
@@ -87,10 +96,95 @@ __device__ __forceinline__ float lane_reduce16(float (&v)[16]) {
   return kMax ? fmaxf(v[0], other) : v[0] + other;
 }
 
-template <int D, int NC, int BITS>
-__global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
-    const AttnDecodeArgs a, int per_group, int groups, int head_groups) {
+// Joins the (m, l, O) of the CS CTAs of a cluster for this CTA's share of the
+// columns, from their shared memory: first a weight for each (CTA, column),
+// then the weighted sums, a warp to a column.  final: also the sink, o and
+// lse; otherwise the cluster's entry of the partial results.
+template <int D, int NC, int CS>
+__device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned char* sm, int rank,
+                                             int part, bool final, int per_group, int nq, int heads,
+                                             int h0, long long row0) {
   using C = Cfg<D, NC>;
+  constexpr int kCols = NC / CS;                           // columns of this CTA
+  const unsigned char* base[CS];
+#pragma unroll
+  for (int r = 0; r < CS; ++r) {
+    if constexpr (CS > 1) base[r] = cg::this_cluster().map_shared_rank(sm, r);
+    else base[r] = sm;
+  }
+  float* wgt = reinterpret_cast<float*>(sm + C::RED);      // [kCols][CS], this CTA's own
+  for (int x = threadIdx.x; x < kCols; x += C::kThreads) {
+    const int col = rank * kCols + x;
+    const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
+    const bool live = qi < nq && h < heads;
+    float2 ml[CS];
+#pragma unroll
+    for (int r = 0; r < CS; ++r) ml[r] = *reinterpret_cast<const float2*>(base[r] + C::ML + col * 8);
+    const float sink2 = live && final && a.sink != nullptr ? a.sink[h0 + h] * kLog2e : -INFINITY;
+    float m = sink2, total = 0.f;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) m = fmaxf(m, ml[r].x);
+    float f[CS];
+#pragma unroll
+    for (int r = 0; r < CS; ++r) {
+      // a CTA without a tile has no O: its weight is zero
+      f[r] = ml[r].y > 0.f ? exp2f(ml[r].x - m) : 0.f;
+      total = fmaf(ml[r].y, f[r], total);
+    }
+    if (sink2 > -INFINITY) total += exp2f(sink2 - m);
+    const float inv = !final ? 1.f : total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+    for (int r = 0; r < CS; ++r) wgt[x * CS + r] = f[r] * inv;
+    if (live) {
+      const long long row = row0 + qi;
+      if (final)
+        a.lse[row * a.H + h0 + h] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
+      else
+        a.part_ml[(row * a.parts + part) * a.H + h0 + h] = make_float2(m, total);
+    }
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int x = warp; x < kCols; x += C::kThreads / 32) {
+    const int col = rank * kCols + x;
+    const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
+    if (qi >= nq || h >= heads) continue;
+    float f[CS];
+#pragma unroll
+    for (int r = 0; r < CS; ++r) f[r] = wgt[x * CS + r];
+    const long long row = row0 + qi;
+    __nv_bfloat16* o = (__nv_bfloat16*)a.o + (row * a.H + h0 + h) * D;
+    float* po = a.part_o + ((row * a.parts + part) * a.H + h0 + h) * D;
+#pragma unroll
+    for (int c = lane * 4; c < D; c += 128) {
+      float4 v[CS];
+#pragma unroll
+      for (int r = 0; r < CS; ++r)
+        v[r] = *reinterpret_cast<const float4*>(base[r] + C::STAGE + (col * D + c) * 4);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < CS; ++r) {
+        if (f[r] > 0.f) {
+          acc.x = fmaf(v[r].x, f[r], acc.x);
+          acc.y = fmaf(v[r].y, f[r], acc.y);
+          acc.z = fmaf(v[r].z, f[r], acc.z);
+          acc.w = fmaf(v[r].w, f[r], acc.w);
+        }
+      }
+      if (final)
+        *reinterpret_cast<uint2*>(o + c) =
+            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+      else
+        *reinterpret_cast<float4*>(po + c) = acc;
+    }
+  }
+}
+
+template <int D, int NC, int BITS>
+__global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC)) attn_decode_tc_kernel(
+    const AttnDecodeArgs a, int per_group, int groups, int head_groups, int cs) {
+  using C = Cfg<D, NC>;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -100,21 +194,21 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
   uint64_t* bar_o = bar_kv + C::kMT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
-  int* rescale = reinterpret_cast<int*>(sm + C::MISC + 8);
   float* red = reinterpret_cast<float*>(sm + C::RED);
   float* m_run = reinterpret_cast<float*>(sm + C::MRUN);
-  float* fac = reinterpret_cast<float*>(sm + C::FAC);
+  float2* ml = reinterpret_cast<float2*>(sm + C::ML);
   unsigned char* oks = sm + C::OKS;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // group of queries (per_group of one sequence) and of heads
-  const int hg = (int)blockIdx.x % head_groups;
-  const int qg = (int)blockIdx.x / head_groups;
+  // blockIdx.x: part of the slots (the cs CTAs of a cluster are neighbours);
+  // blockIdx.y: group of queries (per_group of one sequence) and of heads
+  const int split = blockIdx.x, rank = split % cs;
+  const int hg = (int)blockIdx.y % head_groups;
+  const int qg = (int)blockIdx.y / head_groups;
   const int bi = qg / groups, i0 = (qg - bi * groups) * per_group;
   const int nq = min(per_group, a.s_q - i0);
   const int h0 = hg * NC, heads = min(a.H - h0, per_group > 1 ? a.H : NC);   // heads of a query
   const long long row0 = (long long)bi * a.s_q + i0;
-  const int split = blockIdx.y;
 
   // The slots: the union window of the group's queries, then the index
   // entries (one query) or the blocks the last query sees.
@@ -125,31 +219,128 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
   const int ring0 = w0 >= 0 ? w0 % ring : ring - 1 - (int)((unsigned)(-1 - w0) % (unsigned)ring);
   const int slots = last.t < 0 ? 0 : wext + (a.idx != nullptr ? a.K : last.vis);
   const int tiles = (slots + kSlots - 1) / kSlots;
-  const int it0 = (int)((long long)tiles * split / a.splits);
-  const int n = (int)((long long)tiles * (split + 1) / a.splits) - it0;
+  const int it0 = (int)((long long)tiles * split / (int)gridDim.x);
+  const int n = (int)((long long)tiles * (split + 1) / (int)gridDim.x) - it0;
 
   if (tid == 0) {
     mbar_init(bar_s, 1);
-    mbar_init(bar_p, C::kCompute);
+    mbar_init(bar_p, C::kWarps);
     for (int m = 0; m < C::kMT; ++m) {
-      mbar_init(&bar_kv[m], C::kCompute);
+      mbar_init(&bar_kv[m], C::kWarps);
       mbar_init(&bar_o[m], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *dead = 0;
   }
   if (warp == C::kWarps && n > 0) tmem_alloc(tmem_slot, C::kTmem);
-  if (tid < NC) m_run[tid] = -INFINITY;
+  if (tid < NC) {
+    m_run[tid] = -INFINITY;
+    ml[tid] = make_float2(-INFINITY, 0.f);
+  }
+
+  // ---- the converting side's reads: index entry, page id, codes -----------------
+  const int cgr = (lane >> 3) % C::kGroups;                // scale group this thread converts
+  const int cslot = warp * C::kPerWarp + (lane / C::kLanes) * 8 + (lane & 7);
+  const bool conv = warp < C::kWarps;
+  int jraw[C::kSpt], lslot[C::kSpt], page[C::kSpt];
+  Codes<BITS> cd[C::kSpt * C::kMT];
+  const int32_t* raw_pages = a.raw_table + (long long)bi * a.P_raw;
+  const int32_t* cmp_pages = a.cmp_table + (long long)bi * a.P_cmp;
+  auto slot_of = [&](int it, int k) {                      // -1: past the tiles or the list
+    const int s = (it0 + it) * kSlots + cslot + k * C::kPass;
+    return it < n && cslot + k * C::kPass < kSlots && s < slots ? s : -1;
+  };
+  auto read_index = [&](int it) {
+#pragma unroll
+    for (int k = 0; k < C::kSpt; ++k) {
+      const int s = slot_of(it, k);
+      jraw[k] = s - wext;
+      if (a.idx != nullptr) jraw[k] = __ldg(a.idx + row0 * a.K + max(s - wext, 0));
+    }
+  };
+  auto read_page = [&](int it) {
+#pragma unroll
+    for (int k = 0; k < C::kSpt; ++k) {
+      const int s = slot_of(it, k);
+      const bool raw = s < wext;
+      const int rs = ring0 + s >= ring ? ring0 + s - ring : ring0 + s;
+      int x = raw ? (w0 + s >= 0 ? rs : -1) : (jraw[k] < last.vis ? jraw[k] : -1);
+      if (s < 0) x = -1;
+      lslot[k] = max(x, -1);
+      page[k] = __ldg((raw || x < 0 ? raw_pages : cmp_pages) + (x < 0 ? 0 : page_index(a.cs, x)));
+    }
+  };
+  auto fetch = [&](int it) {
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
+#pragma unroll
+    for (int k = 0; k < C::kSpt; ++k) {
+      const bool inside = (unsigned)page[k] < (unsigned)a.cs.n_pages;
+      const bool ok = lslot[k] >= 0 && inside;
+      if (lslot[k] >= 0 && !inside) set_status(a.status, kDevCheck, kSiteCachePage);
+      if (cgr == 0 && cslot + k * C::kPass < kSlots)
+        oks[(it & 1) * kSlots + cslot + k * C::kPass] = ok;
+      const int r = lslot[k] - page_index(a.cs, lslot[k]) * a.cs.page_size;
+      const uint8_t* base = a.cache + page_base(a.cs, page[k]);
+      const uint8_t* code = (ok ? base + row_code(a.cs, r) : zero) + cgr * (4 * BITS);
+      const uint8_t* scale = ok ? base + row_scale(a.cs, r) : zero;
+      uint32_t sw[C::kMT];                                 // the row's scale bytes, four a word
+      if constexpr (C::kMT == 4) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(scale));
+        sw[0] = w.x;
+        sw[1] = w.y;
+        sw[2] = w.z;
+        sw[3] = w.w;
+      } else if constexpr (C::kMT == 2) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(scale));
+        sw[0] = w.x;
+        sw[1] = w.y;
+      } else if constexpr (C::kGroups == 4) {
+        sw[0] = __ldg(reinterpret_cast<const uint32_t*>(scale));
+      } else {
+        sw[0] = __ldg(reinterpret_cast<const uint16_t*>(scale));
+      }
+#pragma unroll
+      for (int m = 0; m < C::kMT; ++m) {
+        Codes<BITS>& c = cd[k * C::kMT + m];
+#pragma unroll
+        for (int e = 0; e < BITS / 4; ++e)
+          c.w[e] = __ldg(reinterpret_cast<const uint4*>(code + m * (16 * BITS)) + e);
+        c.scale = sw[m];                                   // this thread's byte is taken in convert
+      }
+    }
+  };
+  if (conv && n > 0) read_index(0);
+
   // Q: column c is query i0 + c / H, head h0 + c % H; columns past them are zero
-  for (int e = tid; e < NC * (D / 8); e += C::kThreads) {
-    const int c = e / (D / 8), ch = e - c * (D / 8);
-    const int qi = per_group > 1 ? c / a.H : 0, h = per_group > 1 ? c - qi * a.H : c;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (qi < nq && h < heads)
-      v = *reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
-                                          ((row0 + qi) * a.H + h0 + h) * D + ch * 8);
-    *reinterpret_cast<uint4*>(sm + C::Q + (ch >> 3) * C::kQBlk + c * 128 +
-                              (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(v);
+  constexpr int kQIter = (NC * (D / 8) + C::kThreads - 1) / C::kThreads;
+  constexpr int kQBatch = kQIter < 8 ? kQIter : 8;
+  for (int x0 = 0; x0 < kQIter; x0 += kQBatch) {
+    uint4 v[kQBatch];
+#pragma unroll
+    for (int x = 0; x < kQBatch; ++x) {
+      const int e = tid + (x0 + x) * C::kThreads, c = e / (D / 8), ch = e - c * (D / 8);
+      const int qi = per_group > 1 ? c / a.H : 0, h = per_group > 1 ? c - qi * a.H : c;
+      v[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < NC && qi < nq && h < heads)
+        v[x] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                    ((row0 + qi) * a.H + h0 + h) * D + ch * 8));
+    }
+    if (x0 == 0 && conv && n > 0) {
+      read_page(0);
+      read_index(1);
+    }
+#pragma unroll
+    for (int x = 0; x < kQBatch; ++x) {
+      const int e = tid + (x0 + x) * C::kThreads, c = e / (D / 8), ch = e - c * (D / 8);
+      if (c < NC)
+        *reinterpret_cast<uint4*>(sm + C::Q + (ch >> 3) * C::kQBlk + c * 128 +
+                                  (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(v[x]);
+    }
+  }
+  if (conv && n > 0) {
+    fetch(0);
+    read_page(1);
+    read_index(2);
   }
   fence_proxy_async_smem();
   fence_before();
@@ -165,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
     return false;
   };
 
-  if (warp == C::kWarps) {
+  if (!conv) {
     // ---- the issuing warp ------------------------------------------------------
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32_major(kSlots, NC, 0, 0);
@@ -210,57 +401,15 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
     const int my_q = per_group > 1 ? (hq * 16) / a.H : 0;  // query of this thread's columns
     const int my_t = last.t - (nq - 1) + my_q;
     const int my_vis = min(my_t >= 0 ? (int)((unsigned)(my_t + 1) / (unsigned)a.ratio) : 0, last.vis);
-    const int cg = (lane >> 3) % C::kGroups;               // scale group this thread converts
-    const int cslot = warp * C::kPerWarp + (lane / C::kLanes) * 8 + (lane & 7);
 
-    const uint8_t* code_p[C::kSpt];
-    const uint8_t* scale_p[C::kSpt];                       // null: masked
-    Codes<BITS> cd[C::kSpt * C::kMT];
-
-    auto locate = [&](int it) {
-#pragma unroll
-      for (int k = 0; k < C::kSpt; ++k) {
-        const int s = (it0 + it) * kSlots + cslot + k * C::kPass;
-        long long code = 0, scale = 0;
-        bool ok = false;
-        if (it < n && cslot + k * C::kPass < kSlots && s < slots) {
-          if (s < wext) {
-            const int pos = w0 + s;
-            int slot = ring0 + s;                          // ring0 + s < 2 ring
-            slot -= slot >= ring ? ring : 0;
-            if (pos >= 0)
-              ok = cache_row(a.cs, a.raw_table + (long long)bi * a.P_raw, slot, &code, &scale,
-                             a.status);
-          } else {
-            const int j = a.idx != nullptr ? a.idx[row0 * a.K + s - wext] : s - wext;
-            if (j >= 0 && j < last.vis)
-              ok = cache_row(a.cs, a.cmp_table + (long long)bi * a.P_cmp, j, &code, &scale,
-                             a.status);
-          }
-        }
-        code_p[k] = a.cache + code + cg * (4 * BITS);
-        scale_p[k] = ok ? a.cache + scale + cg : nullptr;
-      }
-    };
-    auto fetch = [&]() {
-#pragma unroll
-      for (int k = 0; k < C::kSpt; ++k)
-#pragma unroll
-        for (int m = 0; m < C::kMT; ++m) {
-          Codes<BITS>& c = cd[k * C::kMT + m];
-          c.clear();
-          if (scale_p[k] != nullptr) c.load(code_p[k] + m * (16 * BITS), scale_p[k] + m * 4);
-        }
+    // One arrival a warp: 512 on one barrier take a thousand cycles.
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
     };
     // Expands the fetched codes of tile it into the KV buffer; M tile m's
     // channels are free once O^T of the tile before has read them.
     auto convert = [&](int it) {
-      if (cg == 0) {
-#pragma unroll
-        for (int k = 0; k < C::kSpt; ++k)
-          if (cslot + k * C::kPass < kSlots)
-            oks[(it & 1) * kSlots + cslot + k * C::kPass] = scale_p[k] != nullptr;
-      }
 #pragma unroll
       for (int m = 0; m < C::kMT; ++m) {
         if (it > 0) wait(&bar_o[m], (it - 1) & 1);
@@ -268,12 +417,13 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
         for (int k = 0; k < C::kSpt; ++k) {
           const int s = cslot + k * C::kPass;
           if (s >= kSlots) continue;
-          const Codes<BITS>& c = cd[k * C::kMT + m];
-          unsigned char* dst = sm + C::KV + (uint32_t)(m * 2 + (cg >> 1)) * kKvBlk + s * 128;
-          expand_group<BITS>(c, dst, (cg & 1) * 4, s & 7);
+          Codes<BITS> c = cd[k * C::kMT + m];
+          c.scale = (c.scale >> (8 * cgr)) & 255u;
+          unsigned char* dst = sm + C::KV + (uint32_t)(m * 2 + (cgr >> 1)) * kKvBlk + s * 128;
+          expand_group<BITS>(c, dst, (cgr & 1) * 4, s & 7);
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bar_kv[m]);
+        arrive(&bar_kv[m]);
       }
     };
     auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(C::kCompute) : "memory"); };
@@ -282,18 +432,18 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
 #pragma unroll
     for (int c = 0; c < 16; ++c) l_part[c] = 0.f;
 
-    locate(0);
-    fetch();
     convert(0);
-    locate(1);
     for (int it = 0; it < n; ++it) {
       const bool more = it + 1 < n;
-      if (more) fetch();
-      sync();                                              // oks of this tile, rescale flag free
-      if (tid == 0) *rescale = 0;
+      if (more) {
+        fetch(it + 1);
+        read_page(it + 2);
+        read_index(it + 3);
+      }
       wait(bar_s, it & 1);
       fence_after();
       // ---- softmax over the tile's slots, per column --------------------------
+      // oks of this tile was written before the barrier of the tile before
       const int s = (it0 + it) * kSlots + r;
       bool ok = oks[(it & 1) * kSlots + r] != 0;
       if (s < wext) {
@@ -315,35 +465,43 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
 #pragma unroll
         for (int c = 0; c < 16; ++c) mx[c] = x[c];
         const float m = lane_reduce16<true>(mx);
-        if (lane < 16) red[qd * NC + hq * 16 + lane] = m;
+        if (lane < 16) red[((it & 1) * 4 + qd) * NC + hq * 16 + lane] = m;
       }
       sync();
-      if (tid < NC) {
-        const float mt = fmaxf(fmaxf(red[tid], red[NC + tid]), fmaxf(red[2 * NC + tid], red[3 * NC + tid]));
-        const float mo = m_run[tid];
-        float f = 1.f;
-        if (mt > mo + kRescale || (mo == -INFINITY && mt != -INFINITY)) {
-          f = ex2(mo - mt);                                // 0 when mo = -inf
-          m_run[tid] = mt;
-          if (it > 0) *rescale = 1;
-        }
-        fac[tid] = f;
+      // lane c of every warp takes the new maximum of the warp's column c from the
+      // four quarters; quarter 0 keeps it for the next tile
+      float mt = -INFINITY, mo = -INFINITY;
+      if (lane < 16) {
+        const float* rq = red + (it & 1) * 4 * NC + hq * 16 + lane;
+        mt = fmaxf(fmaxf(rq[0], rq[NC]), fmaxf(rq[2 * NC], rq[3 * NC]));
+        mo = m_run[(it & 1) * NC + hq * 16 + lane];
       }
-      sync();
-      if (*rescale) {
+      const bool g = mt > mo + kRescale || (mo == -INFINITY && mt != -INFINITY);
+      const float m_new = g ? mt : mo;
+      if (qd == 0 && lane < 16) m_run[((it & 1) ^ 1) * NC + hq * 16 + lane] = m_new;
+      const unsigned grow = __ballot_sync(0xffffffffu, g);
+      if (grow != 0) {                                     // warp-uniform
+        const float f = g ? ex2(mo - mt) : 1.f;            // 0 when mo = -inf
 #pragma unroll
-        for (int c = 0; c < 16; ++c) l_part[c] *= fac[hq * 16 + c];
+        for (int c = 0; c < 16; ++c) l_part[c] *= __shfl_sync(0xffffffffu, f, c);
+        if (it > 0) {
 #pragma unroll 1
-        for (int m = 0; m < C::kMT; ++m) {
-          const uint32_t ta = tmem + lane_base + C::kColO + m * NC + hq * 16;
-          uint32_t v[16];
-          tmem_ld16_wait(ta, v);
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            tmem_st1(ta + c, __float_as_uint(__uint_as_float(v[c]) * fac[hq * 16 + c]));
+          for (int m = 0; m < C::kMT; ++m) {
+            const uint32_t ta = tmem + lane_base + C::kColO + m * NC + hq * 16;
+#pragma unroll 1
+            for (int c = 0; c < 16; ++c) {
+              if (grow >> c & 1) {
+                const uint32_t o = tmem_ld1_wait(ta + c);
+                tmem_st1(ta + c, __float_as_uint(__uint_as_float(o) * __shfl_sync(0xffffffffu, f, c)));
+              }
+            }
+          }
+          tmem_wait_st();
         }
-        tmem_wait_st();
       }
+      // P = 2^(x - m), masked slots 2^-inf = 0; a column without an unmasked
+      // slot so far has m = -inf and takes 0 instead
+      const float m_use = m_new == -INFINITY ? 0.f : m_new;
       unsigned char* prow = sm + C::P + r * 128;
 #pragma unroll
       for (int c8 = 0; c8 < 2; ++c8) {
@@ -351,10 +509,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
           const int c = c8 * 8 + e;
-          // a column without an unmasked slot so far has m = -inf: no mass
-          const float m0 = m_run[hq * 16 + c], m1 = m_run[hq * 16 + c + 1];
-          const float p0 = ok ? ex2(x[c] - m0) : 0.f;
-          const float p1 = ok ? ex2(x[c + 1] - m1) : 0.f;
+          const float p0 = ex2(x[c] - __shfl_sync(0xffffffffu, m_use, c));
+          const float p1 = ex2(x[c + 1] - __shfl_sync(0xffffffffu, m_use, c + 1));
           l_part[c] += p0;
           l_part[c + 1] += p1;
           pk[e / 2] = pack_bf16x2(p0, p1);
@@ -364,43 +520,19 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
       }
       fence_proxy_async_smem();
       fence_before();
-      mbar_arrive(bar_p);
-      if (more) {
-        convert(it + 1);
-        locate(it + 2);
-      }
+      arrive(bar_p);
+      if (more) convert(it + 1);
     }
 #pragma unroll
     for (int m = 0; m < C::kMT; ++m) wait(&bar_o[m], (n - 1) & 1);
     fence_after();
     {
       const float l = lane_reduce16<false>(l_part);
-      if (lane < 16) red[qd * NC + hq * 16 + lane] = l;
+      if (lane < 16) red[((n & 1) * 4 + qd) * NC + hq * 16 + lane] = l;
     }
-    sync();
-    if (tid < NC) {
-      const float l = (red[tid] + red[NC + tid]) + (red[2 * NC + tid] + red[3 * NC + tid]);
-      const int qi = per_group > 1 ? tid / a.H : 0, h = per_group > 1 ? tid - qi * a.H : tid;
-      const bool live = qi < nq && h < heads && !*dead;
-      const long long row = row0 + qi;
-      if (a.splits > 1) {
-        if (live) a.part_ml[(row * a.splits + split) * a.H + h0 + h] = make_float2(m_run[tid], l);
-        fac[tid] = 1.f;
-      } else {
-        const float sink2 = a.sink != nullptr && live ? a.sink[h0 + h] * kLog2e : -INFINITY;
-        const float m = m_run[tid], mm = fmaxf(m, sink2);
-        float f = 0.f, out = -INFINITY;
-        if (mm > -INFINITY) {
-          const float fm = exp2f(m - mm), total = fmaf(l, fm, exp2f(sink2 - mm));
-          f = fm / total;
-          out = (mm + log2f(total)) * kLn2;
-        }
-        fac[tid] = f;
-        if (live) a.lse[row * a.H + h0 + h] = out;
-      }
-    }
-    sync();
+    // O^T into shared memory as [column][channel]: the KV tile's place
     if (!*dead) {
+      float* stage = reinterpret_cast<float*>(sm + C::STAGE);
 #pragma unroll 1
       for (int m = 0; m < C::kMT; ++m) {
         const int p = m * 128 + r;
@@ -409,47 +541,37 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
         if (p < D) {
           const int ch = channel_of<BITS>(p);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int col = hq * 16 + c;
-            const int h = per_group > 1 ? col - my_q * a.H : col;
-            if (my_q < nq && h < heads) {
-              const float val = __uint_as_float(v[c]) * fac[col];
-              const long long row = row0 + my_q;
-              if (a.splits > 1)
-                a.part_o[((row * a.splits + split) * a.H + h0 + h) * D + ch] = val;
-              else
-                ((__nv_bfloat16*)a.o)[(row * a.H + h0 + h) * D + ch] = __float2bfloat16_rn(val);
-            }
-          }
+          for (int c = 0; c < 16; ++c) stage[(hq * 16 + c) * D + ch] = __uint_as_float(v[c]);
         }
       }
     }
+    sync();
+    if (tid < NC) {
+      const float* rl = red + (n & 1) * 4 * NC + tid;
+      ml[tid] = make_float2(m_run[(n & 1) * NC + tid], (rl[0] + rl[NC]) + (rl[2 * NC] + rl[3 * NC]));
+    }
     fence_before();
-  } else {
-    // no tile: an empty part of a split, or a query with nothing to attend to
-    for (int c = tid; c < NC; c += C::kCompute) {
-      const int qi = per_group > 1 ? c / a.H : 0, h = per_group > 1 ? c - qi * a.H : c;
-      if (qi >= nq || h >= heads) continue;
-      const long long rh = (row0 + qi) * a.H + h0 + h;
-      if (a.splits > 1)
-        a.part_ml[((row0 + qi) * a.splits + split) * a.H + h0 + h] = make_float2(-INFINITY, 0.f);
-      else
-        a.lse[rh] = a.sink != nullptr ? a.sink[h0 + h] : -INFINITY;
-    }
-    if (a.splits == 1) {
-      for (int e = tid; e < nq * heads * (D / 8); e += C::kCompute) {
-        const int c = e / (D / 8), qi = c / heads, h = c - qi * heads;
-        *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + ((row0 + qi) * a.H + h0 + h) * D +
-                                  (e - c * (D / 8)) * 8) = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
   }
-  __syncthreads();
-  if (tid == 0 && *dead) set_status(a.status, kDevTimeout, kSiteDecode);
+  // ---- join ----------------------------------------------------------------------
+  if (cs > 1) cg::this_cluster().sync();
+  else __syncthreads();
+  if (!*dead) {
+    const bool final = a.parts == 1;
+    const int part = split / cs;
+    switch (cs) {
+      case 1: join_cluster<D, NC, 1>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
+      case 2: join_cluster<D, NC, 2>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
+      case 4: join_cluster<D, NC, 4>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
+      default: join_cluster<D, NC, 8>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
+    }
+  } else if (tid == 0) {
+    set_status(a.status, kDevTimeout, kSiteDecode);
+  }
   if (warp == C::kWarps && n > 0) {
     fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
+  if (cs > 1) cg::this_cluster().sync();                   // no CTA leaves while another reads it
 }
 
 }  // namespace adt
@@ -457,46 +579,53 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads) attn_decode_tc_kernel(
 namespace {
 
 template <int D, int NC, int BITS>
-cudaError_t launch_tc(const AttnDecodeArgs& a, int per_group, int groups, int head_groups,
-                      cudaStream_t st) {
+cudaError_t launch_tc(const AttnDecodeArgs& a, const DecodePlan& p, cudaStream_t st) {
   using C = adt::Cfg<D, NC>;
   const size_t smem = 1024 + C::kBytes;
   auto k = adt::attn_decode_tc_kernel<D, NC, BITS>;
   const cudaError_t e =
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k<<<dim3((unsigned)(a.b * groups * head_groups), a.splits), C::kThreads, smem, st>>>(
-      a, per_group, groups, head_groups);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.cluster * p.parts), (unsigned)(a.b * p.groups * p.head_groups));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
   count_launches(1);
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, k, a, p.per_group, p.groups, p.head_groups, p.cluster);
 }
 
 template <int D, int NC>
-cudaError_t launch_tc_bits(const AttnDecodeArgs& a, int bits, int pg, int g, int hg,
+cudaError_t launch_tc_bits(const AttnDecodeArgs& a, int bits, const DecodePlan& p,
                            cudaStream_t st) {
-  return bits == 4 ? launch_tc<D, NC, 4>(a, pg, g, hg, st) : launch_tc<D, NC, 8>(a, pg, g, hg, st);
+  return bits == 4 ? launch_tc<D, NC, 4>(a, p, st) : launch_tc<D, NC, 8>(a, p, st);
 }
 
 template <int NC>
-cudaError_t launch_tc_width(const AttnDecodeArgs& a, int bits, int pg, int g, int hg,
+cudaError_t launch_tc_width(const AttnDecodeArgs& a, int bits, const DecodePlan& p,
                             cudaStream_t st) {
   switch (a.d) {
-    case 64: return launch_tc_bits<64, NC>(a, bits, pg, g, hg, st);
-    case 128: return launch_tc_bits<128, NC>(a, bits, pg, g, hg, st);
-    case 256: return launch_tc_bits<256, NC>(a, bits, pg, g, hg, st);
-    default: return launch_tc_bits<512, NC>(a, bits, pg, g, hg, st);
+    case 64: return launch_tc_bits<64, NC>(a, bits, p, st);
+    case 128: return launch_tc_bits<128, NC>(a, bits, p, st);
+    case 256: return launch_tc_bits<256, NC>(a, bits, p, st);
+    default: return launch_tc_bits<512, NC>(a, bits, p, st);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_attn_decode_tc(const AttnDecodeArgs& a, int bits, cudaStream_t st) {
-  const DecodePlan p = decode_plan_tc(a.b, a.s_q, a.H, a.d, a.window, a.idx != nullptr ? a.K : 0,
-                                      a.idx == nullptr, (long long)a.P_cmp * a.cs.page_size);
-  const cudaError_t e = p.cols == 32
-                            ? launch_tc_width<32>(a, bits, p.per_group, p.groups, p.head_groups, st)
-                            : launch_tc_width<64>(a, bits, p.per_group, p.groups, p.head_groups, st);
-  if (e != cudaSuccess || a.splits == 1) return e;
+cudaError_t launch_attn_decode_tc(const AttnDecodeArgs& a, const DecodePlan& p, int bits,
+                                  cudaStream_t st) {
+  const cudaError_t e = p.cols == 32 ? launch_tc_width<32>(a, bits, p, st)
+                                     : launch_tc_width<64>(a, bits, p, st);
+  if (e != cudaSuccess || p.parts == 1) return e;
   return launch_attn_decode_combine(a, true, st);
 }
 

@@ -87,22 +87,21 @@ __global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDe
 #pragma unroll
     for (int k = 0; k < C::kKpt; ++k) {
       const int j = tile * kIdxTile + ckey + k * C::kPass;
-      page[k] = j < most ? __ldg(pages + page_index(a.cs, j)) : 0;
+      page[k] = __ldg(pages + page_index(a.cs, min(j, most - 1)));
     }
   };
   auto fetch_codes = [&](int tile) {
 #pragma unroll
     for (int k = 0; k < C::kKpt; ++k) {
       const int j = tile * kIdxTile + ckey + k * C::kPass;
-      cd[k].clear();
-      if (j >= most) continue;
-      if ((unsigned)page[k] < (unsigned)a.cs.n_pages) {
-        const int r = j - page_index(a.cs, j) * a.cs.page_size;
-        const uint8_t* base = a.cache + page_base(a.cs, page[k]);
-        cd[k].load(base + row_code(a.cs, r) + cg * (4 * BITS), base + row_scale(a.cs, r) + cg);
-      } else {
-        set_status(a.status, kDevCheck, kSiteCachePage);
-      }
+      const bool ok = (unsigned)page[k] < (unsigned)a.cs.n_pages;
+      if (!ok) set_status(a.status, kDevCheck, kSiteCachePage);
+      const int r = j - page_index(a.cs, j) * a.cs.page_size;
+      const uint8_t* base = a.cache + page_base(a.cs, page[k]);
+      const bool live = ok && j < most;
+      const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
+      cd[k].load(live ? base + row_code(a.cs, r) + cg * (4 * BITS) : zero,
+                 live ? base + row_scale(a.cs, r) + cg : zero);
     }
   };
   // Q: column c is query c / hpad, head c % hpad; the others are zero

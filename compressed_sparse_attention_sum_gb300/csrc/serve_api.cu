@@ -70,11 +70,11 @@ bool decode_sizes(int b, int s_q, int H, int d, int window, long long cmp_rows) 
   return b >= 1 && s_q >= 1 && H >= 1 && d >= 32 && d % 32 == 0 && window >= 1 && cmp_rows >= 0;
 }
 
-// Partial results of a call that splits its slots.
-size_t attn_decode_layout(csa::AttnDecodeArgs* a, int splits, unsigned char* ws) {
-  a->splits = splits;
-  if (splits == 1) return 0;
-  const size_t n = (size_t)a->b * a->s_q * splits * a->H;
+// Partial results of a call whose queries are cut into parts.
+size_t attn_decode_layout(csa::AttnDecodeArgs* a, int parts, unsigned char* ws) {
+  a->parts = parts;
+  if (parts == 1) return 0;
+  const size_t n = (size_t)a->b * a->s_q * parts * a->H;
   a->part_ml = reinterpret_cast<float2*>(ws);
   const size_t at = (n * sizeof(float2) + 15) / 16 * 16;
   a->part_o = reinterpret_cast<float*>(ws + at);
@@ -182,14 +182,14 @@ size_t csa_attn_decode_workspace_size(int b, int s_q, int H, int d, int window, 
   a.H = H;
   a.d = d;
   // the largest over the kernels and over calls with and without an index list
-  int splits = csa::decode_plan_simt(b, s_q, H, window, cmp_rows).splits;
+  int parts = csa::decode_plan_simt(b, s_q, H, window, cmp_rows).parts;
   if (csa::decode_tc_width(d)) {
     for (const bool dense : {false, true}) {
-      const int t = csa::decode_plan_tc(b, s_q, H, d, window, dense ? 0 : cmp_rows, dense, cmp_rows).splits;
-      splits = t > splits ? t : splits;
+      const int t = csa::decode_plan_tc(b, s_q, H, d, window, dense ? 0 : cmp_rows, dense, cmp_rows).parts;
+      parts = t > parts ? t : parts;
     }
   }
-  return attn_decode_layout(&a, splits, nullptr);
+  return attn_decode_layout(&a, parts, nullptr);
 }
 
 csa_status_t csa_attn_decode(const void* q, const void* cache, const int32_t* raw_table,
@@ -238,16 +238,16 @@ csa_status_t csa_attn_decode(const void* q, const void* cache, const int32_t* ra
   a.P_cmp = P_cmp;
   a.cs = csa::cache_shape(page_size, n_pages, d, bits);
   const bool tc = dt == CSA_BF16 && csa::decode_tc_width(d);
-  const int splits =
+  const csa::DecodePlan plan =
       tc ? csa::decode_plan_tc(b, s_q, H, d, window, K, idx == nullptr,
-                               (long long)P_cmp * page_size).splits
-         : csa::decode_plan_simt(b, s_q, H, window, cmp_rows).splits;
+                               (long long)P_cmp * page_size)
+         : csa::decode_plan_simt(b, s_q, H, window, cmp_rows);
   const size_t need = csa_attn_decode_workspace_size(b, s_q, H, d, window, (int)cmp_rows);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return CSA_ERR_WORKSPACE;
-  attn_decode_layout(&a, splits, (unsigned char*)workspace);
+  attn_decode_layout(&a, plan.parts, (unsigned char*)workspace);
   a.status = csa::device_status_word();
   const cudaStream_t s = (cudaStream_t)stream;
-  return from_cuda(tc ? csa::launch_attn_decode_tc(a, bits, s)
+  return from_cuda(tc ? csa::launch_attn_decode_tc(a, plan, bits, s)
                       : csa::launch_attn_decode_simt(a, dt == CSA_BF16, bits, s));
 }
 
