@@ -10,6 +10,7 @@
 #include <cuda_bf16.h>
 
 #include "attn_decode.h"
+#include "smem_once.h"
 #include "tcgen05.cuh"
 
 namespace csa {
@@ -170,9 +171,8 @@ cudaError_t launch_simt(const AttnDecodeArgs& a, cudaStream_t st) {
   const size_t smem = (size_t)kTile * a.d * sizeof(float);
 #define CSA_DEC(ND)                                                                              \
   do {                                                                                           \
-    const cudaError_t e = cudaFuncSetAttribute(attn_decode_simt_kernel<T, BITS, ND>,             \
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,      \
-                                               (int)smem);                                       \
+    static SmemOnce once;                                                                        \
+    const cudaError_t e = once(attn_decode_simt_kernel<T, BITS, ND>, kTile * 32 * ND * 4);        \
     if (e != cudaSuccess) return e;                                                              \
     attn_decode_simt_kernel<T, BITS, ND><<<grid, kThreads, smem, st>>>(a);                       \
   } while (0)

@@ -34,6 +34,7 @@
 
 #include "attn_decode.h"
 #include "cache_expand.cuh"
+#include "smem_once.h"
 #include "tcgen05.cuh"
 
 namespace csa {
@@ -583,8 +584,8 @@ cudaError_t launch_tc(const AttnDecodeArgs& a, const DecodePlan& p, cudaStream_t
   using C = adt::Cfg<D, NC>;
   const size_t smem = 1024 + C::kBytes;
   auto k = adt::attn_decode_tc_kernel<D, NC, BITS>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemOnce once;
+  const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.cluster * p.parts), (unsigned)(a.b * p.groups * p.head_groups));

@@ -77,6 +77,33 @@ __device__ __forceinline__ void expand8(uint32_t w0, uint32_t w1, uint32_t (&o)[
   }
 }
 
+// Words of expand8 times the group's scale byte's 2^(s - 127).
+template <int BITS>
+__device__ __forceinline__ void scale8(uint32_t s, uint32_t (&o)[4]) {
+  // scale * 2^126 (2^120) as bf16 bits; where that is beyond bf16 (a scale
+  // above 2^1, 2^7) a second factor carries the rest
+  const int e = (int)s + (BITS == 4 ? 126 : 120);
+  const uint32_t f1 = (uint32_t)min(e, 254) * 0x00800080u;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f1);
+  if (e > 254) {
+    const uint32_t f2 = (uint32_t)(e - 254 + 127) * 0x00800080u;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f2);
+  }
+}
+
+// Permuted words of eight channels back into channel order.
+template <int BITS>
+__device__ __forceinline__ uint4 natural8(const uint32_t (&o)[4]) {
+  if constexpr (BITS == 4)
+    return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                      __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+  else
+    return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[0], o[1], 0x7632),
+                      __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[2], o[3], 0x7632));
+}
+
 // A scale group -> four 16-byte chunks (ch0 .. ch0 + 3) of a row of 128 bytes
 // in the 128-byte swizzle (row & 7 = sw).  With NORM returns the sum of its
 // squares, added in bf16 (16 to an accumulator: within 4% below and above).
@@ -84,10 +111,6 @@ template <int BITS, bool NORM = false>
 __device__ __forceinline__ float expand_group(const Codes<BITS>& c, unsigned char* row, int ch0,
                                               int sw) {
   __nv_bfloat162 sq = __floats2bfloat162_rn(0.f, 0.f);
-  // scale * 2^126 (2^120) as bf16 bits; where that is beyond bf16 (a scale
-  // above 2^1, 2^7) a second factor carries the rest
-  const int e = (int)c.scale + (BITS == 4 ? 126 : 120);
-  const uint32_t f1 = (uint32_t)min(e, 254) * 0x00800080u;
   const uint32_t words[8] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w,
                              c.w[BITS / 4 - 1].x, c.w[BITS / 4 - 1].y, c.w[BITS / 4 - 1].z,
                              c.w[BITS / 4 - 1].w};
@@ -96,13 +119,7 @@ __device__ __forceinline__ float expand_group(const Codes<BITS>& c, unsigned cha
     uint32_t o[4];
     if constexpr (BITS == 4) expand8<4>(words[j], 0u, o);
     else expand8<8>(words[2 * j], words[2 * j + 1], o);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f1);
-    if (e > 254) {
-      const uint32_t f2 = (uint32_t)(e - 254 + 127) * 0x00800080u;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[x] = mul_bf16x2(o[x], f2);
-    }
+    scale8<BITS>(c.scale, o);
     *reinterpret_cast<uint4*>(row + (((ch0 + j) ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
     if constexpr (NORM) {
 #pragma unroll

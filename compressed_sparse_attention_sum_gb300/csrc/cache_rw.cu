@@ -3,9 +3,11 @@
 // Both move each row once: d elements of bf16 / fp32 on one side, d * bits / 8
 // code bytes and d / 32 scale bytes on the other, so HBM bounds them (launch
 // latency when a decode step appends a few rows).  A thread owns eight
-// channels (16 or 32 bytes of the row, 4 or 8 bytes of codes), so four lanes
+// channels (16 or 32 bytes of a row, 4 or 8 bytes of codes), so four lanes
 // share a group's maximum through two shuffles and a warp's accesses are
-// contiguous.
+// contiguous; of long ranges it takes several rows, whose page ids and then
+// whose bytes are read all at once.
+#include "cache_expand.cuh"
 #include "cache_format.cuh"
 
 namespace csa {
@@ -13,95 +15,159 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Row `i` of sequence `bi`: its slot in the ring, or -1 when it is not moved
-// (past the count; a later row of the same call takes the slot).
-__device__ __forceinline__ int ring_slot(const int32_t* pos0, const int32_t* counts, int bi, int i,
-                                         int s, int ring, bool write, int* status) {
+// The rows [0, n) of a sequence that a call moves and its first position; n = 0
+// where the position is outside its range.
+__device__ __forceinline__ int range_of(const int32_t* pos0, const int32_t* counts, int bi, int s,
+                                        int* p0, int* status) {
   int n = s;
   if (counts != nullptr) {
     n = counts[bi];
     if (n < 0 || n > s) {
-      if (i == 0) set_status(status, kDevCheck, kSiteCacheRange);
+      set_status(status, kDevCheck, kSiteCacheRange);
       n = max(0, min(n, s));
     }
   }
-  if (i >= n) return -1;
-  const int p0 = pos0[bi];
-  if (p0 < 0 || (long long)p0 + n > 0x7fffffffll) {
-    if (i == 0) set_status(status, kDevCheck, kSiteCacheRange);
-    return -1;
+  *p0 = pos0[bi];
+  if (n > 0 && (*p0 < 0 || (long long)*p0 + n > 0x7fffffffll)) {
+    set_status(status, kDevCheck, kSiteCacheRange);
+    n = 0;
   }
-  if (write && i < n - ring) return -1;
-  return (int)(((unsigned)p0 + (unsigned)i) % (unsigned)ring);
+  return n;
 }
 
-template <typename T, int BITS>
+// The slots of U rows i, i + step, ... : pages read together; -1 for a row that
+// is not moved.
+template <int U>
+__device__ __forceinline__ void slots_of(const CacheShape& cs, const int32_t* pages, int i, int step,
+                                         int first, int n, int p0, int ring, int* status,
+                                         int (&slot)[U], int (&page)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int r = i + u * step;
+    slot[u] = r >= first && r < n ? (int)(((unsigned)p0 + (unsigned)r) % (unsigned)ring) : -1;
+    page[u] = __ldg(pages + (slot[u] < 0 ? 0 : page_index(cs, slot[u])));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (slot[u] >= 0 && (unsigned)page[u] >= (unsigned)cs.n_pages) {
+      set_status(status, kDevCheck, kSiteCachePage);
+      page[u] = -1;
+    }
+  }
+}
+
+// blockIdx.y: sequence; a block takes kThreads / (d / 8) rows at a time, U
+// times.  Threads past the last whole row idle (d / 8 is a multiple of 4, so
+// the lanes of a group stay together).
+template <typename T, int BITS, int U>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(
     const T* __restrict__ x, long long x_bs, long long x_rs, const int32_t* __restrict__ table,
     const int32_t* __restrict__ pos0, const int32_t* __restrict__ counts,
-    uint8_t* __restrict__ cache, int s, int d, int P, CacheShape cs, long long items,
-    int* status) {
-  const int per_row = d / 8;
-  const long long item = (long long)blockIdx.x * kThreads + threadIdx.x;
-  // items is a multiple of 4 (d % 32 == 0): the four lanes of a group are all in or all out
-  if (item >= items) return;
-  const long long rowi = item / per_row;
-  const int c0 = (int)(item - rowi * per_row) * 8;
-  const int bi = (int)(rowi / s), i = (int)(rowi - (long long)bi * s);
-  const int slot = ring_slot(pos0, counts, bi, i, s, P * cs.page_size, true, status);
-  long long code = 0, scale = 0;
-  const bool live = slot >= 0 &&
-                    cache_row(cs, table + (long long)bi * P, slot, &code, &scale, status);
-  float v[8];
-  if (live) {
-    load8(x + bi * x_bs + i * x_rs + c0, v);
-  } else {
+    uint8_t* __restrict__ cache, int s, int d, int P, CacheShape cs, int* status) {
+  const int tpr = d / 8, rpb = kThreads / tpr;
+  const int rr = (int)threadIdx.x / tpr, c0 = ((int)threadIdx.x - rr * tpr) * 8;
+  const int bi = blockIdx.y, ring = P * cs.page_size;
+  const int i = (int)blockIdx.x * rpb * U + rr;
+  int p0;
+  const int n = range_of(pos0, counts, bi, s, &p0, status);
+  int slot[U], page[U];
+  // of more rows than the ring holds the last are kept
+  slots_of<U>(cs, table + (long long)bi * P, i, rpb, rr < rpb ? max(0, n - ring) : n, n, p0, ring,
+              status, slot, page);
+  float v[U][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+  for (int u = 0; u < U; ++u) {
+    if (slot[u] >= 0) {
+      load8(x + bi * x_bs + (long long)(i + u * rpb) * x_rs + c0, v[u]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
+    }
   }
-  float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
-  const unsigned mask = __activemask();
-  m = fmaxf(m, __shfl_xor_sync(mask, m, 1));
-  m = fmaxf(m, __shfl_xor_sync(mask, m, 2));
-  if (!live) return;
-  const int e = scale_exponent<BITS>(m);
-  const float inv = pow2f(-e);
+  for (int u = 0; u < U; ++u) {
+    float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] *= inv;
-  if constexpr (BITS == 4) {
-    *reinterpret_cast<uint32_t*>(cache + code + c0 / 2) = encode8_e2m1(v);
-  } else {
-    *reinterpret_cast<uint2*>(cache + code + c0) =
-        make_uint2(encode4_e4m3(v[0], v[1], v[2], v[3]), encode4_e4m3(v[4], v[5], v[6], v[7]));
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[u][k]));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if (slot[u] < 0 || page[u] < 0) continue;
+    const int e = scale_exponent<BITS>(m);
+    const float inv = pow2f(-e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[u][k] *= inv;
+    const int row = slot[u] - page_index(cs, slot[u]) * cs.page_size;
+    uint8_t* base = cache + page_base(cs, page[u]);
+    uint8_t* code = base + row_code(cs, row);
+    if constexpr (BITS == 4) {
+      *reinterpret_cast<uint32_t*>(code + c0 / 2) = encode8_e2m1(v[u]);
+    } else {
+      *reinterpret_cast<uint2*>(code + c0) =
+          make_uint2(encode4_e4m3(v[u][0], v[u][1], v[u][2], v[u][3]),
+                     encode4_e4m3(v[u][4], v[u][5], v[u][6], v[u][7]));
+    }
+    if ((c0 & 31) == 0) base[row_scale(cs, row) + c0 / kCacheGroup] = (uint8_t)(e + 127);
   }
-  if ((c0 & 31) == 0) cache[scale + c0 / kCacheGroup] = (uint8_t)(e + 127);
 }
 
-template <typename T, int BITS>
+template <typename T, int BITS, int U>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(
     const uint8_t* __restrict__ cache, const int32_t* __restrict__ table,
     const int32_t* __restrict__ pos0, const int32_t* __restrict__ counts, T* __restrict__ out,
-    long long o_bs, long long o_rs, int s, int d, int P, CacheShape cs, long long items,
-    int* status) {
-  const int per_row = d / 8;
-  const long long item = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (item >= items) return;
-  const long long rowi = item / per_row;
-  const int c0 = (int)(item - rowi * per_row) * 8;
-  const int bi = (int)(rowi / s), i = (int)(rowi - (long long)bi * s);
-  const int slot = ring_slot(pos0, counts, bi, i, s, P * cs.page_size, false, status);
-  if (slot < 0) return;
-  long long code, scale;
-  float v[8];
-  if (cache_row(cs, table + (long long)bi * P, slot, &code, &scale, status)) {
-    cache_load8<BITS>(cache + code, scale_value(cache[scale + c0 / kCacheGroup]), c0, v);
-  } else {
+    long long o_bs, long long o_rs, int s, int d, int P, CacheShape cs, int* status) {
+  const int tpr = d / 8, rpb = kThreads / tpr;
+  const int rr = (int)threadIdx.x / tpr, c0 = ((int)threadIdx.x - rr * tpr) * 8;
+  const int bi = blockIdx.y;
+  const int i = (int)blockIdx.x * rpb * U + rr;
+  int p0;
+  const int n = range_of(pos0, counts, bi, s, &p0, status);
+  int slot[U], page[U];
+  slots_of<U>(cs, table + (long long)bi * P, i, rpb, rr < rpb ? 0 : n, n, p0, P * cs.page_size,
+              status, slot, page);
+  uint2 w[U];
+  uint32_t sc[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+  for (int u = 0; u < U; ++u) {
+    const bool live = slot[u] >= 0 && page[u] >= 0;
+    const int row = slot[u] - page_index(cs, slot[u]) * cs.page_size;
+    const uint8_t* base = cache + page_base(cs, page[u]);
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
+    const uint8_t* code = live ? base + row_code(cs, row) + c0 * BITS / 8 : zero;
+    w[u].y = 0;
+    if constexpr (BITS == 4) w[u].x = __ldg(reinterpret_cast<const uint32_t*>(code));
+    else w[u] = __ldg(reinterpret_cast<const uint2*>(code));
+    sc[u] = __ldg(live ? base + row_scale(cs, row) + c0 / kCacheGroup : zero);
   }
-  store8(out + bi * o_bs + i * o_rs + c0, v);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (slot[u] < 0) continue;
+    T* dst = out + bi * o_bs + (long long)(i + u * rpb) * o_rs + c0;
+    if constexpr (sizeof(T) == 2) {
+      uint32_t o[4];
+      expand8<BITS>(w[u].x, w[u].y, o);
+      scale8<BITS>(sc[u], o);
+      *reinterpret_cast<uint4*>(dst) = natural8<BITS>(o);
+    } else {
+      float v[8];
+      const float f = scale_value(sc[u]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (BITS == 4) v[k] = code_e2m1(w[u].x >> (4 * k)) * f;
+        else v[k] = code_e4m3((k < 4 ? w[u].x : w[u].y) >> (8 * (k & 3))) * f;
+      }
+      store8(dst, v);
+    }
+  }
+}
+
+// Rows of a thread: several once the call fills the GPU with one each.
+inline int rows_per_thread(int b, int s, int d) {
+  const long long rpb = kThreads / (d / 8);
+  return (long long)b * ((s + rpb - 1) / rpb) > 152ll * 16 ? 8 : 1;
+}
+inline dim3 rows_grid(int b, int s, int d, int U) {
+  const int rows = kThreads / (d / 8) * U;
+  return dim3((unsigned)((s + rows - 1) / rows), (unsigned)b);
 }
 
 }  // namespace
@@ -111,12 +177,14 @@ cudaError_t launch_cache_write(const void* x, long long x_bs, long long x_rs, bo
                                void* cache, int b, int s, int d, int P, int n_pages,
                                int page_size, int bits, int* status, cudaStream_t st) {
   const CacheShape cs = cache_shape(page_size, n_pages, d, bits);
-  const long long items = (long long)b * s * (d / 8);
-  const unsigned grid = (unsigned)((items + kThreads - 1) / kThreads);
+  const int u = rows_per_thread(b, s, d) > 1 ? 4 : 1;    // eight rows of fp32 values would spill
+  const dim3 grid = rows_grid(b, s, d, u);
   uint8_t* c = (uint8_t*)cache;
 #define CSA_WRITE(T, B)                                                                          \
-  cache_write_kernel<T, B><<<grid, kThreads, 0, st>>>((const T*)x, x_bs, x_rs, table, pos0,      \
-                                                      counts, c, s, d, P, cs, items, status)
+  (u > 1 ? cache_write_kernel<T, B, 4><<<grid, kThreads, 0, st>>>(                               \
+               (const T*)x, x_bs, x_rs, table, pos0, counts, c, s, d, P, cs, status)             \
+         : cache_write_kernel<T, B, 1><<<grid, kThreads, 0, st>>>(                               \
+               (const T*)x, x_bs, x_rs, table, pos0, counts, c, s, d, P, cs, status))
   if (bf16) {
     if (bits == 4) CSA_WRITE(__nv_bfloat16, 4); else CSA_WRITE(__nv_bfloat16, 8);
   } else {
@@ -132,12 +200,14 @@ cudaError_t launch_cache_read(const void* cache, const int32_t* table, const int
                               bool bf16, int b, int s, int d, int P, int n_pages, int page_size,
                               int bits, int* status, cudaStream_t st) {
   const CacheShape cs = cache_shape(page_size, n_pages, d, bits);
-  const long long items = (long long)b * s * (d / 8);
-  const unsigned grid = (unsigned)((items + kThreads - 1) / kThreads);
+  const int u = rows_per_thread(b, s, d);
+  const dim3 grid = rows_grid(b, s, d, u);
   const uint8_t* c = (const uint8_t*)cache;
 #define CSA_READ(T, B)                                                                           \
-  cache_read_kernel<T, B><<<grid, kThreads, 0, st>>>(c, table, pos0, counts, (T*)out, o_bs,      \
-                                                     o_rs, s, d, P, cs, items, status)
+  (u > 1 ? cache_read_kernel<T, B, 8><<<grid, kThreads, 0, st>>>(                                \
+               c, table, pos0, counts, (T*)out, o_bs, o_rs, s, d, P, cs, status)                 \
+         : cache_read_kernel<T, B, 1><<<grid, kThreads, 0, st>>>(                                \
+               c, table, pos0, counts, (T*)out, o_bs, o_rs, s, d, P, cs, status))
   if (bf16) {
     if (bits == 4) CSA_READ(__nv_bfloat16, 4); else CSA_READ(__nv_bfloat16, 8);
   } else {

@@ -16,6 +16,7 @@
 // tile's largest |k| goes to the select.
 #include "cache_expand.cuh"
 #include "indexer_decode.h"
+#include "smem_once.h"
 #include "tcgen05.cuh"
 
 namespace csa {
@@ -211,8 +212,8 @@ cudaError_t launch(const IndexDecodeArgs& a, int per_group, int hpad, cudaStream
   using C = Cfg<D, NC>;
   const size_t smem = 1024 + C::kBytes;
   auto k = index_scores_tc_kernel<D, NC, BITS>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemOnce once;
+  const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
   const int groups = (a.s_q + per_group - 1) / per_group;
   // CTAs of a sequence: over all sequences twice the four that fit an SM, as

@@ -33,6 +33,7 @@
 #include <cuda_bf16.h>
 
 #include "indexer_decode.h"
+#include "smem_once.h"
 
 namespace csa {
 namespace {
@@ -626,8 +627,8 @@ cudaError_t launch_select_cs(const IndexDecodeArgs& a, cudaStream_t st) {
   cap = cap < kMaxStaged ? cap : kMaxStaged;
   const size_t smem = (size_t)cap * 4 + (size_t)kSelWarps * a.d * sizeof(float);
   auto k = index_select_kernel<T, BITS, CS>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static SmemOnce once;
+  const cudaError_t e = once(k, (size_t)kMaxStaged * 4 + kSelWarps * kMaxDecodeDI * sizeof(float));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.b * a.s_q * CS));

@@ -56,8 +56,8 @@ def load_library():
 
 def _check(t, name, dtype, shape, dev):
     """A contiguous CUDA tensor of this dtype and shape on device dev."""
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.get_device() == dev):
+    if not (t.get_device() == dev and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
         _refuse(t, name, dtype, shape, dev)
 
 
