@@ -110,10 +110,10 @@ __device__ __forceinline__ uint4 natural8(const uint32_t (&o)[4]) {
 template <int BITS, bool NORM = false>
 __device__ __forceinline__ float expand_group(const Codes<BITS>& c, unsigned char* row, int ch0,
                                               int sw) {
-  __nv_bfloat162 sq = __floats2bfloat162_rn(0.f, 0.f);
   const uint32_t words[8] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w,
                              c.w[BITS / 4 - 1].x, c.w[BITS / 4 - 1].y, c.w[BITS / 4 - 1].z,
                              c.w[BITS / 4 - 1].w};
+  __nv_bfloat162 sq = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t o[4];

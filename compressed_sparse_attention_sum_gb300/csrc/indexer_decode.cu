@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(kScoreThreads) index_scores_simt_kernel(
     const IndexDecodeArgs a) {
   extern __shared__ __align__(16) float q_s[];   // [kHeadChunk][d]
   __shared__ int s_scale[kScoreThreads / 32];
+  __shared__ float2 s_range[kScoreThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tile = blockIdx.x, bi = blockIdx.y, tid = threadIdx.x;
   const int d = a.d, j = tile * kIdxTile + tid;
@@ -73,13 +74,22 @@ __global__ void __launch_bounds__(kScoreThreads) index_scores_simt_kernel(
         if (h < nh) total = fmaf(a.w[row * a.H + h0 + h], fmaxf(dot[h], 0.f), total);
     }
     if (j < vis) a.scores[row * a.slots + j] = total;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    for (int k = 1; k < kScoreThreads / 32; ++k) s_scale[0] = max(s_scale[0], s_scale[k]);
-    const float top = scale_value((uint32_t)s_scale[0]) * (BITS == 4 ? 6.f : 448.f);
-    for (int i = 0; i < a.s_q; ++i)
-      a.tile_norm[((long long)bi * a.s_q + i) * a.tiles + tile] = top * sqrtf((float)d) * 1.000001f;
+    float mn = j < vis ? total : INFINITY, mx = j < vis ? total : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = warp_max(mx);
+    if ((tid & 31) == 0) s_range[tid >> 5] = make_float2(mn, mx);
+    __syncthreads();
+    if (tid == 0) {
+      int scale_byte = 0;
+      for (int k = 0; k < kScoreThreads / 32; ++k) {
+        mn = fminf(mn, s_range[k].x);
+        mx = fmaxf(mx, s_range[k].y);
+        scale_byte = max(scale_byte, s_scale[k]);
+      }
+      const float top = scale_value((uint32_t)scale_byte) * (BITS == 4 ? 6.f : 448.f);
+      a.tile_info[row * a.tiles + tile] = make_float4(top * sqrtf((float)d) * 1.000001f, mn, mx, 0.f);
+    }
   }
 }
 

@@ -23,7 +23,7 @@ struct IndexDecodeArgs {
   float* scores;       // [b * s_q][slots]
   double* exact;       // [b * s_q][slots]: exact scores of the row's close candidates
   int32_t* list;       // [b * s_q][slots]: their blocks, ascending
-  float* tile_norm;    // [b * s_q][tiles]: bound on |k_j| of a tile's keys
+  float4* tile_info;   // [b * s_q][tiles]: bound on |k_j| of a tile's keys, its smallest and largest score
   float err;           // bound of a score's error over sum_h |w_h| |q_h| times |k_j|
   int b, s_q, H, d, ratio, topk, P, slots, tiles;
   CacheShape cs;
@@ -56,7 +56,7 @@ inline size_t index_decode_layout(IndexDecodeArgs* a, unsigned char* ws) {
   a->exact = (double*)take(n * sizeof(double));
   a->scores = (float*)take(n * sizeof(float));
   a->list = (int32_t*)take(n * sizeof(int32_t));
-  a->tile_norm = (float*)take(rows * (size_t)a->tiles * sizeof(float));
+  a->tile_info = (float4*)take(rows * (size_t)a->tiles * sizeof(float4));
   return at;
 }
 

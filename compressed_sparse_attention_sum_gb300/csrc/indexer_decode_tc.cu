@@ -7,13 +7,12 @@
 // query, or of several) in shared memory and walks every gridDim.x-th tile of
 // 128 keys.  The codes of the next tile are fetched into registers while the
 // present one is multiplied; a tile is expanded to bf16 once for all heads
-// (exactly, cache_expand.cuh).  A thread then owns a key: it reads its row of
-// S^T from TMEM and adds w_h ReLU(s) over the heads, and a warp stores 32
-// consecutive scores.
+// (exactly, cache_expand.cuh).  Two threads then own a key: each reads half of
+// its row of S^T from TMEM and adds w_h ReLU(s) over those heads.
 //
-// What bounds it: expanding the codes and the weighted ReLU, both on the
-// integer and FMA pipes; four CTAs on an SM hide each other's latency.  The
-// tile's largest |k| goes to the select.
+// What bounds it: expanding the codes and the weighted ReLU, in instructions
+// issued; four CTAs on an SM hide each other's latency.  The
+// tile's largest |k| and its range of scores go to the select.
 #include "cache_expand.cuh"
 #include "indexer_decode.h"
 #include "smem_once.h"
@@ -24,10 +23,19 @@ namespace idt {
 
 using namespace csa::umma;
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;            // two threads a key
 constexpr int kSiteIndex = 0x74;
 constexpr uint32_t kBlk = kIdxTile * 128;
 constexpr float kNormSlack = 1.05f;       // the squares are summed 16 at a time in bf16
+
+// Floats as signed integers of the same order (NaN beyond the infinities), and back.
+__device__ __forceinline__ int float_order(float x) {
+  const int u = __float_as_int(x);
+  return u ^ ((u >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float order_float(int k) {
+  return __int_as_float(k ^ ((k >> 31) & 0x7fffffff));
+}
 
 template <int D, int NC>
 struct Cfg {
@@ -40,12 +48,14 @@ struct Cfg {
   static constexpr uint32_t W = K + (D / 64) * kBlk;     // [NC] head weights
   static constexpr uint32_t BAR = W + NC * 4;
   static constexpr uint32_t MISC = BAR + 8;              // TMEM slot, dead
-  static constexpr uint32_t BND = MISC + 8;              // [4]
-  static constexpr uint32_t kBytes = BND + 16;
+  static constexpr uint32_t BND = MISC + 8;              // [2][8], by tile parity
+  static constexpr uint32_t RNG = BND + 64;              // [NC / 16][4] score ranges of the warps
+  static constexpr uint32_t SUM = RNG + NC / 16 * 32;    // [2][NC / 16][128] sums over half the heads
+  static constexpr uint32_t kBytes = SUM + 2 * (NC / 16) * kIdxTile * 4;
 };
 
 template <int D, int NC, int BITS>
-__global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDecodeArgs a,
+__global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_kernel(const IndexDecodeArgs a,
                                                                    int per_group, int hpad) {
   using C = Cfg<D, NC>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -56,7 +66,8 @@ __global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDe
   uint64_t* bar = reinterpret_cast<uint64_t*>(sm + C::BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
-  float* bnd = reinterpret_cast<float*>(sm + C::BND);
+  int2* rng = reinterpret_cast<int2*>(sm + C::RNG);
+  float* sums = reinterpret_cast<float*>(sm + C::SUM);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int bi = blockIdx.y, i0 = blockIdx.z * per_group;
@@ -108,6 +119,11 @@ __global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDe
   // Q: column c is query c / hpad, head c % hpad; the others are zero
   constexpr int kQChunks = NC * (D / 8) / kThreads;
   uint4 qv[kQChunks];
+  float wv = 0.f;
+  if (tid < NC) {
+    const int qi = tid / hpad, h = tid - qi * hpad;
+    if (qi < nq && h < a.H) wv = __ldg(a.w + (row0 + qi) * a.H + h);
+  }
 #pragma unroll
   for (int x = 0; x < kQChunks; ++x) {
     const int e = tid + x * kThreads, c = e / (D / 8), ch = e - c * (D / 8);
@@ -123,18 +139,16 @@ __global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDe
 #pragma unroll
   for (int x = 0; x < kQChunks; ++x) {
     const int e = tid + x * kThreads, c = e / (D / 8), ch = e - c * (D / 8);
-    *reinterpret_cast<uint4*>(sm + (ch >> 3) * C::kQBlk + c * 128 +
-                              (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(qv[x]);
+    *reinterpret_cast<uint4*>(sm + (ch >> 3) * C::kQBlk + c * 128 + (((ch & 7) ^ (c & 7)) << 4)) =
+        permute8<BITS>(qv[x]);
   }
-  for (int c = tid; c < NC; c += kThreads) {
-    const int qi = c / hpad, h = c - qi * hpad;
-    w_s[c] = qi < nq && h < a.H ? a.w[(row0 + qi) * a.H + h] : 0.f;
-  }
+  if (tid < NC) w_s[tid] = wv;
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+  const int half = warp >> 2, key_t = tid & 127;         // TMEM lane quarter: warp % 4
+  const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
 
   uint32_t parity = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -152,6 +166,8 @@ __global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDe
       norm2 = fmaxf(norm2, s);
     }
     norm2 = warp_max(norm2);
+    // by parity: the tile before is still read after its last barrier
+    float* bnd = reinterpret_cast<float*>(sm + C::BND) + parity * 8;
     if (lane == 0) bnd[warp] = norm2;
     fence_proxy_async_smem();
     fence_before();
@@ -166,38 +182,58 @@ __global__ void __launch_bounds__(kThreads) index_scores_tc_kernel(const IndexDe
                     sw128_desc(qa + (k >> 2) * C::kQBlk + (k & 3) * 32), idesc, k > 0 ? 1u : 0u);
       mma_commit(bar);
     }
-    if (tid < nq)
-      a.tile_norm[(row0 + tid) * a.tiles + tile] =
-          sqrtf(fmaxf(fmaxf(bnd[0], bnd[1]), fmaxf(bnd[2], bnd[3]))) * kNormSlack;
     if (tile + (int)gridDim.x < tiles) {
       fetch_codes(tile + gridDim.x);
       fetch_pages(tile + 2 * gridDim.x);
     }
     if (!mbar_wait(bar, parity)) *dead = 1;
-    parity ^= 1;
     fence_after();
-    // ---- sum_h w_h ReLU(s_h) for this thread's key ------------------------------
-    const int j = tile * kIdxTile + tid;
+    // ---- sum_h w_h ReLU(s_h) for this thread's key, every other 16 heads ---------
 #pragma unroll 1
     for (int q = 0; q < nq; ++q) {
       float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
 #pragma unroll 1
-      for (int c0 = q * hpad; c0 < (q + 1) * hpad; c0 += 16) {
+      for (int c0 = q * hpad + half * 16; c0 < (q + 1) * hpad; c0 += 32) {
         uint32_t v[16];
         tmem_ld16_wait(tmem + lane_base + c0, v);
 #pragma unroll
         for (int c = 0; c < 16; c += 4) {
           const float4 w4 = *reinterpret_cast<const float4*>(w_s + c0 + c);
-          t0 = fmaf(w4.x, fmaxf(__uint_as_float(v[c]), 0.f), t0);
-          t1 = fmaf(w4.y, fmaxf(__uint_as_float(v[c + 1]), 0.f), t1);
-          t2 = fmaf(w4.z, fmaxf(__uint_as_float(v[c + 2]), 0.f), t2);
-          t3 = fmaf(w4.w, fmaxf(__uint_as_float(v[c + 3]), 0.f), t3);
+          fma_f32x2(t0, t1, pack_f32x2(w4.x, w4.y), fmaxf(__uint_as_float(v[c]), 0.f),
+                    fmaxf(__uint_as_float(v[c + 1]), 0.f));
+          fma_f32x2(t2, t3, pack_f32x2(w4.z, w4.w), fmaxf(__uint_as_float(v[c + 2]), 0.f),
+                    fmaxf(__uint_as_float(v[c + 3]), 0.f));
         }
       }
-      if (j < most && !*dead) a.scores[(row0 + q) * a.slots + j] = (t0 + t1) + (t2 + t3);
+      sums[(half * (NC / 16) + q) * kIdxTile + key_t] = (t0 + t1) + (t2 + t3);
     }
     fence_before();
-    __syncthreads();                                     // K, S and bnd are free
+    __syncthreads();                                     // sums; K and S are free
+    const int j = tile * kIdxTile + key_t;
+    for (int q = half; q < nq; q += 2) {
+      const float score = sums[q * kIdxTile + key_t] + sums[(NC / 16 + q) * kIdxTile + key_t];
+      if (j < most && !*dead) a.scores[(row0 + q) * a.slots + j] = score;
+      // the tile's range of scores, as ordered integers
+      const int key = float_order(score);
+      const int mn = __reduce_min_sync(0xffffffffu, j < most ? key : 0x7fffffff);
+      const int mx = __reduce_max_sync(0xffffffffu, j < most ? key : (int)0x80000000);
+      if (lane == 0) rng[q * 4 + (warp & 3)] = make_int2(mn, mx);
+    }
+    __syncthreads();                                     // rng
+    if (tid < nq) {
+      int2 r = rng[tid * 4];
+#pragma unroll
+      for (int k = 1; k < 4; ++k) {
+        r.x = min(r.x, rng[tid * 4 + k].x);
+        r.y = max(r.y, rng[tid * 4 + k].y);
+      }
+      float n2 = bnd[0];
+#pragma unroll
+      for (int k = 1; k < kThreads / 32; ++k) n2 = fmaxf(n2, bnd[k]);
+      a.tile_info[(row0 + tid) * a.tiles + tile] =
+          make_float4(sqrtf(n2) * kNormSlack, order_float(r.x), order_float(r.y), 0.f);
+    }
+    parity ^= 1;
     if (*dead) break;
   }
   if (tid == 0 && *dead) set_status(a.status, kDevTimeout, kSiteIndex);
@@ -216,9 +252,9 @@ cudaError_t launch(const IndexDecodeArgs& a, int per_group, int hpad, cudaStream
   const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
   const int groups = (a.s_q + per_group - 1) / per_group;
-  // CTAs of a sequence: over all sequences twice the four that fit an SM, as
-  // those of shorter sequences find no tile
-  long long g = (8ll * 152 + (long long)a.b * groups - 1) / ((long long)a.b * groups);
+  // CTAs of a sequence: over all sequences half again as many as the four that
+  // fit an SM, as those of shorter sequences find no tile
+  long long g = (6ll * 152 + (long long)a.b * groups - 1) / ((long long)a.b * groups);
   g = g > a.tiles ? a.tiles : g;
   k<<<dim3((unsigned)g, a.b, groups), kThreads, smem, st>>>(a, per_group, hpad);
   count_launches(1);

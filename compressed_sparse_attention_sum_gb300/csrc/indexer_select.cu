@@ -14,21 +14,25 @@
 //     2^-24 where that is 56 2^-24 (128 heads x 128 channels, all terms
 //     positive), 0.1 2^-24 on N(0, 1) inputs.
 // A close block's dot products are accumulated as pairs of fp32 (the rounding
-// error of every addition is itself summed, which leaves about 2^-40) and
-// added over the heads in fp64; the best fill the places that the blocks above
+// error of every addition is itself summed, which leaves about 2^-40), as is
+// their sum over the heads; the best fill the places that the blocks above
 // T + 2 eps leave, ties to the lower block.
 //
-// A cluster of up to eight CTAs takes a row, each a contiguous part of its
-// scores, kept in shared memory as ordered integers.  A histogram of 1024 bins
-// over the range of scores, whose counts the CTAs read from each other, gives
+// A CTA takes a row and keeps its scores in shared memory as ordered integers;
+// long rows take a cluster of up to eight CTAs, each a contiguous part of the
+// scores.  A histogram of 1024 bins over the range of scores (the tiles'
+// ranges come with them), whose counts the CTAs read from each other, gives
 // the bin that T lies in (where outliers leave more than 512 scores in it,
 // histograms over the bits of the keys, four rounds at most, narrow it down).
-// The keys of that bin and of 2 eps around it are gathered in every CTA; T and the close blocks follow from ranks among them.  The heads
-// of the close blocks' exact scores are dealt over the CTAs.  A row with more than 512 keys there (ties) is
+// The keys of that bin and of 2 eps around it are gathered in every CTA; T and
+// the close blocks follow from ranks among them.  The heads of the close
+// blocks' exact scores are dealt over the CTAs.  The blocks above set bits of a
+// map as they are passed, the close ones that are chosen theirs; the map gives
+// the ascending list.  A row with more than 512 keys around T (ties) is
 // finished by the first CTA alone, by radix selects over global lists.
-// Latency bounds it: cluster barriers, reads of the other CTAs' shared memory
-// (all of a step are in flight at once) and the chain of dependent additions of
-// a dot product (d_I / 4 long: four threads share a head).
+// Latency bounds it: barriers, dependent reads, reads of the other CTAs' shared
+// memory (all of a step are in flight at once) and the chain of dependent
+// additions of a dot product (d_I / 4 long: four threads share a head).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -40,14 +44,14 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSel = 512;            // threads of a CTA
+constexpr int kSel = 1024;           // threads of a CTA
 constexpr int kSelWarps = kSel / 32;
-constexpr int kBins = 2 * kSel;
+constexpr int kBins = kSel;          // one a thread
 constexpr int kBinBits = 10;
 constexpr int kNarrow = 256;         // keys of the bin around T
-constexpr int kList = kSel;          // keys around T that are ranked directly: one a thread
+constexpr int kList = 512;           // keys around T that are ranked directly
 constexpr int kMaxCluster = 8;
-constexpr int kMaxStaged = 40960;    // scores a CTA keeps in shared memory
+constexpr int kMaxStaged = 32768;    // scores a CTA keeps in shared memory
 
 // Unsigned keys in the order of the floats they come from (-0 as +0).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -68,12 +72,12 @@ struct __align__(16) SelShared {
   uint32_t list_key[kList];
   int list_j[kList];
   float2 exact[kList];               // close blocks' exact scores over this CTA's heads
-  uint32_t range[2];                 // smallest and largest key of this part
   int n[2];                          // keys in the list, keys above it
   // this CTA's own
-  uint32_t all_key[kList];
+  alignas(16) uint32_t all_key[kList];   // read four at a time
   int all_j[kList];
   int close_j[kList];
+  int close_page[kList];
   unsigned long long all_exact[kList];
   int warp_n[kSelWarps];
   int warp_m[kSelWarps];
@@ -95,12 +99,13 @@ __device__ __forceinline__ const V* peer(V* p, int rank) {
   else return p;
 }
 
+static_assert(kSelWarps == 32, "a warp's lanes hold the warps' counts");
+
 __device__ __forceinline__ int block_count(SelShared& sh, int c) {
   c = __reduce_add_sync(0xffffffffu, c);
   if ((threadIdx.x & 31) == 0) sh.warp_n[threadIdx.x >> 5] = c;
   __syncthreads();
-  int t = 0;
-  for (int k = 0; k < kSelWarps; ++k) t += sh.warp_n[k];
+  const int t = __reduce_add_sync(0xffffffffu, sh.warp_n[threadIdx.x & 31]);
   __syncthreads();
   return t;
 }
@@ -152,59 +157,84 @@ __device__ __forceinline__ unsigned long long pair_key(float2 a) {
   return order_key((double)a.x + (double)a.y);
 }
 
-// Part `part` of four of the dot product of q and k over d channels: a product
-// is split by an fma (exact already for bf16 q), a sum by the exact error of an
-// addition.
+// The dot product of n channels of q and k: a product is split by an fma (exact
+// already for bf16 q), a sum by the exact error of an addition.  The first four
+// 16-byte words of q come in registers, read ahead of the keys.
+constexpr int kQAhead = 4;
 template <typename T>
-__device__ __forceinline__ float2 dot_pair(const T* q, const float* k, int d, int part) {
+__device__ __forceinline__ float2 dot_pair(const uint4 (&ahead)[kQAhead], const T* q,
+                                           const float* k, int n) {
   float hi = 0.f, lo = 0.f;
-  const int c1 = (part + 1) * (d / 4);
-  for (int c0 = part * (d / 4); c0 < c1; c0 += 8) {
-    float qv[8];
-    load8(q + c0, qv);
-    const float4 k0 = *reinterpret_cast<const float4*>(k + c0);
-    const float4 k1 = *reinterpret_cast<const float4*>(k + c0 + 4);
-    const float kv[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+  constexpr int kPer = 16 / sizeof(T);
+  auto add = [&](uint4 u, const float* kc) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float kv[kPer];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float p = __fmul_rn(qv[e], kv[e]);
-      if (sizeof(T) == 4) lo += __fmaf_rn(qv[e], kv[e], -p);
+    for (int e = 0; e < kPer; e += 4)
+      *reinterpret_cast<float4*>(kv + e) = *reinterpret_cast<const float4*>(kc + e);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      float qv;
+      if constexpr (sizeof(T) == 2)
+        qv = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+      else
+        qv = __uint_as_float(w[e]);
+      const float p = __fmul_rn(qv, kv[e]);
+      if (sizeof(T) == 4) lo += __fmaf_rn(qv, kv[e], -p);
       const float s = __fadd_rn(hi, p), t = __fsub_rn(s, hi);
       lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t));
       hi = s;
     }
-  }
+  };
+#pragma unroll
+  for (int c = 0; c < kQAhead; ++c)
+    if (c * kPer < n) add(ahead[c], k + c * kPer);
+#pragma unroll 1
+  for (int c = kQAhead; c * kPer < n; ++c)
+    add(reinterpret_cast<const uint4*>(q)[c], k + c * kPer);
   return pair_add(make_float2(hi, 0.f), make_float2(lo, 0.f));
 }
 
 // Sums over the heads [h0, h0 + nh) of the exact scores of blocks block(0) ..
-// block(m - 1), each given to store(e, sum).  Four threads a (block, head);
-// scratch k_s holds the dequantised keys of a round (up to 16 of them).  Called
-// by the whole CTA.
-template <typename T, int BITS, typename B, typename S>
-__device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long row, int bi,
-                            float* k_s, int m, int h0, int nh, B block, S store) {
+// block(m - 1) on pages page(0) .. page(m - 1), each given to store(e, sum).
+// Four threads a (block, head); scratch k_s holds the dequantised keys of a
+// round (up to 32 of them).  Called by the whole CTA.
+template <typename T, int BITS, typename B, typename P, typename S>
+__device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long row, float* k_s,
+                            int m, int h0, int nh, B block, P page, S store) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const T* q = (const T*)a.q + (row * a.H + h0) * a.d;
-  const int32_t* pages = a.table + (long long)bi * a.P;
   const int wpb = max(1, (nh + 7) / 8);                  // warps of a block
   const int per = kSelWarps / wpb;
   const int mine = warp / wpb, h = (warp - mine * wpb) * 8 + (lane >> 2), part = lane & 3;
-  const float w = h < nh ? a.w[row * a.H + h0 + h] : 0.f;
+  const int n4 = a.d / 4, pitch = a.d + 16;
+  const T* qh = (const T*)a.q + (row * a.H + h0 + min(h, max(nh - 1, 0))) * a.d + part * n4;
+  uint4 ahead[kQAhead];
+  float w = 0.f;
+  if (h < nh) {
+#pragma unroll
+    for (int c = 0; c < kQAhead; ++c)
+      ahead[c] = reinterpret_cast<const uint4*>(qh)[c * (16 / (int)sizeof(T)) < n4 ? c : 0];
+    w = a.w[row * a.H + h0 + h];
+  }
   for (int e0 = 0; e0 < m; e0 += per) {
     const int n = min(per, m - e0);
     for (int x = tid; x < n * (a.d / 8); x += kSel) {
       const int s = x / (a.d / 8), c0 = (x - s * (a.d / 8)) * 8;
-      long long code, scale;
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (cache_row(a.cs, pages, block(e0 + s), &code, &scale, a.status))
-        cache_load8<BITS>(a.cache + code, scale_value(a.cache[scale + c0 / 32]), c0, v);
-      store8(k_s + s * a.d + c0, v);
+      const int j = block(e0 + s), pg = page(e0 + s);
+      if ((unsigned)pg < (unsigned)a.cs.n_pages) {       // recorded by the score kernel
+        const int r = j - page_index(a.cs, j) * a.cs.page_size;
+        const uint8_t* base = a.cache + page_base(a.cs, pg);
+        cache_load8<BITS>(base + row_code(a.cs, r), scale_value(base[row_scale(a.cs, r) + c0 / 32]),
+                          c0, v);
+      }
+      // quarters four banks apart: the lanes of a head read all four at once
+      store8(k_s + s * pitch + c0 + c0 / n4 * 4, v);
     }
     __syncthreads();
     if (mine < n) {                                      // warp-uniform
       float2 x = make_float2(0.f, 0.f);
-      if (h < nh) x = dot_pair(q + h * a.d, k_s + mine * a.d, a.d, part);
+      if (h < nh) x = dot_pair<T>(ahead, qh, k_s + mine * pitch + part * (n4 + 4), n4);
       x = pair_add(x, pair_shfl(x, 1));
       x = pair_add(x, pair_shfl(x, 2));
       x = x.x > 0.f ? pair_mul(x, w) : make_float2(0.f, 0.f);   // hi carries the sum's sign
@@ -213,10 +243,11 @@ __device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long r
       if (lane == 0) sh.pair[warp] = x;
     }
     __syncthreads();
-    if (tid < n) {
-      float2 x = sh.pair[tid * wpb];
-      for (int k = 1; k < wpb; ++k) x = pair_add(x, sh.pair[tid * wpb + k]);
-      store(e0 + tid, x);
+    if (warp < n) {                                      // block `warp` of the round
+      float2 x = lane < wpb ? sh.pair[warp * wpb + lane] : make_float2(0.f, 0.f);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) x = pair_add(x, pair_shfl(x, o));
+      if (lane == 0) store(e0 + warp, x);
     }
     __syncthreads();
   }
@@ -293,12 +324,14 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ SelShared sh;
   uint32_t* staged = reinterpret_cast<uint32_t*>(dyn);
-  float* k_s = reinterpret_cast<float*>(dyn + (size_t)staged_cap * 4);
+  uint32_t* bitmap = staged + staged_cap;
+  float* k_s = reinterpret_cast<float*>(bitmap + staged_cap / 32);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = CS > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const long long row = blockIdx.x / CS;
   const int bi = (int)(row / a.s_q), i = (int)(row - (long long)bi * a.s_q);
   const int vis = index_vis(a, bi, i), K = a.topk;
+  const int32_t* pages = a.table + (long long)bi * a.P;
   int32_t* out = a.out + row * K;
   if (vis <= K) {                                        // every block, whatever the scores
     for (int k = rank * kSel + tid; k < K; k += CS * kSel) out[k] = k < vis ? k : -1;
@@ -329,57 +362,37 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   if (lane == 0) sh.part[warp] = aw;
   for (int e = tid; e < kBins; e += kSel) sh.hist[0][e] = 0;
   __syncthreads();
-  aw = 0.f;
-  for (int k = 0; k < kSelWarps; ++k) aw += sh.part[k];
+  aw = warp_sum(sh.part[lane]);
   __syncthreads();
 
   asm volatile("griddepcontrol.wait;" ::: "memory");     // the scores
 
-  const int seg = (vis + CS - 1) / CS;
+  const int seg = ((vis + CS - 1) / CS + 31) / 32 * 32;  // whole words of the bitmap
   const int j0 = min(rank * seg, vis), n = min(seg, vis - j0);
   float* score = a.scores + row * a.slots;
   const bool is_staged = seg <= staged_cap;              // the same in every CTA
-  uint32_t lo = 0xffffffffu, hi = 0u;
-  const float* norms = a.tile_norm + row * a.tiles;
-  float kmax = tid * kIdxTile < vis ? norms[tid] : 0.f;  // in flight with the scores
-#pragma unroll 4
-  for (int j = tid; j < n; j += kSel) {
-    const uint32_t k = order_key(score[j0 + j]);
-    if (is_staged) staged[j] = k;
-    lo = min(lo, k);
-    hi = max(hi, k);
+  // chosen blocks of this part, a bit each
+  uint32_t* bits = is_staged ? bitmap : reinterpret_cast<uint32_t*>(a.list + row * a.slots) + j0 / 32;
+  float kmax = 0.f, mn = INFINITY, mx = -INFINITY;
+  for (int t = tid; t * kIdxTile < vis; t += kSel) {
+    const float4 v = a.tile_info[row * a.tiles + t];
+    kmax = fmaxf(kmax, v.x);
+    mn = fminf(mn, v.y);
+    mx = fmaxf(mx, v.z);
   }
-  for (int t = tid + kSel; t * kIdxTile < vis; t += kSel) kmax = fmaxf(kmax, norms[t]);
   kmax = warp_max(kmax);
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
+  mn = -warp_max(-mn);
+  mx = warp_max(mx);
   if (lane == 0) {
     sh.part[warp] = kmax;
-    sh.warp_n[warp] = (int)lo;
-    sh.warp_m[warp] = (int)hi;
+    sh.pair[warp] = make_float2(mn, mx);
   }
   __syncthreads();
-  kmax = 0.f;
-  for (int k = 0; k < kSelWarps; ++k) {
-    kmax = fmaxf(kmax, sh.part[k]);
-    lo = min(lo, (uint32_t)sh.warp_n[k]);
-    hi = max(hi, (uint32_t)sh.warp_m[k]);
-  }
-  if (CS > 1) {
-    if (tid == 0) {
-      sh.range[0] = lo;
-      sh.range[1] = hi;
-    }
-    cluster_sync<CS>();
-#pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      const uint32_t* p = peer<CS>(sh.range, r);
-      lo = min(lo, p[0]);
-      hi = max(hi, p[1]);
-    }
-  } else {
-    __syncthreads();
-  }
+  kmax = warp_max(sh.part[lane]);
+  mn = -warp_max(-sh.pair[lane].x);
+  mx = warp_max(sh.pair[lane].y);
+  const uint32_t lo0 = order_key(mn), hi0 = order_key(mx);
+  uint32_t lo = lo0, hi = hi0;
   auto key = [&](int j) { return is_staged ? staged[j] : order_key(score[j0 + j]); };
   const float eps2 = 2.f * a.err * aw * kmax;
 
@@ -389,21 +402,15 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   int buf = 0;
   auto find_bin = [&](int k) {
     cluster_sync<CS>();
-    // bins from the top: thread t holds two of them, of all CTAs
-    const int b0 = kBins - 2 - 2 * tid;
-    int2 c = make_int2(0, 0), pc[CS];
+    // bins from the top: thread t holds one, of all CTAs
+    const int bin = kBins - 1 - tid;
+    int c = 0, pc[CS];
 #pragma unroll
-    for (int r = 0; r < CS; ++r)
-      pc[r] = *reinterpret_cast<const int2*>(peer<CS>(sh.hist[buf], r) + b0);
+    for (int r = 0; r < CS; ++r) pc[r] = peer<CS>(sh.hist[buf], r)[bin];
 #pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      c.x += pc[r].x;
-      c.y += pc[r].y;
-    }
-    // the other histogram was last read before this barrier
-    *reinterpret_cast<int2*>(sh.hist[buf ^ 1] + b0) = make_int2(0, 0);
-    const int sum = c.x + c.y;
-    int before = sum;
+    for (int r = 0; r < CS; ++r) c += pc[r];
+    sh.hist[buf ^ 1][bin] = 0;         // last read before this barrier
+    int before = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, before, o);
@@ -411,35 +418,46 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     }
     if (lane == 31) sh.warp_n[warp] = before;
     __syncthreads();
-    for (int v = 0; v < warp; ++v) before += sh.warp_n[v];
-    before -= sum;
-    if (before < k && before + sum >= k) {               // exactly one thread
-      const bool second = before + c.y < k;
-      sh.bin = second ? b0 : b0 + 1;
-      sh.above = second ? before + c.y : before;
-      sh.in_bin = second ? c.x : c.y;
+    int base = lane < warp ? sh.warp_n[lane] : 0;
+    base = __reduce_add_sync(0xffffffffu, base);
+    before += base - c;
+    if (before < k && before + c >= k) {                 // exactly one thread
+      sh.bin = bin;
+      sh.above = before;
+      sh.in_bin = c;
     }
     __syncthreads();
     buf ^= 1;
   };
-  // First by value, 1024 bins between the smallest and largest score.  The bin
-  // is then widened by what rounding may have moved a score across its edge.
-  const uint32_t lo0 = lo, hi0 = hi;
-  bool by_value = false;
-  if (vis > kNarrow && lo < hi) {
-    const float mn = order_value(lo), mx = order_value(hi), range = mx - mn;
-    const float inv = (float)kBins / range;
-    if (range < 3e38f && inv < 3e38f && inv > 0.f) {     // finite, not NaN
-      int* hist = sh.hist[buf];
-#pragma unroll 4
-      for (int j = tid; j < n; j += kSel)
-        atomicAdd(&hist[min((int)((order_value(key(j)) - mn) * inv), kBins - 1)], 1);
-      find_bin(K);
-      const float w = range / (float)kBins, slack = 0.01f * w + fmaxf(fabsf(mn), fabsf(mx)) * 0x1p-21f;
-      lo = max(lo0, order_key(mn + (float)sh.bin * w - slack));
-      hi = sh.bin == kBins - 1 ? hi0 : min(hi0, order_key(mn + (float)(sh.bin + 1) * w + slack));
-      by_value = true;
+  // First by value, 1024 bins between the smallest and largest score, counted
+  // as the scores are read.  The bin is then widened by what rounding may have
+  // moved a score across its edge.
+  const float range = mx - mn, inv = (float)kBins / range;
+  const bool by_range = vis > kNarrow && range < 3e38f && inv < 3e38f && inv > 0.f;   // finite, not NaN
+  bool by_value = by_range;
+  for (int jb = 0; jb < n; jb += 8 * kSel) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = jb + e * kSel + tid;
+      v[e] = j < n ? score[j0 + j] : 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = jb + e * kSel + tid;
+      if (j < n) {
+        if (is_staged) staged[j] = order_key(v[e]);
+        if (by_range) atomicAdd(&sh.hist[0][max(0, min((int)((v[e] - mn) * inv), kBins - 1))], 1);
+      }
+    }
+  }
+  if (by_value) {
+    find_bin(K);
+    const float w = range / (float)kBins, slack = 0.01f * w + fmaxf(fabsf(mn), fabsf(mx)) * 0x1p-21f;
+    if (sh.bin > 0) lo = max(lo0, order_key(mn + (float)sh.bin * w - slack));
+    if (sh.bin < kBins - 1) hi = min(hi0, order_key(mn + (float)(sh.bin + 1) * w + slack));
+  } else {
+    __syncthreads();
   }
   int k = K, in_range = vis;
   int m = 0, above = 0, before_me = 0;
@@ -467,10 +485,15 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     __syncthreads();
     int c = 0;
 #pragma unroll 4
-    for (int j = tid; j < n; j += kSel) {
-      const uint32_t x = key(j);
-      c += x > list_hi;
-      if (x >= list_lo && x <= list_hi) {
+    for (int jw = warp * 32; jw < n; jw += kSel) {
+      const int j = jw + lane;
+      const uint32_t x = j < n ? key(j) : 0u;
+      const unsigned word = __ballot_sync(0xffffffffu, j < n && x > list_hi);
+      if (lane == 0) {
+        bits[jw / 32] = word;
+        c += __popc(word);
+      }
+      if (j < n && x >= list_lo && x <= list_hi) {
         const int at = atomicAdd(&sh.n[0], 1);
         if (at < kList) {
           sh.list_key[at] = x;
@@ -497,8 +520,10 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
       if (r < rank) before_me += pn[r].y;
     }
     if (m <= kList) {
-      sh.all_key[tid] = from >= 0 ? peer<CS>(sh.list_key, max(from, 0))[at] : 0u;
-      sh.all_j[tid] = from >= 0 ? peer<CS>(sh.list_j, max(from, 0))[at] : -1;
+      if (tid < kList) {
+        sh.all_key[tid] = from >= 0 ? peer<CS>(sh.list_key, max(from, 0))[at] : 0u;
+        sh.all_j[tid] = from >= 0 ? peer<CS>(sh.list_j, max(from, 0))[at] : -1;
+      }
       __syncthreads();
       break;
     }
@@ -515,10 +540,11 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
 
   if (m <= kList) {
     // ---- T by rank, then the close blocks ----------------------------------------
-    const uint32_t x = sh.all_key[tid];
-    const int j = sh.all_j[tid];
-    int gt = 0, eq = 0;
+    const uint32_t x = sh.all_key[tid & (kList - 1)];
+    const int j = sh.all_j[tid & (kList - 1)];             // of the threads below m
+    int gt = 0, eq = 0, page = 0;
     if (tid < m) {
+      page = __ldg(pages + page_index(a.cs, j));           // in flight during the ranking
       count_keys(sh, m, x, &gt, &eq);
       if (above + gt < K && above + gt + eq >= K) sh.tkey = x;
     }
@@ -533,21 +559,22 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
       sh.warp_m[warp] = __popc(cm);
     }
     __syncthreads();
-    int need = K - above, mc = 0, place = 0;
-    for (int v = 0; v < kSelWarps; ++v) {
-      need -= sh.warp_n[v];
-      if (v < warp) place += sh.warp_m[v];
-      mc += sh.warp_m[v];
+    const int need = K - above - __reduce_add_sync(0xffffffffu, sh.warp_n[lane]);
+    const int mc = __reduce_add_sync(0xffffffffu, sh.warp_m[lane]);
+    const int place = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_m[lane] : 0) +
+                      __popc(cm & ((1u << lane) - 1u));
+    if (close) {
+      sh.close_j[place] = j;
+      sh.close_page[place] = page;
     }
-    place += __popc(cm & ((1u << lane) - 1u));
-    if (close) sh.close_j[place] = j;
     __syncthreads();
     bool in = sure;
     if (need < mc && eps2 > 0.f) {
       // every CTA scores all close blocks over its share of the heads
       const int share = (a.H + CS - 1) / CS, h0 = min(rank * share, a.H);
-      score_exact<T, BITS>(sh, a, row, bi, k_s, mc, h0, min(share, a.H - h0),
+      score_exact<T, BITS>(sh, a, row, k_s, mc, h0, min(share, a.H - h0),
                            [&](int e) { return sh.close_j[e]; },
+                           [&](int e) { return sh.close_page[e]; },
                            [&](int e, float2 v) { sh.exact[e] = v; });
       cluster_sync<CS>();
       if (tid < mc) {
@@ -574,15 +601,27 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     }
     // this CTA's place: behind the chosen blocks of the parts before it
     before_me += block_count(sh, in && j < j0 ? 1 : 0);
-    // the list's blocks of this part: chosen ones as the largest key, the others as the smallest
-    if (tid < m && j >= j0 && j < j0 + n) {
-      if (is_staged) staged[j - j0] = in ? 0xffffffffu : 0u;
-      else score[j] = in ? INFINITY : -INFINITY;
-    }
-    if (list_hi == 0xffffffffu) list_hi = 0xfffffffeu;
+    if (in && j >= j0 && j < j0 + n) atomicOr(&bits[(j - j0) / 32], 1u << (j & 31));
     __syncthreads();
-    compact(sh, n, [&](int y) { return key(y) > list_hi; },
-            [&](int y, int pos) { if (before_me + pos < K) out[before_me + pos] = j0 + y; });
+    // the chosen blocks in ascending order, a word of the bitmap a thread
+    for (int w0 = 0; w0 * 32 < n; w0 += kSel) {
+      const int wi = w0 + tid;
+      uint32_t mask = wi * 32 < n ? bits[wi] : 0u;
+      const int c = __popc(mask);
+      int at = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += v;
+      }
+      if (lane == 31) sh.warp_n[warp] = at;
+      __syncthreads();
+      at += before_me - c + __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_n[lane] : 0);
+      for (; mask != 0; mask &= mask - 1, ++at)
+        if (at < K) out[at] = j0 + wi * 32 + __ffs(mask) - 1;
+      before_me += __reduce_add_sync(0xffffffffu, sh.warp_n[lane]);
+      __syncthreads();
+    }
     cluster_sync<CS>();                                  // no CTA leaves while another reads it
     return;
   }
@@ -601,7 +640,8 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
           [&](int j, int at) { list[at] = j; });
   if (need < m && eps2 > 0.f) {
     double* ex = a.exact + row * a.slots;
-    score_exact<T, BITS>(sh, a, row, bi, k_s, m, 0, a.H, [&](int e) { return list[e]; },
+    score_exact<T, BITS>(sh, a, row, k_s, m, 0, a.H, [&](int e) { return list[e]; },
+                         [&](int e) { return pages[page_index(a.cs, list[e])]; },
                          [&](int e, float2 v) { ex[e] = (double)v.x + (double)v.y; });
     int eq = 0;
     const unsigned long long bar =
@@ -623,12 +663,12 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
 
 template <typename T, int BITS, int CS>
 cudaError_t launch_select_cs(const IndexDecodeArgs& a, cudaStream_t st) {
-  int cap = ((a.slots + CS - 1) / CS + 3) / 4 * 4;
+  int cap = ((a.slots + CS - 1) / CS + 127) / 128 * 128;
   cap = cap < kMaxStaged ? cap : kMaxStaged;
-  const size_t smem = (size_t)cap * 4 + (size_t)kSelWarps * a.d * sizeof(float);
+  const size_t smem = (size_t)cap * 4 + cap / 8 + (size_t)kSelWarps * (a.d + 16) * sizeof(float);
   auto k = index_select_kernel<T, BITS, CS>;
   static SmemOnce once;
-  const cudaError_t e = once(k, (size_t)kMaxStaged * 4 + kSelWarps * kMaxDecodeDI * sizeof(float));
+  const cudaError_t e = once(k, (size_t)kMaxStaged * 4 + kMaxStaged / 8 + kSelWarps * (kMaxDecodeDI + 16) * sizeof(float));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.b * a.s_q * CS));
@@ -648,13 +688,16 @@ cudaError_t launch_select_cs(const IndexDecodeArgs& a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k, a, cap);
 }
 
-// CTAs of a row: one for every 256 slots, up to eight, as long as the rows
-// together leave SMs for them.
+// CTAs of a row, up to eight: one for every 32768 slots, and where SMs are left
+// one for every 8192 (a cluster barrier costs about as much as passing over
+// 8192 scores).
 template <typename T, int BITS>
 cudaError_t launch_select(const IndexDecodeArgs& a, cudaStream_t st) {
-  const long long rows = (long long)a.b * a.s_q;
   int cs = 1;
-  while (cs < kMaxCluster && a.slots > cs * 256 && rows * cs * 2 <= 152) cs *= 2;
+  const long long rows = (long long)a.b * a.s_q;
+  while (cs < kMaxCluster &&
+         (a.slots > cs * kMaxStaged || (a.slots > cs * 8192 && rows * cs * 2 <= 152)))
+    cs *= 2;
   switch (cs) {
     case 1: return launch_select_cs<T, BITS, 1>(a, st);
     case 2: return launch_select_cs<T, BITS, 2>(a, st);
