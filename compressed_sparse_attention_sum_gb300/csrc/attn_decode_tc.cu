@@ -55,6 +55,8 @@ struct Cfg {
   static constexpr int kThreads = kCompute + 32;           // one more warp issues the MMAs
   static constexpr int kBlocks = D < 128 ? 2 : D / 64;     // 64-channel blocks of the KV tile
   static constexpr int kMT = D < 128 ? 1 : D / 128;        // M tiles of O^T
+  static constexpr int kPart = kMT < 2 ? 1 : 2;            // M tiles whose channels are handed over at once
+  static constexpr int kParts = kMT / kPart;
   static constexpr int kGroups = D < 128 ? D / 32 : 4;     // scale groups of a row in one M tile
   static constexpr int kLanes = 8 * kGroups;               // lanes of eight slots
   static constexpr int kPerWarp = 8 * (32 / kLanes);       // slots a warp converts at once
@@ -67,8 +69,8 @@ struct Cfg {
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t KV = (D / 64) * kQBlk;
   static constexpr uint32_t P = KV + kBlocks * kKvBlk;
-  static constexpr uint32_t BARS = P + kSlots * 128;       // s, p, kv[kMT], o[kMT]
-  static constexpr uint32_t MISC = BARS + (2 + 2 * kMT) * 8;   // TMEM slot, dead
+  static constexpr uint32_t BARS = P + kSlots * 128;       // s, p, kv[kParts], o[kParts]
+  static constexpr uint32_t MISC = BARS + (2 + 2 * kParts) * 8;   // TMEM slot, dead
   static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][4][NC] column maxima
   static constexpr uint32_t MRUN = RED + 8 * NC * 4;       // [2][NC]
   static constexpr uint32_t ML = MRUN + 2 * NC * 4;        // [NC] (maximum, sum) of this CTA
@@ -183,7 +185,7 @@ __device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned c
 
 template <int D, int NC, int BITS>
 __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC)) attn_decode_tc_kernel(
-    const AttnDecodeArgs a, int per_group, int groups, int head_groups, int cs) {
+    const AttnDecodeArgs a, int per_group, int groups, int head_groups, int cs, int splits) {
   using C = Cfg<D, NC>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
   uint64_t* bar_s = reinterpret_cast<uint64_t*>(sm + C::BARS);
   uint64_t* bar_p = bar_s + 1;
   uint64_t* bar_kv = bar_s + 2;
-  uint64_t* bar_o = bar_kv + C::kMT;
+  uint64_t* bar_o = bar_kv + C::kParts;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
   float* red = reinterpret_cast<float*>(sm + C::RED);
@@ -201,11 +203,11 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
   unsigned char* oks = sm + C::OKS;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // blockIdx.x: part of the slots (the cs CTAs of a cluster are neighbours);
-  // blockIdx.y: group of queries (per_group of one sequence) and of heads
-  const int split = blockIdx.x, rank = split % cs;
-  const int hg = (int)blockIdx.y % head_groups;
-  const int qg = (int)blockIdx.y / head_groups;
+  // blockIdx.x: group of queries (per_group of one sequence) and of heads, and
+  // its split of the slots (the cs CTAs of a cluster are neighbours)
+  const int group = (int)blockIdx.x / splits, split = (int)blockIdx.x - group * splits;
+  const int rank = split % cs;
+  const int hg = group % head_groups, qg = group / head_groups;
   const int bi = qg / groups, i0 = (qg - bi * groups) * per_group;
   const int nq = min(per_group, a.s_q - i0);
   const int h0 = hg * NC, heads = min(a.H - h0, per_group > 1 ? a.H : NC);   // heads of a query
@@ -220,13 +222,13 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
   const int ring0 = w0 >= 0 ? w0 % ring : ring - 1 - (int)((unsigned)(-1 - w0) % (unsigned)ring);
   const int slots = last.t < 0 ? 0 : wext + (a.idx != nullptr ? a.K : last.vis);
   const int tiles = (slots + kSlots - 1) / kSlots;
-  const int it0 = (int)((long long)tiles * split / (int)gridDim.x);
-  const int n = (int)((long long)tiles * (split + 1) / (int)gridDim.x) - it0;
+  const int it0 = (int)((long long)tiles * split / splits);
+  const int n = (int)((long long)tiles * (split + 1) / splits) - it0;
 
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_p, C::kWarps);
-    for (int m = 0; m < C::kMT; ++m) {
+    for (int m = 0; m < C::kParts; ++m) {
       mbar_init(&bar_kv[m], C::kWarps);
       mbar_init(&bar_o[m], 1);
     }
@@ -367,12 +369,12 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
       constexpr int kSteps = D < 128 ? D / 16 : 8;        // K steps of S^T in one M tile
       for (int it = 0; it < n; ++it) {
 #pragma unroll 1
-        for (int m = 0; m < C::kMT; ++m) {
-          if (!wait(&bar_kv[m], it & 1)) break;
+        for (int x = 0; x < C::kParts; ++x) {
+          if (!wait(&bar_kv[x], it & 1)) break;
           fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kSteps; ++kk) {
-            const int k = m * 8 + kk;
+          for (int kk = 0; kk < kSteps * C::kPart; ++kk) {
+            const int k = x * 8 * C::kPart + kk;
             mma_bf16_ss(tmem, sw128_desc(kva + (k >> 2) * kKvBlk + (k & 3) * 32),
                         sw128_desc(qa + (k >> 2) * C::kQBlk + (k & 3) * 32), idesc_s,
                         k > 0 ? 1u : 0u);
@@ -383,12 +385,17 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
         if (!wait(bar_p, it & 1)) break;
         fence_after();
 #pragma unroll 1
-        for (int m = 0; m < C::kMT; ++m) {
+        for (int x = 0; x < C::kParts; ++x) {
 #pragma unroll
-          for (int k = 0; k < kSlots / 16; ++k)
-            mma_bf16_ss(tmem + C::kColO + m * NC, sw128_desc_mn(kva + 2 * m * kKvBlk + k * 2048, kKvBlk),
-                        sw128_desc_mn(pa + k * 2048, kKvBlk), idesc_o, (it > 0 || k > 0) ? 1u : 0u);
-          mma_commit(&bar_o[m]);
+          for (int mm = 0; mm < C::kPart; ++mm) {
+            const int m = x * C::kPart + mm;
+#pragma unroll
+            for (int k = 0; k < kSlots / 16; ++k)
+              mma_bf16_ss(tmem + C::kColO + m * NC,
+                          sw128_desc_mn(kva + 2 * m * kKvBlk + k * 2048, kKvBlk),
+                          sw128_desc_mn(pa + k * 2048, kKvBlk), idesc_o, (it > 0 || k > 0) ? 1u : 0u);
+          }
+          mma_commit(&bar_o[x]);
         }
       }
     }
@@ -408,23 +415,28 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    // Expands the fetched codes of tile it into the KV buffer; M tile m's
-    // channels are free once O^T of the tile before has read them.
+    // Expands the fetched codes of tile it into the KV buffer, two M tiles at a
+    // time; their channels are free once O^T of the tile before has read them.
     auto convert = [&](int it) {
 #pragma unroll
-      for (int m = 0; m < C::kMT; ++m) {
-        if (it > 0) wait(&bar_o[m], (it - 1) & 1);
+      for (int x = 0; x < C::kParts; ++x) {
+        if (it > 0) wait(&bar_o[x], (it - 1) & 1);
 #pragma unroll
-        for (int k = 0; k < C::kSpt; ++k) {
-          const int s = cslot + k * C::kPass;
-          if (s >= kSlots) continue;
-          Codes<BITS> c = cd[k * C::kMT + m];
-          c.scale = (c.scale >> (8 * cgr)) & 255u;
-          unsigned char* dst = sm + C::KV + (uint32_t)(m * 2 + (cgr >> 1)) * kKvBlk + s * 128;
-          expand_group<BITS>(c, dst, (cgr & 1) * 4, s & 7);
+        for (int mm = 0; mm < C::kPart; ++mm) {
+          const int m = x * C::kPart + mm;
+#pragma unroll
+          for (int k = 0; k < C::kSpt; ++k) {
+            const int s = cslot + k * C::kPass;
+            if (s >= kSlots) continue;
+            Codes<BITS> c = cd[k * C::kMT + m];
+            c.scale = (c.scale >> (8 * cgr)) & 255u;
+            unsigned char* dst = sm + C::KV + (uint32_t)(m * 2 + (cgr >> 1)) * kKvBlk + s * 128;
+            expand_group<BITS>(c, dst, (cgr & 1) * 4, s & 7);
+          }
         }
+        // the fence waits for the stores (about 500 cycles): one for two M tiles
         fence_proxy_async_smem();
-        arrive(&bar_kv[m]);
+        arrive(&bar_kv[x]);
       }
     };
     auto sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(C::kCompute) : "memory"); };
@@ -525,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
       if (more) convert(it + 1);
     }
 #pragma unroll
-    for (int m = 0; m < C::kMT; ++m) wait(&bar_o[m], (n - 1) & 1);
+    for (int x = 0; x < C::kParts; ++x) wait(&bar_o[x], (n - 1) & 1);
     fence_after();
     {
       const float l = lane_reduce16<false>(l_part);
@@ -588,7 +600,8 @@ cudaError_t launch_tc(const AttnDecodeArgs& a, const DecodePlan& p, cudaStream_t
   const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.cluster * p.parts), (unsigned)(a.b * p.groups * p.head_groups));
+  const int splits = p.cluster * p.parts;
+  cfg.gridDim = dim3((unsigned)splits * (unsigned)(a.b * p.groups * p.head_groups));
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -600,7 +613,8 @@ cudaError_t launch_tc(const AttnDecodeArgs& a, const DecodePlan& p, cudaStream_t
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, k, a, p.per_group, p.groups, p.head_groups, p.cluster);
+  return cudaLaunchKernelEx(&cfg, k, a, p.per_group, p.groups, p.head_groups, p.cluster,
+                            splits);
 }
 
 template <int D, int NC>

@@ -50,62 +50,60 @@ def load_library():
     return lib
 
 
-# A decode step makes these calls for every layer and token, each with kernels
-# of a few microseconds: the checks below are written to cost little where
-# nothing is wrong (one condition a tensor; the message is made on failure).
+# A decode step makes these calls for every layer and token, with kernels of a
+# few microseconds, so the checks cost as little as they can where nothing is
+# wrong: one condition over all of a call's tensors, and _refuse names the first
+# that is at fault when it fails.
 
-def _check(t, name, dtype, shape, dev):
-    """A contiguous CUDA tensor of this dtype and shape on device dev."""
+def _refuse(dev, **tensors):
+    """Raise for the first (tensor, dtype, shape) that is not a contiguous CUDA
+    tensor of that dtype and shape on device dev."""
+    for name, (t, dtype, shape) in tensors.items():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    raise ValueError("arguments do not agree")
+
+
+def _optional(t, name, dtype, shape, dev):
     if not (t.get_device() == dev and t.dtype is dtype and t.shape == shape
             and t.is_contiguous()):
-        _refuse(t, name, dtype, shape, dev)
-
-
-def _refuse(t, name, dtype, shape, dev):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        _refuse(dev, **{name: (t, dtype, shape)})
 
 
 def _first(t, name, dims):
     """The device index and dtype code of a call's main tensor."""
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     dt = _DT.get(t.dtype)
     if dt is None:
         raise TypeError(f"unsupported dtype {t.dtype} (bf16 or fp32)")
-    if t.dim() != len(dims):
+    if t.ndim != len(dims):
         raise ValueError(f"{name} must be [{', '.join(dims)}]")
-    return t.get_device(), dt
+    return dev, dt
 
 
-def _table(t, name, b, dev):
-    """P of a page table [b, P]."""
-    P = t.shape[1] if t.dim() == 2 else 0
-    _check(t, name, _I32, (b, max(P, 1)), dev)
-    return P
-
-
-def _pages(cache, page_size, bits, d, dev):
-    """n_pages of a cache tensor [n_pages, page bytes]."""
-    want = csa_cache_page_bytes(page_size, d, bits)
-    n = cache.shape[0] if cache.dim() == 2 else 0
-    _check(cache, "cache", _U8, (n, want), dev)
-    return n
+def _columns(t, name):
+    """Columns of a two-dimensional tensor, at least one."""
+    if t.ndim != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must have two dimensions and at least one column")
+    return t.shape[1]
 
 
 def _workspace(ws, nbytes, dev):
     """Pointer and size of the workspace; the tensor is returned to be kept alive."""
     if ws is None:
         ws = torch.empty(max(nbytes, 16), dtype=_U8, device=f"cuda:{dev}")
-    elif not (ws.is_cuda and ws.is_contiguous() and ws.get_device() == dev):
-        _refuse(ws, "workspace", ws.dtype, ws.shape, dev)
+    elif not (ws.get_device() == dev and ws.is_contiguous()):
+        _refuse(dev, workspace=(ws, ws.dtype, ws.shape))
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -141,11 +139,17 @@ def _rows_args(x, name, cache, table, pos0, page_size, bits, counts):
     bs, rs, cs = x.stride()
     if cs != 1 and b and s:
         raise ValueError(f"{name} rows must be contiguous")
-    n_pages = _pages(cache, page_size, bits, d, dev)
-    P = _table(table, "table", b, dev)
-    _check(pos0, "pos0", _I32, (b,), dev)
+    want = csa_cache_page_bytes(page_size, d, bits)
+    n_pages, row = cache.shape if cache.ndim == 2 else (0, -1)
+    P = _columns(table, "table")
+    if not (row == want and cache.dtype is _U8 and table.dtype is _I32 and pos0.dtype is _I32
+            and cache.get_device() == dev and table.get_device() == dev
+            and pos0.get_device() == dev and table.shape[0] == b and pos0.shape == (b,)
+            and cache.is_contiguous() and table.is_contiguous() and pos0.is_contiguous()):
+        _refuse(dev, cache=(cache, _U8, (n_pages, want)), table=(table, _I32, (b, P)),
+                pos0=(pos0, _I32, (b,)))
     if counts is not None:
-        _check(counts, "counts", _I32, (b,), dev)
+        _optional(counts, "counts", _I32, (b,), dev)
     return dev, dt, b, s, d, bs, rs, P, n_pages
 
 
@@ -201,18 +205,25 @@ def csa_indexer_topk_decode(q_I: torch.Tensor, cache: torch.Tensor, table: torch
     ascending, -1 behind the min(topk, vis) blocks.
     """
     dev, dt = _first(q_I, "q_I", ("b", "s_q", "H_I", "d_I"))
-    b, s_q, H, d = shape = q_I.shape
-    _check(q_I, "q_I", q_I.dtype, shape, dev)
-    n_pages = _pages(cache, page_size, bits, d, dev)
-    P = _table(table, "table", b, dev)
-    _check(w, "w", _F32, (b, s_q, H), dev)
-    _check(seq_lens, "seq_lens", _I32, (b,), dev)
+    b, s_q, H, d = q_I.shape
+    want = csa_cache_page_bytes(page_size, d, bits)
+    n_pages, row = cache.shape if cache.ndim == 2 else (0, -1)
+    P = _columns(table, "table")
+    if not (row == want and cache.dtype is _U8 and table.dtype is _I32 and w.dtype is _F32
+            and seq_lens.dtype is _I32 and cache.get_device() == dev and table.get_device() == dev
+            and w.get_device() == dev and seq_lens.get_device() == dev and table.shape[0] == b
+            and w.shape == (b, s_q, H) and seq_lens.shape == (b,) and q_I.is_contiguous()
+            and cache.is_contiguous() and table.is_contiguous() and w.is_contiguous()
+            and seq_lens.is_contiguous()):
+        _refuse(dev, q_I=(q_I, q_I.dtype, q_I.shape), cache=(cache, _U8, (n_pages, want)),
+                table=(table, _I32, (b, P)), w=(w, _F32, (b, s_q, H)),
+                seq_lens=(seq_lens, _I32, (b,)))
     if topk < 1:
         raise ValueError("topk must be at least 1")
     if out_idx is None:
-        out_idx = torch.empty((b, s_q, topk), dtype=_I32, device=q_I.device)
+        out_idx = q_I.new_empty((b, s_q, topk), dtype=_I32)
     else:
-        _check(out_idx, "out_idx", _I32, (b, s_q, topk), dev)
+        _optional(out_idx, "out_idx", _I32, (b, s_q, topk), dev)
     nbytes = (csa_indexer_topk_decode_workspace_size(b, s_q, H, d, P * page_size)
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
@@ -243,34 +254,44 @@ def csa_attn_decode(q: torch.Tensor, cache: torch.Tensor, raw_table: torch.Tenso
     Returns (O [b, s_q, H, d], lse [b, s_q, H] fp32).
     """
     dev, dt = _first(q, "q", ("b", "s_q", "H", "d"))
-    b, s_q, H, d = shape = q.shape
-    _check(q, "q", q.dtype, shape, dev)
-    n_pages = _pages(cache, page_size, bits, d, dev)
-    P_raw = _table(raw_table, "raw_table", b, dev)
-    P_cmp = 0 if cmp_table is None else _table(cmp_table, "cmp_table", b, dev)
-    K = 0
+    b, s_q, H, d = q.shape
+    want = csa_cache_page_bytes(page_size, d, bits)
+    n_pages, row = cache.shape if cache.ndim == 2 else (0, -1)
+    P_raw = _columns(raw_table, "raw_table")
+    if not (row == want and cache.dtype is _U8 and raw_table.dtype is _I32
+            and seq_lens.dtype is _I32 and cache.get_device() == dev
+            and raw_table.get_device() == dev and seq_lens.get_device() == dev
+            and raw_table.shape[0] == b and seq_lens.shape == (b,) and q.is_contiguous()
+            and cache.is_contiguous() and raw_table.is_contiguous() and seq_lens.is_contiguous()):
+        _refuse(dev, q=(q, q.dtype, q.shape), cache=(cache, _U8, (n_pages, want)),
+                raw_table=(raw_table, _I32, (b, P_raw)), seq_lens=(seq_lens, _I32, (b,)))
+    P_cmp = K = 0
+    cmp_ptr = idx_ptr = sink_ptr = None
+    if cmp_table is not None:
+        P_cmp = _columns(cmp_table, "cmp_table")
+        _optional(cmp_table, "cmp_table", _I32, (b, P_cmp), dev)
+        cmp_ptr = cmp_table.data_ptr()
     if idx is not None:
-        K = idx.shape[2] if idx.dim() == 3 else 0
-        _check(idx, "idx", _I32, (b, s_q, K), dev)
+        K = idx.shape[2] if idx.ndim == 3 else 0
         if K == 0 or cmp_table is None:
             raise ValueError("idx needs at least one entry a row, and cmp_table")
+        _optional(idx, "idx", _I32, (b, s_q, K), dev)
+        idx_ptr = idx.data_ptr()
     if sink is not None:
-        _check(sink, "sink", _F32, (H,), dev)
-    _check(seq_lens, "seq_lens", _I32, (b,), dev)
+        _optional(sink, "sink", _F32, (H,), dev)
+        sink_ptr = sink.data_ptr()
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check(out, "out", q.dtype, shape, dev)
+        _optional(out, "out", q.dtype, q.shape, dev)
     if lse is None:
-        lse = torch.empty((b, s_q, H), dtype=_F32, device=q.device)
+        lse = q.new_empty((b, s_q, H), dtype=_F32)
     else:
-        _check(lse, "lse", _F32, (b, s_q, H), dev)
+        _optional(lse, "lse", _F32, (b, s_q, H), dev)
     nbytes = (csa_attn_decode_workspace_size(b, s_q, H, d, window, K or P_cmp * page_size)
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
     _call("csa_attn_decode", dev, stream, q.data_ptr(), cache.data_ptr(), raw_table.data_ptr(),
-          None if cmp_table is None else cmp_table.data_ptr(),
-          None if idx is None else idx.data_ptr(), None if sink is None else sink.data_ptr(),
-          seq_lens.data_ptr(), scale, out.data_ptr(), lse.data_ptr(), b, s_q, H, d, ratio, window,
+          cmp_ptr, idx_ptr, sink_ptr, seq_lens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), b, s_q, H, d, ratio, window,
           K, P_raw, P_cmp, n_pages, page_size, bits, dt, ws, nbytes)
     return out, lse

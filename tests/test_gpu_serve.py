@@ -231,6 +231,9 @@ INDEX_CASES = [
     (2, 1, 64, 128, 4, [900, 37], 50, 4, 64, F32),
     (1, 2, 5, 64, 3, [500], 20, 8, 16, F32),
     (1, 1, 16, 128, 128, [40000], 512, 4, 64, BF),      # topk above the visible blocks
+    (1, 2, 70, 128, 4, [900], 40, 4, 16, BF),           # a query a CTA of 128 columns
+    (2, 9, 8, 64, 2, [400, 5], 25, 8, 16, BF),          # nine queries: two groups of columns
+    (1, 1, 128, 64, 1, [385], 100, 4, 128, BF),
 ]
 
 
@@ -325,6 +328,30 @@ def test_indexer_long_row():
         got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev([n], I32), topk, 1,
                                             page, bits)
         assert torch.equal(got[0, 0].long(), want)
+
+
+@pytest.mark.parametrize("n,kind", [(300000, "random"), (300000, "ties"), (40000, "ties"),
+                                    (40000, "outlier")])
+def test_indexer_rows_of_several_ctas(n, kind):
+    """Rows beyond what one CTA, and beyond what eight, keep in shared memory;
+    rows of ties, and rows whose range one outlier stretches."""
+    rng = np.random.default_rng(n)
+    d, H, page, bits, topk = 64, 8, 64, 8, 700
+    keys = rng.standard_normal((1, n, d)).astype(np.float32)
+    if kind == "ties":
+        keys = keys[:, rng.integers(0, 3, n)]
+    if kind == "outlier":
+        keys[0, 777] *= 1e6
+    keys = torch.from_numpy(keys).to(BF)
+    cache, table, keys, q, w = index_case(rng, 1, 1, H, d, 1, [n], bits, page, BF, keys=keys)
+    w = w.abs()
+    held = torch.zeros(1, n, d, dtype=F32, device="cuda")
+    serve.csa_cache_read(cache, dev(table), dev(np.zeros(1, np.int32)), held, page, bits)
+    score = ((held[0].double() @ q[0, 0].cuda().double().T).clamp(min=0) * w[0, 0].cuda().double()).sum(1)
+    want = score.sort(descending=True, stable=True).indices[:topk].sort().values
+    got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev([n], I32), topk, 1, page,
+                                        bits)
+    assert torch.equal(got[0, 0].long(), want)
 
 
 def test_indexer_bad_page_and_length():
@@ -543,6 +570,134 @@ def test_calls_on_a_side_stream_and_in_two_graphs_that_share_workspaces():
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, graphs[0][1]))
     assert not torch.equal(want[1], ref[1])
+
+
+def test_two_calls_at_once_on_two_streams():
+    rng = np.random.default_rng(33)
+    case = (3, 1, 64, 512, 4, 128, [900, 5, 1300], 200, 4, 16, BF, True)
+    parts = attn_case(rng, case)
+    icache, itable, keys, qi, w = index_case(rng, 3, 1, 64, 128, 4, [40000, 9000, 100], 4, 64, BF)
+    lens = dev([40000, 9000, 100], I32)
+    qi, w, itable = qi.cuda(), w.cuda(), dev(itable)
+    want_o, want_l = run_attn(case, parts)
+    want_i = serve.csa_indexer_topk_decode(qi, icache, itable, w, lens, 512, 4, 64, 4)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for r in range(6):
+        with torch.cuda.stream(streams[r % 2]):
+            got.append((run_attn(case, parts),
+                        serve.csa_indexer_topk_decode(qi, icache, itable, w, lens, 512, 4, 64, 4)))
+    torch.cuda.synchronize()
+    for (o, lse), idx in got:
+        assert torch.equal(o, want_o) and torch.equal(lse, want_l) and torch.equal(idx, want_i)
+
+
+def test_many_short_sequences():
+    """More queries than a grid dimension of 65535 CTAs times two head groups."""
+    b, H, d, page, bits = 33000, 128, 64, 16, 4
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache = empty_cache(3, page, d, bits)
+    table = torch.ones(b, 1, dtype=I32, device="cuda")
+    raw = torch.randn(1, 4, d, generator=g, device="cuda").to(BF)
+    serve.csa_cache_write(raw, cache, table[:1], torch.zeros(1, dtype=I32, device="cuda"), page, bits)
+    q = torch.randn(b, 1, H, d, generator=g, device="cuda").to(BF)
+    lens = (torch.arange(b, device="cuda") % 5).to(I32)
+    o, lse = serve.csa_attn_decode(q, cache, table, None, None, None, lens, 0.125, 4, 3, page, bits)
+    held = torch.zeros(1, 4, d, dtype=F32, device="cuda")
+    serve.csa_cache_read(cache, table[:1], torch.zeros(1, dtype=I32, device="cuda"), held, page, bits)
+    z = (q[:, 0].double() @ held[0].double().T) * 0.125
+    pos = torch.arange(4, device="cuda")
+    t = lens.long()[:, None] - 1
+    ok = (pos <= t) & (pos > t - 3)
+    z = torch.where(ok[:, None], z, torch.full_like(z, -float("inf")))
+    want = torch.softmax(z, -1).nan_to_num(0.0) @ held[0].double()
+    # probabilities, their sum and o in bf16 half steps, as in check_row
+    spread = torch.softmax(z, -1).nan_to_num(0.0) @ held[0].double().abs()
+    assert bool(((o[:, 0].double() - want).abs() <= 3 * 2.0 ** -8 * spread + 1e-4).all())
+    assert bool((lse[lens == 0] == -float("inf")).all())
+
+
+FUZZ = list(range(24))
+
+
+@pytest.mark.parametrize("seed", FUZZ)
+def test_random_configurations(seed):
+    """A random layer: cache rows written in ragged pieces over a ring, selected
+    and attended to, against fp64 torch on the rows read back."""
+    import random
+    r = random.Random(seed)
+    rng = np.random.default_rng(seed)
+    b, s_q, bits = r.randint(1, 6), r.choice([1, 1, 2, 3, 5]), r.choice([4, 8])
+    page, ratio = r.choice([16, 32, 48, 64]), r.choice([1, 2, 4, 16])
+    H, d = r.choice([1, 8, 16, 24, 32, 64, 96]), r.choice([32, 64, 128, 192, 256, 512])
+    H_I, d_I, topk = r.choice([1, 4, 16, 40, 64, 128]), r.choice([32, 64, 128, 256]), r.choice([1, 9, 64, 257])
+    window = r.choice([1, 5, 40, 128])
+    dtype = r.choice([BF, BF, BF, F32])
+    lens = [r.choice([0, 1, r.randint(2, 60), r.randint(60, 1500)]) for _ in range(b)]
+    n_c = max(1, max(lens) // ratio)
+    P_raw, P_cmp = -(-(window + s_q - 1) // page) + r.randint(0, 2), -(-n_c // page)
+    n_pages, (raw_t, cmp_t) = tables(rng, b, P_raw, P_cmp)
+    i_pages, (key_t,) = tables(rng, b, P_cmp)
+    raw_t, cmp_t, key_t, seq = dev(raw_t), dev(cmp_t), dev(key_t), dev(lens, I32)
+    cache, icache = empty_cache(n_pages, page, d, bits), empty_cache(i_pages, page, d_I, bits)
+    top = max(max(lens), 1)
+    raw = torch.from_numpy(rng.standard_normal((b, top, d))).to(dtype).cuda()
+    cmp = torch.from_numpy(rng.standard_normal((b, n_c, d))).to(dtype).cuda()
+    keys = torch.from_numpy(rng.standard_normal((b, n_c, d_I))).to(dtype).cuda()
+    zero = torch.zeros(b, dtype=I32, device="cuda")
+    cut = top // 3
+    first = torch.minimum(seq, torch.full_like(seq, cut))
+    serve.csa_cache_write(raw[:, :max(cut, 1)], cache, raw_t, zero, page, bits, counts=first)
+    serve.csa_cache_write(raw[:, cut:], cache, raw_t, first, page, bits, counts=seq - first)
+    serve.csa_cache_write(cmp, cache, cmp_t, zero, page, bits, counts=seq // ratio)
+    serve.csa_cache_write(keys, icache, key_t, zero, page, bits, counts=seq // ratio)
+    q = torch.from_numpy(rng.standard_normal((b, s_q, H, d))).to(dtype).cuda()
+    q_I = torch.from_numpy(rng.standard_normal((b, s_q, H_I, d_I))).to(dtype).cuda()
+    w = torch.from_numpy(rng.standard_normal((b, s_q, H_I))).float().cuda()
+    sink = torch.from_numpy(rng.standard_normal(H)).float().cuda() if r.random() < 0.7 else None
+    idx = serve.csa_indexer_topk_decode(q_I, icache, key_t, w, seq, topk, ratio, page, bits)
+    use = None if r.random() < 0.3 else idx
+    o, lse = serve.csa_attn_decode(q, cache, raw_t, cmp_t, use, sink, seq, d ** -0.5, ratio, window, page, bits)
+    assert csa.csa_get_device_status() == 0
+    k_held = serve.csa_cache_read(icache, key_t, zero, torch.zeros(b, n_c, d_I, device="cuda"), page, bits,
+                                  counts=seq // ratio)
+    c_held = serve.csa_cache_read(cache, cmp_t, zero, torch.zeros(b, n_c, d, device="cuda"), page, bits,
+                                  counts=seq // ratio)
+    keep = min(P_raw * page, window + s_q - 1)
+    start = (seq - keep).clamp(min=0)
+    r_held = serve.csa_cache_read(cache, raw_t, start, torch.zeros(b, keep, d, device="cuda"), page, bits,
+                                  counts=seq - start)
+    for s in range(b):
+        for i in range(s_q):
+            t = lens[s] - s_q + i
+            vis = (t + 1) // ratio if t >= 0 else 0
+            sc = ((k_held[s, :vis].double() @ q_I[s, i].double().T).clamp(min=0) * w[s, i].double()).sum(1)
+            want = sc.sort(descending=True, stable=True).indices[:topk].sort().values
+            got = idx[s, i]
+            assert torch.equal(got[:len(want)].long(), want) and bool((got[len(want):] == -1).all()), (s, i)
+            rows = torch.zeros(0, d, dtype=torch.float64, device="cuda")
+            if t >= 0:
+                p0 = max(0, t - window + 1)
+                off = int(start[s])
+                js = idx[s, i][idx[s, i] >= 0].long() if use is not None else torch.arange(vis, device="cuda")
+                rows = torch.cat([r_held[s, p0 - off:t + 1 - off], c_held[s][js]]).double()
+            z = q[s, i].double() @ rows.T * d ** -0.5
+            zs = sink.double()[:, None] if sink is not None else torch.full((H, 1), -float("inf"), device="cuda",
+                                                                        dtype=torch.float64)
+            l = torch.logsumexp(torch.cat([z, zs], 1), 1)
+            p = torch.exp(z - l[:, None])
+            p = torch.where(torch.isfinite(p), p, torch.zeros_like(p))
+            ref, spread = p @ rows, p @ rows.abs()
+            # as in check_row: fp32 logits, probabilities and o in bf16 half steps
+            big = (q[s, i].double().abs().sum(-1).max() * rows.abs().max() * d ** -0.5).item() if len(rows) else 0.0
+            logit = 2 * d * 2.0 ** -23 * big + 2.0 ** -20
+            tol = (logit + (2 * 2.0 ** -8 if dtype == BF else 0)) * spread + (
+                2.0 ** -8 if dtype == BF else 2.0 ** -23) * ref.abs() + 1e-30
+            assert bool(((o[s, i].double() - ref).abs() <= tol).all()), (s, i)
+            fin = torch.isfinite(l)
+            assert torch.equal(lse[s, i][~fin].double(), l[~fin])
+            assert bool(((lse[s, i].double() - l)[fin].abs() <= logit + 2.0 ** -22 * l[fin].abs()).all())
 
 
 @pytest.mark.parametrize("bits", [4, 8])
