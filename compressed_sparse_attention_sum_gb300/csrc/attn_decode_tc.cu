@@ -74,9 +74,11 @@ struct Cfg {
   static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][4][NC] column maxima
   static constexpr uint32_t MRUN = RED + 8 * NC * 4;       // [2][NC]
   static constexpr uint32_t ML = MRUN + 2 * NC * 4;        // [NC] (maximum, sum) of this CTA
-  static constexpr uint32_t OKS = ML + NC * 8;             // [2][kSlots] bytes
+  static constexpr uint32_t SINK = ML + NC * 8;            // [NC] sink logits of the heads (log2 units)
+  static constexpr uint32_t OKS = SINK + NC * 4;           // [2][kSlots] bytes
   static constexpr uint32_t kBytes = OKS + 2 * kSlots;
-  static constexpr uint32_t STAGE = KV;                    // [NC][D] fp32: O, after the last tile
+  static constexpr uint32_t STAGE = KV;                    // [NC][D] O after the last tile: fp32, or
+                                                           // bf16 where this CTA has the whole query
 };
 
 // Transposing butterfly: v[c] holds this lane's value of column c; afterwards
@@ -100,86 +102,59 @@ __device__ __forceinline__ float lane_reduce16(float (&v)[16]) {
 }
 
 // Joins the (m, l, O) of the CS CTAs of a cluster for this CTA's share of the
-// columns, from their shared memory: first a weight for each (CTA, column),
-// then the weighted sums, a warp to a column.  final: also the sink, o and
-// lse; otherwise the cluster's entry of the partial results.
+// columns, from their shared memory, four channels a thread: all of its reads
+// are in flight at once.  final: also the sink, o and lse; otherwise the
+// cluster's entry of the partial results.
 template <int D, int NC, int CS>
 __device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned char* sm, int rank,
-                                             int part, bool final, int per_group, int nq, int heads,
-                                             int h0, long long row0) {
+                                             int part, int per_group, int nq, int heads, int h0,
+                                             long long row0) {
   using C = Cfg<D, NC>;
   constexpr int kCols = NC / CS;                           // columns of this CTA
+  const bool final = a.parts == 1;
+  const float* sink = reinterpret_cast<const float*>(sm + C::SINK);
   const unsigned char* base[CS];
 #pragma unroll
-  for (int r = 0; r < CS; ++r) {
-    if constexpr (CS > 1) base[r] = cg::this_cluster().map_shared_rank(sm, r);
-    else base[r] = sm;
-  }
-  float* wgt = reinterpret_cast<float*>(sm + C::RED);      // [kCols][CS], this CTA's own
-  for (int x = threadIdx.x; x < kCols; x += C::kThreads) {
-    const int col = rank * kCols + x;
-    const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
-    const bool live = qi < nq && h < heads;
+  for (int r = 0; r < CS; ++r) base[r] = cg::this_cluster().map_shared_rank(sm, r);
+  for (int e = threadIdx.x; e < kCols * (D / 4); e += C::kThreads) {
+    const int col = rank * kCols + e / (D / 4), c = e % (D / 4) * 4;
     float2 ml[CS];
+    float4 v[CS];
 #pragma unroll
-    for (int r = 0; r < CS; ++r) ml[r] = *reinterpret_cast<const float2*>(base[r] + C::ML + col * 8);
-    const float sink2 = live && final && a.sink != nullptr ? a.sink[h0 + h] * kLog2e : -INFINITY;
+    for (int r = 0; r < CS; ++r) {
+      ml[r] = *reinterpret_cast<const float2*>(base[r] + C::ML + col * 8);
+      v[r] = *reinterpret_cast<const float4*>(base[r] + C::STAGE + (col * D + c) * 4);
+    }
+    const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
+    if (qi >= nq || h >= heads) continue;
+    const float sink2 = final ? sink[h] : -INFINITY;
     float m = sink2, total = 0.f;
 #pragma unroll
     for (int r = 0; r < CS; ++r) m = fmaxf(m, ml[r].x);
-    float f[CS];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
-      // a CTA without a tile has no O: its weight is zero
-      f[r] = ml[r].y > 0.f ? exp2f(ml[r].x - m) : 0.f;
-      total = fmaf(ml[r].y, f[r], total);
-    }
-    if (sink2 > -INFINITY) total += exp2f(sink2 - m);
-    const float inv = !final ? 1.f : total > 0.f ? 1.f / total : 0.f;
-#pragma unroll
-    for (int r = 0; r < CS; ++r) wgt[x * CS + r] = f[r] * inv;
-    if (live) {
-      const long long row = row0 + qi;
-      if (final)
-        a.lse[row * a.H + h0 + h] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
-      else
-        a.part_ml[(row * a.parts + part) * a.H + h0 + h] = make_float2(m, total);
-    }
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int x = warp; x < kCols; x += C::kThreads / 32) {
-    const int col = rank * kCols + x;
-    const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
-    if (qi >= nq || h >= heads) continue;
-    float f[CS];
-#pragma unroll
-    for (int r = 0; r < CS; ++r) f[r] = wgt[x * CS + r];
-    const long long row = row0 + qi;
-    __nv_bfloat16* o = (__nv_bfloat16*)a.o + (row * a.H + h0 + h) * D;
-    float* po = a.part_o + ((row * a.parts + part) * a.H + h0 + h) * D;
-#pragma unroll
-    for (int c = lane * 4; c < D; c += 128) {
-      float4 v[CS];
-#pragma unroll
-      for (int r = 0; r < CS; ++r)
-        v[r] = *reinterpret_cast<const float4*>(base[r] + C::STAGE + (col * D + c) * 4);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int r = 0; r < CS; ++r) {
-        if (f[r] > 0.f) {
-          acc.x = fmaf(v[r].x, f[r], acc.x);
-          acc.y = fmaf(v[r].y, f[r], acc.y);
-          acc.z = fmaf(v[r].z, f[r], acc.z);
-          acc.w = fmaf(v[r].w, f[r], acc.w);
-        }
+      if (ml[r].y > 0.f) {                                 // a CTA without a tile has no O
+        const float f = ex2(ml[r].x - m);
+        total = fmaf(ml[r].y, f, total);
+        acc.x = fmaf(v[r].x, f, acc.x);
+        acc.y = fmaf(v[r].y, f, acc.y);
+        acc.z = fmaf(v[r].z, f, acc.z);
+        acc.w = fmaf(v[r].w, f, acc.w);
       }
-      if (final)
-        *reinterpret_cast<uint2*>(o + c) =
-            make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-      else
-        *reinterpret_cast<float4*>(po + c) = acc;
     }
+    const long long row = row0 + qi;
+    if (!final) {
+      const long long at = (row * a.parts + part) * a.H + h0 + h;
+      *reinterpret_cast<float4*>(a.part_o + at * D + c) = acc;
+      if (c == 0) a.part_ml[at] = make_float2(m, total);
+      continue;
+    }
+    if (sink2 > -INFINITY) total += ex2(sink2 - m);
+    const float inv = total > 0.f ? __fdividef(1.f, total) : 0.f;
+    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + (row * a.H + h0 + h) * D + c) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (c == 0) a.lse[row * a.H + h0 + h] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
   }
 }
 
@@ -213,6 +188,35 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
   const int h0 = hg * NC, heads = min(a.H - h0, per_group > 1 ? a.H : NC);   // heads of a query
   const long long row0 = (long long)bi * a.s_q + i0;
 
+  // Q: column c is query i0 + c / H, head h0 + c % H; columns past them are zero.
+  // The first reads leave before anything is waited for.
+  constexpr int kQIter = (NC * (D / 8) + C::kThreads - 1) / C::kThreads;
+  constexpr int kQBatch = kQIter < 8 ? kQIter : 8;
+  uint4 qv[kQBatch];
+  auto read_q = [&](int x0) {
+#pragma unroll
+    for (int x = 0; x < kQBatch; ++x) {
+      const int e = tid + (x0 + x) * C::kThreads, c = e / (D / 8), ch = e - c * (D / 8);
+      const int qi = per_group > 1 ? c / a.H : 0, h = per_group > 1 ? c - qi * a.H : c;
+      qv[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < NC && qi < nq && h < heads)
+        qv[x] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                     ((row0 + qi) * a.H + h0 + h) * D + ch * 8));
+    }
+  };
+  auto store_q = [&](int x0) {
+#pragma unroll
+    for (int x = 0; x < kQBatch; ++x) {
+      const int e = tid + (x0 + x) * C::kThreads, c = e / (D / 8), ch = e - c * (D / 8);
+      if (c < NC)
+        *reinterpret_cast<uint4*>(sm + C::Q + (ch >> 3) * C::kQBlk + c * 128 +
+                                  (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(qv[x]);
+    }
+  };
+  read_q(0);
+  float sink_v = -INFINITY;
+  if (tid < heads && tid < NC && a.sink != nullptr) sink_v = __ldg(a.sink + h0 + tid) * kLog2e;
+
   // The slots: the union window of the group's queries, then the index
   // entries (one query) or the blocks the last query sees.
   const DecodeRow last = decode_row(a, bi, i0 + nq - 1);
@@ -239,6 +243,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
   if (tid < NC) {
     m_run[tid] = -INFINITY;
     ml[tid] = make_float2(-INFINITY, 0.f);
+    reinterpret_cast<float*>(sm + C::SINK)[tid] = sink_v;
   }
 
   // ---- the converting side's reads: index entry, page id, codes -----------------
@@ -314,31 +319,15 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
   };
   if (conv && n > 0) read_index(0);
 
-  // Q: column c is query i0 + c / H, head h0 + c % H; columns past them are zero
-  constexpr int kQIter = (NC * (D / 8) + C::kThreads - 1) / C::kThreads;
-  constexpr int kQBatch = kQIter < 8 ? kQIter : 8;
-  for (int x0 = 0; x0 < kQIter; x0 += kQBatch) {
-    uint4 v[kQBatch];
-#pragma unroll
-    for (int x = 0; x < kQBatch; ++x) {
-      const int e = tid + (x0 + x) * C::kThreads, c = e / (D / 8), ch = e - c * (D / 8);
-      const int qi = per_group > 1 ? c / a.H : 0, h = per_group > 1 ? c - qi * a.H : c;
-      v[x] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < NC && qi < nq && h < heads)
-        v[x] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
-                                                    ((row0 + qi) * a.H + h0 + h) * D + ch * 8));
-    }
-    if (x0 == 0 && conv && n > 0) {
-      read_page(0);
-      read_index(1);
-    }
-#pragma unroll
-    for (int x = 0; x < kQBatch; ++x) {
-      const int e = tid + (x0 + x) * C::kThreads, c = e / (D / 8), ch = e - c * (D / 8);
-      if (c < NC)
-        *reinterpret_cast<uint4*>(sm + C::Q + (ch >> 3) * C::kQBlk + c * 128 +
-                                  (((ch & 7) ^ (c & 7)) << 4)) = permute8<BITS>(v[x]);
-    }
+  if (conv && n > 0) {
+    read_page(0);
+    read_index(1);
+  }
+  store_q(0);
+#pragma unroll 1
+  for (int x0 = kQBatch; x0 < kQIter; x0 += kQBatch) {
+    read_q(x0);
+    store_q(x0);
   }
   if (conv && n > 0) {
     fetch(0);
@@ -361,6 +350,10 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
 
   if (!conv) {
     // ---- the issuing warp ------------------------------------------------------
+    // The tiles are written through the generic proxy and read through the async
+    // one.  The proxy fence between stands on this side of the barriers, where one
+    // thread executes it: it has to lie on the path from the write to the read, and
+    // executed by all 16 writing warps it takes about 600 cycles each time.
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32_major(kSlots, NC, 0, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32_major(128, NC, 1, 1);
@@ -371,6 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
 #pragma unroll 1
         for (int x = 0; x < C::kParts; ++x) {
           if (!wait(&bar_kv[x], it & 1)) break;
+          fence_proxy_async_smem();
           fence_after();
 #pragma unroll
           for (int kk = 0; kk < kSteps * C::kPart; ++kk) {
@@ -383,6 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
         if (*dead) break;
         mma_commit(bar_s);
         if (!wait(bar_p, it & 1)) break;
+        fence_proxy_async_smem();
         fence_after();
 #pragma unroll 1
         for (int x = 0; x < C::kParts; ++x) {
@@ -420,22 +415,22 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
     auto convert = [&](int it) {
 #pragma unroll
       for (int x = 0; x < C::kParts; ++x) {
+        // expanded in registers before the wait
+        uint32_t o[C::kPart * C::kSpt][16];
+#pragma unroll
+        for (int e = 0; e < C::kPart * C::kSpt; ++e) {
+          Codes<BITS> c = cd[(e % C::kSpt) * C::kMT + x * C::kPart + e / C::kSpt];
+          c.scale = (c.scale >> (8 * cgr)) & 255u;
+          expand_words<BITS>(c, o[e]);
+        }
         if (it > 0) wait(&bar_o[x], (it - 1) & 1);
 #pragma unroll
-        for (int mm = 0; mm < C::kPart; ++mm) {
-          const int m = x * C::kPart + mm;
-#pragma unroll
-          for (int k = 0; k < C::kSpt; ++k) {
-            const int s = cslot + k * C::kPass;
-            if (s >= kSlots) continue;
-            Codes<BITS> c = cd[k * C::kMT + m];
-            c.scale = (c.scale >> (8 * cgr)) & 255u;
-            unsigned char* dst = sm + C::KV + (uint32_t)(m * 2 + (cgr >> 1)) * kKvBlk + s * 128;
-            expand_group<BITS>(c, dst, (cgr & 1) * 4, s & 7);
-          }
+        for (int e = 0; e < C::kPart * C::kSpt; ++e) {
+          const int m = x * C::kPart + e / C::kSpt, s = cslot + (e % C::kSpt) * C::kPass;
+          if (s < kSlots)
+            store_words(o[e], sm + C::KV + (uint32_t)(m * 2 + (cgr >> 1)) * kKvBlk + s * 128,
+                        (cgr & 1) * 4, s & 7);
         }
-        // the fence waits for the stores (about 500 cycles): one for two M tiles
-        fence_proxy_async_smem();
         arrive(&bar_kv[x]);
       }
     };
@@ -531,7 +526,6 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
         *reinterpret_cast<uint4*>(prow + (((hq * 2 + c8) ^ (r & 7)) << 4)) =
             make_uint4(pk[0], pk[1], pk[2], pk[3]);
       }
-      fence_proxy_async_smem();
       fence_before();
       arrive(bar_p);
       if (more) convert(it + 1);
@@ -543,9 +537,34 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
       const float l = lane_reduce16<false>(l_part);
       if (lane < 16) red[((n & 1) * 4 + qd) * NC + hq * 16 + lane] = l;
     }
+    sync();
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (tid < NC) {
+      const float* rl = red + (n & 1) * 4 * NC + tid;
+      mine = make_float2(m_run[(n & 1) * NC + tid], (rl[0] + rl[NC]) + (rl[2 * NC] + rl[3 * NC]));
+    }
+    if (cs == 1) {
+      // the whole query: its sums with the sink, and each column's factor
+      if (tid < NC) {
+        const int qi = per_group > 1 ? tid / a.H : 0, h = per_group > 1 ? tid - qi * a.H : tid;
+        const bool live = qi < nq && h < heads;
+        const float sink2 = live ? reinterpret_cast<const float*>(sm + C::SINK)[h] : -INFINITY;
+        const float m = fmaxf(mine.x, sink2);
+        float f = 0.f, out = -INFINITY;
+        if (m > -INFINITY) {
+          const float fm = ex2(mine.x - m), total = fmaf(mine.y, fm, ex2(sink2 - m));
+          f = __fdividef(fm, total);
+          out = (m + log2f(total)) * kLn2;
+        }
+        m_run[tid] = f;
+        if (live && !*dead) a.lse[(row0 + qi) * a.H + h0 + h] = out;
+      }
+      sync();
+    } else if (tid < NC) {
+      ml[tid] = mine;
+    }
     // O^T into shared memory as [column][channel]: the KV tile's place
     if (!*dead) {
-      float* stage = reinterpret_cast<float*>(sm + C::STAGE);
 #pragma unroll 1
       for (int m = 0; m < C::kMT; ++m) {
         const int p = m * 128 + r;
@@ -553,32 +572,46 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC
         tmem_ld16_wait(tmem + lane_base + C::kColO + m * NC + hq * 16, v);
         if (p < D) {
           const int ch = channel_of<BITS>(p);
+          if (cs == 1) {
+            __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sm + C::STAGE);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) stage[(hq * 16 + c) * D + ch] = __uint_as_float(v[c]);
+            for (int c = 0; c < 16; ++c)
+              stage[(hq * 16 + c) * D + ch] =
+                  __float2bfloat16_rn(__uint_as_float(v[c]) * m_run[hq * 16 + c]);
+          } else {
+            float* stage = reinterpret_cast<float*>(sm + C::STAGE);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) stage[(hq * 16 + c) * D + ch] = __uint_as_float(v[c]);
+          }
         }
       }
-    }
-    sync();
-    if (tid < NC) {
-      const float* rl = red + (n & 1) * 4 * NC + tid;
-      ml[tid] = make_float2(m_run[(n & 1) * NC + tid], (rl[0] + rl[NC]) + (rl[2 * NC] + rl[3 * NC]));
     }
     fence_before();
   }
   // ---- join ----------------------------------------------------------------------
   if (cs > 1) cg::this_cluster().sync();
   else __syncthreads();
-  if (!*dead) {
-    const bool final = a.parts == 1;
+  if (*dead) {
+    if (tid == 0) set_status(a.status, kDevTimeout, kSiteDecode);
+  } else if (cs == 1) {
+    // the columns' rows of o lie one behind the other
+    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + (row0 * a.H + h0) * D);
+    const uint4* src = reinterpret_cast<const uint4*>(sm + C::STAGE);
+    const int chunks = nq * heads * (D / 8);
+#pragma unroll 4
+    for (int e = tid; e < chunks; e += C::kThreads)
+      dst[e] = n > 0 ? src[e] : make_uint4(0u, 0u, 0u, 0u);
+    if (n == 0 && tid < nq * heads) {                      // nothing to attend to
+      const int qi = tid / heads, h = tid - qi * heads;
+      a.lse[(row0 + qi) * a.H + h0 + h] = a.sink != nullptr ? a.sink[h0 + h] : -INFINITY;
+    }
+  } else {
     const int part = split / cs;
     switch (cs) {
-      case 1: join_cluster<D, NC, 1>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
-      case 2: join_cluster<D, NC, 2>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
-      case 4: join_cluster<D, NC, 4>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
-      default: join_cluster<D, NC, 8>(a, sm, rank, part, final, per_group, nq, heads, h0, row0); break;
+      case 2: join_cluster<D, NC, 2>(a, sm, rank, part, per_group, nq, heads, h0, row0); break;
+      case 4: join_cluster<D, NC, 4>(a, sm, rank, part, per_group, nq, heads, h0, row0); break;
+      default: join_cluster<D, NC, 8>(a, sm, rank, part, per_group, nq, heads, h0, row0); break;
     }
-  } else if (tid == 0) {
-    set_status(a.status, kDevTimeout, kSiteDecode);
   }
   if (warp == C::kWarps && n > 0) {
     fence_after();

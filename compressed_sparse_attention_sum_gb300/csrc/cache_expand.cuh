@@ -104,30 +104,41 @@ __device__ __forceinline__ uint4 natural8(const uint32_t (&o)[4]) {
                       __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[2], o[3], 0x7632));
 }
 
-// A scale group -> four 16-byte chunks (ch0 .. ch0 + 3) of a row of 128 bytes
-// in the 128-byte swizzle (row & 7 = sw).  With NORM returns the sum of its
-// squares, added in bf16 (16 to an accumulator: within 4% below and above).
-template <int BITS, bool NORM = false>
-__device__ __forceinline__ float expand_group(const Codes<BITS>& c, unsigned char* row, int ch0,
-                                              int sw) {
+// A scale group (32 channels) -> 16 words of two bf16, in permuted order.
+template <int BITS>
+__device__ __forceinline__ void expand_words(const Codes<BITS>& c, uint32_t (&o)[16]) {
   const uint32_t words[8] = {c.w[0].x, c.w[0].y, c.w[0].z, c.w[0].w,
                              c.w[BITS / 4 - 1].x, c.w[BITS / 4 - 1].y, c.w[BITS / 4 - 1].z,
                              c.w[BITS / 4 - 1].w};
-  __nv_bfloat162 sq = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t o[4];
-    if constexpr (BITS == 4) expand8<4>(words[j], 0u, o);
-    else expand8<8>(words[2 * j], words[2 * j + 1], o);
-    scale8<BITS>(c.scale, o);
-    *reinterpret_cast<uint4*>(row + (((ch0 + j) ^ sw) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-    if constexpr (NORM) {
+    uint32_t v[4];
+    if constexpr (BITS == 4) expand8<4>(words[j], 0u, v);
+    else expand8<8>(words[2 * j], words[2 * j + 1], v);
+    scale8<BITS>(c.scale, v);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&o[x]);
-        sq = __hfma2(v, v, sq);
-      }
-    }
+    for (int x = 0; x < 4; ++x) o[4 * j + x] = v[x];
+  }
+}
+
+// Those words as four 16-byte chunks (ch0 .. ch0 + 3) of a row of 128 bytes in
+// the 128-byte swizzle (row & 7 = sw).
+__device__ __forceinline__ void store_words(const uint32_t (&o)[16], unsigned char* row, int ch0,
+                                            int sw) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(row + (((ch0 + j) ^ sw) << 4)) =
+        make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+}
+
+// The sum of their squares, added in bf16 (16 to an accumulator: within 4%
+// below and above).
+__device__ __forceinline__ float words_norm2(const uint32_t (&o)[16]) {
+  __nv_bfloat162 sq = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&o[x]);
+    sq = __hfma2(v, v, sq);
   }
   const float2 f = __bfloat1622float2(sq);
   return f.x + f.y;

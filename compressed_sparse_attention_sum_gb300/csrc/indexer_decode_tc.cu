@@ -157,8 +157,10 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
 #pragma unroll
     for (int k = 0; k < C::kKpt; ++k) {
       const int key = ckey + k * C::kPass;
-      float s = expand_group<BITS, true>(cd[k], sm + C::K + (cg >> 1) * kBlk + key * 128,
-                                         (cg & 1) * 4, key & 7);
+      uint32_t o[16];
+      expand_words<BITS>(cd[k], o);
+      store_words(o, sm + C::K + (cg >> 1) * kBlk + key * 128, (cg & 1) * 4, key & 7);
+      float s = words_norm2(o);
       // squares of groups below 2^-40 may underflow
       if (cd[k].scale < 87u) s = fmaxf(s, 32.f * (BITS == 4 ? 36.f : 448.f * 448.f) * 0x1p-80f);
 #pragma unroll
