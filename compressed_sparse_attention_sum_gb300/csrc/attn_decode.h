@@ -96,14 +96,20 @@ inline DecodePlan decode_plan_simt(int b, int s_q, int H, int window, long long 
 
 inline bool decode_tc_width(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
 
-// CTAs of the tensor-core kernel that fit an SM (registers: 9 or 17 warps).
-constexpr int decode_tc_resident(int d, int cols) { return d <= 128 && cols == 32 ? 2 : 1; }
+// CTAs of the tensor-core kernel that the GPU holds at once, one on an SM, in
+// clusters of a size (a cluster stays within a GPC: what
+// cudaOccupancyMaxActiveClusters answers on a GB300).  Two on an SM, with 80
+// registers a thread, were slower: 64 queries of 32 x 128 in 14.7 us, not 12.1.
+inline long long decode_tc_capacity(int cluster) {
+  return cluster <= 2 ? 152 : cluster == 4 ? 144 : 120;
+}
 
 // Without an index list the queries of a sequence see the same rows (all but
-// the newest), so as many of them as fit 64 columns share a CTA.  The slots go
-// to one CTA per tile of 128 as long as the GPU holds them at once: up to eight
-// in a cluster, more in several clusters.
-inline DecodePlan decode_plan_tc(int b, int s_q, int H, int d, int window, int K, bool dense,
+// the newest), so as many of them as fit 64 columns share a CTA.  The tiles of
+// 128 slots go to a cluster of up to eight CTAs, as long as the GPU holds all
+// of them at once (a second wave doubles the time), and where it holds twelve
+// a query or more to several clusters of four, joined by a second kernel.
+inline DecodePlan decode_plan_tc(int b, int s_q, int H, int window, int K, bool dense,
                                  long long cmp_cap) {
   DecodePlan p{};
   p.per_group = dense && H % 16 == 0 && H <= 32 ? 64 / H : 1;
@@ -113,11 +119,19 @@ inline DecodePlan decode_plan_tc(int b, int s_q, int H, int d, int window, int K
   p.head_groups = p.per_group > 1 ? 1 : (H + p.cols - 1) / p.cols;
   const long long slots = window + p.per_group - 1 + (dense ? cmp_cap : K);
   const long long tiles = (slots + 127) / 128;
-  long long n = (long long)decode_tc_resident(d, p.cols) * kDecodeSms / ((long long)b * p.groups * p.head_groups);
-  n = n > tiles ? tiles : n;
+  const long long ctas = (long long)b * p.groups * p.head_groups;
+  const long long most = decode_tc_capacity(4) / ctas;   // CTAs of a query in clusters of four
   p.cluster = 1;
-  while (p.cluster < 8 && p.cluster < n) p.cluster *= 2;
-  p.parts = n < 16 ? 1 : (int)(n / 8);
+  p.parts = 1;
+  if (tiles > 8 && most >= 12) {
+    const long long n = most < tiles ? most : tiles;
+    p.cluster = 4;
+    p.parts = (int)((n + (most < tiles ? 0 : 3)) / 4);
+  } else {
+    while (p.cluster < 8 && p.cluster < tiles &&
+           ctas * p.cluster * 2 <= decode_tc_capacity(p.cluster * 2))
+      p.cluster *= 2;
+  }
   return p;
 }
 

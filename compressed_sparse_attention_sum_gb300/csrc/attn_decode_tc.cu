@@ -53,6 +53,7 @@ struct Cfg {
   static constexpr int kWarps = NC / 4;                    // lane quarter x 16 columns
   static constexpr int kCompute = kWarps * 32;
   static constexpr int kThreads = kCompute + 32;           // one more warp issues the MMAs
+  static constexpr int kBound = (kThreads + 127) / 128 * 128;   // registers are given out to four warps at a time
   static constexpr int kBlocks = D < 128 ? 2 : D / 64;     // 64-channel blocks of the KV tile
   static constexpr int kMT = D < 128 ? 1 : D / 128;        // M tiles of O^T
   static constexpr int kPart = kMT < 2 ? 1 : 2;            // M tiles whose channels are handed over at once
@@ -159,7 +160,7 @@ __device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned c
 }
 
 template <int D, int NC, int BITS>
-__global__ void __launch_bounds__(Cfg<D, NC>::kThreads, decode_tc_resident(D, NC)) attn_decode_tc_kernel(
+__global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
     const AttnDecodeArgs a, int per_group, int groups, int head_groups, int cs, int splits) {
   using C = Cfg<D, NC>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -185,7 +185,7 @@ size_t csa_attn_decode_workspace_size(int b, int s_q, int H, int d, int window, 
   int parts = csa::decode_plan_simt(b, s_q, H, window, cmp_rows).parts;
   if (csa::decode_tc_width(d)) {
     for (const bool dense : {false, true}) {
-      const int t = csa::decode_plan_tc(b, s_q, H, d, window, dense ? 0 : cmp_rows, dense, cmp_rows).parts;
+      const int t = csa::decode_plan_tc(b, s_q, H, window, dense ? 0 : cmp_rows, dense, cmp_rows).parts;
       parts = t > parts ? t : parts;
     }
   }
@@ -239,7 +239,7 @@ csa_status_t csa_attn_decode(const void* q, const void* cache, const int32_t* ra
   a.cs = csa::cache_shape(page_size, n_pages, d, bits);
   const bool tc = dt == CSA_BF16 && csa::decode_tc_width(d);
   const csa::DecodePlan plan =
-      tc ? csa::decode_plan_tc(b, s_q, H, d, window, K, idx == nullptr,
+      tc ? csa::decode_plan_tc(b, s_q, H, window, K, idx == nullptr,
                                (long long)P_cmp * page_size)
          : csa::decode_plan_simt(b, s_q, H, window, cmp_rows);
   const size_t need = csa_attn_decode_workspace_size(b, s_q, H, d, window, (int)cmp_rows);
