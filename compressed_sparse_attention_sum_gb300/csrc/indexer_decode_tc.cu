@@ -11,8 +11,11 @@
 // its row of S^T from TMEM and adds w_h ReLU(s) over those heads.
 //
 // What bounds it: expanding the codes and the weighted ReLU, in instructions
-// issued; four CTAs on an SM hide each other's latency.  The
-// tile's largest |k| and its range of scores go to the select.
+// issued; four CTAs on an SM hide each other's latency.  The tile's largest |k|
+// and its range of scores go to the select.  Counting all tiles through and
+// dealing them out evenly was slower (16 sequences 36 -> 42 us with the select:
+// the count costs every CTA more than the uneven lengths do), as was a CTA of
+// 128 threads, one a key.
 #include "cache_expand.cuh"
 #include "indexer_decode.h"
 #include "smem_once.h"
@@ -50,7 +53,7 @@ struct Cfg {
   static constexpr uint32_t MISC = BAR + 8;              // TMEM slot, dead
   static constexpr uint32_t BND = MISC + 8;              // [2][8], by tile parity
   static constexpr uint32_t RNG = BND + 64;              // [NC / 16][4] score ranges of the warps
-  static constexpr uint32_t SUM = RNG + NC / 16 * 32;    // [2][NC / 16][128] sums over half the heads
+  static constexpr uint32_t SUM = RNG + NC / 16 * 32;    // [2][NC / 16][128] half the heads' sums
   static constexpr uint32_t kBytes = SUM + 2 * (NC / 16) * kIdxTile * 4;
 };
 

@@ -158,40 +158,26 @@ __device__ __forceinline__ unsigned long long pair_key(float2 a) {
 }
 
 // The dot product of n channels of q and k: a product is split by an fma (exact
-// already for bf16 q), a sum by the exact error of an addition.  The first four
-// 16-byte words of q come in registers, read ahead of the keys.
-constexpr int kQAhead = 4;
+// already for bf16 q), a sum by the exact error of an addition.  Eight channels
+// a step and no more unrolling: the code runs once a row, and fetching
+// instructions would take longer than the loop.
 template <typename T>
-__device__ __forceinline__ float2 dot_pair(const uint4 (&ahead)[kQAhead], const T* q,
-                                           const float* k, int n) {
+__device__ __forceinline__ float2 dot_pair(const T* q, const float* k, int n) {
   float hi = 0.f, lo = 0.f;
-  constexpr int kPer = 16 / sizeof(T);
-  auto add = [&](uint4 u, const float* kc) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float kv[kPer];
+#pragma unroll 1
+  for (int c = 0; c < n; c += 8) {
+    float qv[8], kv[8];
+    load8(q + c, qv);
+    load8(k + c, kv);
 #pragma unroll
-    for (int e = 0; e < kPer; e += 4)
-      *reinterpret_cast<float4*>(kv + e) = *reinterpret_cast<const float4*>(kc + e);
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      float qv;
-      if constexpr (sizeof(T) == 2)
-        qv = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-      else
-        qv = __uint_as_float(w[e]);
-      const float p = __fmul_rn(qv, kv[e]);
-      if (sizeof(T) == 4) lo += __fmaf_rn(qv, kv[e], -p);
+    for (int e = 0; e < 8; ++e) {
+      const float p = __fmul_rn(qv[e], kv[e]);
+      if (sizeof(T) == 4) lo += __fmaf_rn(qv[e], kv[e], -p);
       const float s = __fadd_rn(hi, p), t = __fsub_rn(s, hi);
       lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t));
       hi = s;
     }
-  };
-#pragma unroll
-  for (int c = 0; c < kQAhead; ++c)
-    if (c * kPer < n) add(ahead[c], k + c * kPer);
-#pragma unroll 1
-  for (int c = kQAhead; c * kPer < n; ++c)
-    add(reinterpret_cast<const uint4*>(q)[c], k + c * kPer);
+  }
   return pair_add(make_float2(hi, 0.f), make_float2(lo, 0.f));
 }
 
@@ -208,25 +194,31 @@ __device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long r
   const int mine = warp / wpb, h = (warp - mine * wpb) * 8 + (lane >> 2), part = lane & 3;
   const int n4 = a.d / 4, pitch = a.d + 16;
   const T* qh = (const T*)a.q + (row * a.H + h0 + min(h, max(nh - 1, 0))) * a.d + part * n4;
-  uint4 ahead[kQAhead];
-  float w = 0.f;
-  if (h < nh) {
-#pragma unroll
-    for (int c = 0; c < kQAhead; ++c)
-      ahead[c] = reinterpret_cast<const uint4*>(qh)[c * (16 / (int)sizeof(T)) < n4 ? c : 0];
-    w = a.w[row * a.H + h0 + h];
-  }
+  const float w = h < nh ? a.w[row * a.H + h0 + h] : 0.f;
   for (int e0 = 0; e0 < m; e0 += per) {
     const int n = min(per, m - e0);
-    for (int x = tid; x < n * (a.d / 8); x += kSel) {
-      const int s = x / (a.d / 8), c0 = (x - s * (a.d / 8)) * 8;
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // eight channels a thread: at most 32 keys of 256
+    const int s = tid / (a.d / 8), c0 = (tid - s * (a.d / 8)) * 8;
+    uint2 code = make_uint2(0u, 0u);
+    uint32_t scale = 0;
+    if (s < n) {
       const int j = block(e0 + s), pg = page(e0 + s);
       if ((unsigned)pg < (unsigned)a.cs.n_pages) {       // recorded by the score kernel
         const int r = j - page_index(a.cs, j) * a.cs.page_size;
         const uint8_t* base = a.cache + page_base(a.cs, pg);
-        cache_load8<BITS>(base + row_code(a.cs, r), scale_value(base[row_scale(a.cs, r) + c0 / 32]),
-                          c0, v);
+        const uint8_t* src = base + row_code(a.cs, r) + c0 * BITS / 8;
+        if constexpr (BITS == 4) code.x = __ldg(reinterpret_cast<const uint32_t*>(src));
+        else code = __ldg(reinterpret_cast<const uint2*>(src));
+        scale = __ldg(base + row_scale(a.cs, r) + c0 / 32);
+      }
+    }
+    if (s < n) {
+      const float f = scale_value(scale);
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (BITS == 4) v[k] = code_e2m1(code.x >> (4 * k)) * f;
+        else v[k] = code_e4m3((k < 4 ? code.x : code.y) >> (8 * (k & 3))) * f;
       }
       // quarters four banks apart: the lanes of a head read all four at once
       store8(k_s + s * pitch + c0 + c0 / n4 * 4, v);
@@ -234,18 +226,18 @@ __device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long r
     __syncthreads();
     if (mine < n) {                                      // warp-uniform
       float2 x = make_float2(0.f, 0.f);
-      if (h < nh) x = dot_pair<T>(ahead, qh, k_s + mine * pitch + part * (n4 + 4), n4);
-      x = pair_add(x, pair_shfl(x, 1));
-      x = pair_add(x, pair_shfl(x, 2));
-      x = x.x > 0.f ? pair_mul(x, w) : make_float2(0.f, 0.f);   // hi carries the sum's sign
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) x = pair_add(x, pair_shfl(x, o));
+      if (h < nh) x = dot_pair(qh, k_s + mine * pitch + part * (n4 + 4), n4);
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {                 // the quarters, then the heads
+        x = pair_add(x, pair_shfl(x, o));
+        if (o == 2) x = x.x > 0.f ? pair_mul(x, w) : make_float2(0.f, 0.f);   // hi has the sum's sign
+      }
       if (lane == 0) sh.pair[warp] = x;
     }
     __syncthreads();
     if (warp < n) {                                      // block `warp` of the round
       float2 x = lane < wpb ? sh.pair[warp * wpb + lane] : make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
       for (int o = 1; o < 16; o <<= 1) x = pair_add(x, pair_shfl(x, o));
       if (lane == 0) store(e0 + warp, x);
     }
@@ -373,6 +365,12 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   const bool is_staged = seg <= staged_cap;              // the same in every CTA
   // chosen blocks of this part, a bit each
   uint32_t* bits = is_staged ? bitmap : reinterpret_cast<uint32_t*>(a.list + row * a.slots) + j0 / 32;
+  float v0[8];                                           // the first scores, in flight with the tiles' data
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int j = e * kSel + tid;
+    v0[e] = j < n ? score[j0 + j] : 0.f;
+  }
   float kmax = 0.f, mn = INFINITY, mx = -INFINITY;
   for (int t = tid; t * kIdxTile < vis; t += kSel) {
     const float4 v = a.tile_info[row * a.tiles + t];
@@ -440,7 +438,7 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int j = jb + e * kSel + tid;
-      v[e] = j < n ? score[j0 + j] : 0.f;
+      v[e] = jb == 0 ? v0[e] : j < n ? score[j0 + j] : 0.f;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -504,25 +502,39 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     c = block_count(sh, c);
     if (tid == 0) sh.n[1] = c;
     cluster_sync<CS>();
+    // every CTA's counts, and with them the first entries of its list: more than
+    // kAhead of them are read in a second step
     int2 pn[CS];
+    constexpr int kAhead = kSel / CS < kList ? kSel / CS : kList;
+    const int ar = min(tid / kAhead, CS - 1), ai = tid - ar * kAhead;
+    const uint32_t akey = ai < kAhead ? peer<CS>(sh.list_key, ar)[ai] : 0u;
+    const int aj = ai < kAhead ? peer<CS>(sh.list_j, ar)[ai] : 0;
 #pragma unroll
     for (int r = 0; r < CS; ++r) pn[r] = *reinterpret_cast<const int2*>(peer<CS>(sh.n, r));
     m = above = before_me = 0;
-    int at = 0, from = -1;                               // entry tid: of CTA `from`, its entry `at`
+    int at = 0, from = -1, place = -1;                   // entry tid: of CTA `from`, its entry `at`
+    bool more = false;
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
       if (tid >= m && tid < m + pn[r].x) {
         from = r;
         at = tid - m;
       }
+      if (r == ar && ai < min(pn[r].x, kAhead)) place = m + ai;
+      more |= pn[r].x > kAhead;
       m += pn[r].x;
       above += pn[r].y;
       if (r < rank) before_me += pn[r].y;
     }
     if (m <= kList) {
-      if (tid < kList) {
-        sh.all_key[tid] = from >= 0 ? peer<CS>(sh.list_key, max(from, 0))[at] : 0u;
-        sh.all_j[tid] = from >= 0 ? peer<CS>(sh.list_j, max(from, 0))[at] : -1;
+      if (tid < kList && tid >= m) sh.all_key[tid] = 0u;
+      if (place >= 0) {
+        sh.all_key[place] = akey;
+        sh.all_j[place] = aj;
+      }
+      if (more && from >= 0 && at >= kAhead) {
+        sh.all_key[tid] = peer<CS>(sh.list_key, max(from, 0))[at];
+        sh.all_j[tid] = peer<CS>(sh.list_j, max(from, 0))[at];
       }
       __syncthreads();
       break;
@@ -553,6 +565,13 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     const float tval = order_value(tkey);
     const uint32_t clo = min(tkey, order_key(tval - eps2)), chi = max(tkey, order_key(tval + eps2));
     const bool sure = tid < m && x > chi, close = tid < m && x >= clo && x <= chi;
+    if (close && (unsigned)page < (unsigned)a.cs.n_pages) {
+      // the key's bytes, on their way while the close blocks are counted
+      const int r = j - page_index(a.cs, j) * a.cs.page_size;
+      const uint8_t* base = a.cache + page_base(a.cs, page);
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(base + row_code(a.cs, r)));
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(base + row_scale(a.cs, r)));
+    }
     const unsigned sm = __ballot_sync(0xffffffffu, sure), cm = __ballot_sync(0xffffffffu, close);
     if (lane == 0) {
       sh.warp_n[warp] = __popc(sm);
@@ -570,20 +589,27 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     __syncthreads();
     bool in = sure;
     if (need < mc && eps2 > 0.f) {
-      // every CTA scores all close blocks over its share of the heads
-      const int share = (a.H + CS - 1) / CS, h0 = min(rank * share, a.H);
+      // Every CTA scores all close blocks itself where one round of its warps
+      // does, otherwise over its share of the heads.
+      const bool whole = CS == 1 || mc * ((a.H + 7) / 8) <= kSelWarps;
+      const int share = whole ? a.H : (a.H + CS - 1) / CS, h0 = whole ? 0 : min(rank * share, a.H);
       score_exact<T, BITS>(sh, a, row, k_s, mc, h0, min(share, a.H - h0),
                            [&](int e) { return sh.close_j[e]; },
                            [&](int e) { return sh.close_page[e]; },
                            [&](int e, float2 v) { sh.exact[e] = v; });
-      cluster_sync<CS>();
-      if (tid < mc) {
-        float2 v[CS];
+      if (whole) {
+        __syncthreads();
+        if (tid < mc) sh.all_exact[tid] = pair_key(sh.exact[tid]);
+      } else {
+        cluster_sync<CS>();
+        if (tid < mc) {
+          float2 v[CS];
 #pragma unroll
-        for (int r = 0; r < CS; ++r) v[r] = peer<CS>(sh.exact, r)[tid];
+          for (int r = 0; r < CS; ++r) v[r] = peer<CS>(sh.exact, r)[tid];
 #pragma unroll
-        for (int r = 1; r < CS; ++r) v[0] = pair_add(v[0], v[r]);
-        sh.all_exact[tid] = pair_key(v[0]);
+          for (int r = 1; r < CS; ++r) v[0] = pair_add(v[0], v[r]);
+          sh.all_exact[tid] = pair_key(v[0]);
+        }
       }
     } else {
       // all of them, or blocks whose scores are exactly equal
