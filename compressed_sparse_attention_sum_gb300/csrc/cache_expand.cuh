@@ -16,7 +16,7 @@ namespace csa {
 
 // A row of zeros, read in the place of a masked one: with an address chosen
 // instead of a branch, a load stays in flight until its value is used.
-static __device__ uint4 g_zero_row[32];
+static __device__ __align__(32) uint4 g_zero_row[32];
 
 template <int BITS>
 __device__ __forceinline__ int channel_of(int p) {

@@ -123,6 +123,44 @@ def test_write_bytes_and_read_back(case):
                 assert np.array_equal(got[i, r, :d], want_row), (i, r)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d", [64, 96, 512])
+def test_long_ranges_equal_short_ones(bits, d):
+    """The kernels of long ranges (several rows a thread, 8 or 16 channels by
+    alignment) write and read what the same rows in short calls do."""
+    rng = np.random.default_rng(d)
+    b, page, s = 2, 48, 2500 * 256 // (d // 8) // 2 + 77
+    P = -(-s // page) + 1
+    n_pages, (table,) = tables(rng, b, P)
+    table, pos0 = dev(table), dev(np.array([5, 41], np.int32))
+    counts = dev(np.array([s, s - 130], np.int32))
+    g = torch.Generator(device="cuda").manual_seed(d)
+    buf = torch.randn(b, s + 1, d + 8, generator=g, device="cuda").to(BF) * 3
+    want = empty_cache(n_pages, page, d, bits)
+    x = buf[:, :s, :d].contiguous()
+    for at in range(0, s, 999):
+        n = min(999, s - at)
+        serve.csa_cache_write(x[:, at:at + n], want, table, pos0 + at, page, bits,
+                              counts=(counts - at).clamp(min=0, max=n))
+    for rows in (x, buf[:, :s, :d], x.float()):        # 32-byte boundaries, 16-byte ones, fp32
+        cache = empty_cache(n_pages, page, d, bits)
+        serve.csa_cache_write(rows, cache, table, pos0, page, bits, counts=counts)
+        assert torch.equal(cache, want)
+    ref = torch.full((b, s, d), 7.0, dtype=BF, device="cuda")
+    for at in range(0, s, 999):
+        n = min(999, s - at)
+        serve.csa_cache_read(want, table, pos0 + at, ref[:, at:at + n], page, bits,
+                             counts=(counts - at).clamp(min=0, max=n))
+    assert bool((ref[1, s - 130:] == 7.0).all())
+    wide = torch.full((b, s, d), 7.0, dtype=BF, device="cuda")
+    odd = torch.full((b, s, d + 8), 7.0, dtype=BF, device="cuda")
+    single = torch.full((b, s, d), 7.0, device="cuda")
+    for out in (wide, odd[..., :d], single):
+        serve.csa_cache_read(want, table, pos0, out, page, bits, counts=counts)
+        assert torch.equal(out.to(BF), ref)
+    assert bool((odd[..., d:] == 7.0).all())
+
+
 def test_bad_pages_and_counts_are_skipped_and_recorded():
     bits, d, page = 4, 64, 16
     rng = np.random.default_rng(0)
