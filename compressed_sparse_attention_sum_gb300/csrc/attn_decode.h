@@ -139,6 +139,8 @@ inline DecodePlan decode_plan_tc(int b, int s_q, int H, int window, int K, bool 
 cudaError_t launch_attn_decode_combine(const AttnDecodeArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_attn_decode_simt(const AttnDecodeArgs& a, bool bf16, int bits,
                                     cudaStream_t st);
+cudaError_t launch_attn_decode_512(const AttnDecodeArgs& a, const DecodePlan& p, int bits,
+                                   cudaStream_t st);
 cudaError_t launch_attn_decode_tc(const AttnDecodeArgs& a, const DecodePlan& p, int bits,
                                   cudaStream_t st);
 

@@ -1,5 +1,6 @@
 // csa_attn_decode on the 5th-generation tensor cores (tcgen05 + TMEM): bf16
-// queries, d in {64, 128, 256, 512}, cache of 4 or 8 bits.
+// queries, d in {64, 128, 256, 512}, cache of 4 or 8 bits (d = 512 with more than
+// 32 columns: attn_decode_512.cu).
 //
 // Of one query, H rows of Q meet a few hundred to a thousand cached rows: the
 // heads alone would fill a quarter to half of an M = 128 tile, so the products
@@ -22,30 +23,22 @@
 // (cache_expand.cuh): Q is permuted alike, and O is put back where it is
 // stored.
 //
-// What bounds it: at 64 heads x 512 the shared memory (a tile is written once
-// and read twice by the tensor core, whose N = 64 leaves A's reads 1.5 times
-// as long as the products); at 32 x 128 the latency of the chain index - page
-// - codes - S - softmax - O - join.  The arithmetic follows attn_fwd_tc512:
+// What bounds it: the latency of the chain index - page - codes - S - softmax -
+// O - join (64 queries of 32 x 128, 8 bits: 11.7 us, 5 tiles each).  The
+// arithmetic follows attn_fwd_tc512:
 // probabilities in bf16 (a weight of the values, which the sum of 2^-9
 // relative errors of both signs moves by less than the rounding of o), their
 // sum and the running maximum in fp32, rescaling only when a column's maximum
 // grows by more than 2^8.
-#include <cooperative_groups.h>
-
 #include "attn_decode.h"
+#include "attn_decode_join.cuh"
 #include "cache_expand.cuh"
 #include "smem_once.h"
-#include "tcgen05.cuh"
 
 namespace csa {
 namespace adt {
 
-using namespace csa::umma;
-namespace cg = cooperative_groups;
-
 constexpr int kSlots = 128;
-constexpr float kRescale = 8.f;
-constexpr int kSiteDecode = 0x73;
 constexpr uint32_t kKvBlk = kSlots * 128;     // 64 channels of 128 slots
 
 template <int D, int NC>
@@ -78,86 +71,8 @@ struct Cfg {
   static constexpr uint32_t SINK = ML + NC * 8;            // [NC] sink logits of the heads (log2 units)
   static constexpr uint32_t OKS = SINK + NC * 4;           // [2][kSlots] bytes
   static constexpr uint32_t kBytes = OKS + 2 * kSlots;
-  static constexpr uint32_t STAGE = KV;                    // [NC][D] O after the last tile: fp32, or
-                                                           // bf16 where this CTA has the whole query
+  static constexpr uint32_t STAGE = KV;                    // [NC][D] O after the last tile
 };
-
-// Transposing butterfly: v[c] holds this lane's value of column c; afterwards
-// lanes l and l + 16 hold op over all 32 lanes of column l % 16.
-template <bool kMax>
-__device__ __forceinline__ float lane_reduce16(float (&v)[16]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int off = 8, n = 8; off >= 1; off >>= 1, n >>= 1) {
-    const bool up = (lane & off) != 0;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = up ? v[i] : v[i + n];
-      const float keep = up ? v[i + n] : v[i];
-      const float recv = __shfl_xor_sync(0xffffffffu, send, off);
-      v[i] = kMax ? fmaxf(keep, recv) : keep + recv;
-    }
-  }
-  const float other = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return kMax ? fmaxf(v[0], other) : v[0] + other;
-}
-
-// Joins the (m, l, O) of the CS CTAs of a cluster for this CTA's share of the
-// columns, from their shared memory, four channels a thread: all of its reads
-// are in flight at once.  final: also the sink, o and lse; otherwise the
-// cluster's entry of the partial results.
-template <int D, int NC, int CS>
-__device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned char* sm, int rank,
-                                             int part, int per_group, int nq, int heads, int h0,
-                                             long long row0) {
-  using C = Cfg<D, NC>;
-  constexpr int kCols = NC / CS;                           // columns of this CTA
-  const bool final = a.parts == 1;
-  const float* sink = reinterpret_cast<const float*>(sm + C::SINK);
-  const unsigned char* base[CS];
-#pragma unroll
-  for (int r = 0; r < CS; ++r) base[r] = cg::this_cluster().map_shared_rank(sm, r);
-  for (int e = threadIdx.x; e < kCols * (D / 4); e += C::kThreads) {
-    const int col = rank * kCols + e / (D / 4), c = e % (D / 4) * 4;
-    float2 ml[CS];
-    float4 v[CS];
-#pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      ml[r] = *reinterpret_cast<const float2*>(base[r] + C::ML + col * 8);
-      v[r] = *reinterpret_cast<const float4*>(base[r] + C::STAGE + (col * D + c) * 4);
-    }
-    const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
-    if (qi >= nq || h >= heads) continue;
-    const float sink2 = final ? sink[h] : -INFINITY;
-    float m = sink2, total = 0.f;
-#pragma unroll
-    for (int r = 0; r < CS; ++r) m = fmaxf(m, ml[r].x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int r = 0; r < CS; ++r) {
-      if (ml[r].y > 0.f) {                                 // a CTA without a tile has no O
-        const float f = ex2(ml[r].x - m);
-        total = fmaf(ml[r].y, f, total);
-        acc.x = fmaf(v[r].x, f, acc.x);
-        acc.y = fmaf(v[r].y, f, acc.y);
-        acc.z = fmaf(v[r].z, f, acc.z);
-        acc.w = fmaf(v[r].w, f, acc.w);
-      }
-    }
-    const long long row = row0 + qi;
-    if (!final) {
-      const long long at = (row * a.parts + part) * a.H + h0 + h;
-      *reinterpret_cast<float4*>(a.part_o + at * D + c) = acc;
-      if (c == 0) a.part_ml[at] = make_float2(m, total);
-      continue;
-    }
-    if (sink2 > -INFINITY) total += ex2(sink2 - m);
-    const float inv = total > 0.f ? __fdividef(1.f, total) : 0.f;
-    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + (row * a.H + h0 + h) * D + c) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (c == 0) a.lse[row * a.H + h0 + h] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
-  }
-}
 
 template <int D, int NC, int BITS>
 __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
@@ -178,7 +93,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   float2* ml = reinterpret_cast<float2*>(sm + C::ML);
   unsigned char* oks = sm + C::OKS;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // blockIdx.x: group of queries (per_group of one sequence) and of heads, and
   // its split of the slots (the cs CTAs of a cluster are neighbours)
   const int group = (int)blockIdx.x / splits, split = (int)blockIdx.x - group * splits;
@@ -227,8 +143,8 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   const int ring0 = w0 >= 0 ? w0 % ring : ring - 1 - (int)((unsigned)(-1 - w0) % (unsigned)ring);
   const int slots = last.t < 0 ? 0 : wext + (a.idx != nullptr ? a.K : last.vis);
   const int tiles = (slots + kSlots - 1) / kSlots;
-  const int it0 = (int)((long long)tiles * split / splits);
-  const int n = (int)((long long)tiles * (split + 1) / splits) - it0;
+  const int it0 = (unsigned)tiles * (unsigned)split / (unsigned)splits;   // tiles <= 2^18, splits <= 152
+  const int n = (int)((unsigned)tiles * (unsigned)(split + 1) / (unsigned)splits) - it0;
 
   if (tid == 0) {
     mbar_init(bar_s, 1);
@@ -341,11 +257,13 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   fence_after();
   const uint32_t tmem = n > 0 ? *tmem_slot : 0u;
 
-  // A wait that gives up ends every later wait of the CTA at once.
+  // A wait that gives up ends every later wait of the CTA.
+  bool gone = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (*dead) return false;
-    if (mbar_wait(bar, parity)) return true;
+    if (gone) return false;
+    if (mbar_try(bar, parity) || (!*dead && mbar_wait(bar, parity))) return true;
     *dead = 1;
+    gone = true;
     return false;
   };
 
@@ -355,45 +273,53 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
     // one.  The proxy fence between stands on this side of the barriers, where one
     // thread executes it: it has to lie on the path from the write to the read, and
     // executed by all 16 writing warps it takes about 600 cycles each time.
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32_major(kSlots, NC, 0, 0);
-      constexpr uint32_t idesc_o = idesc_bf16_f32_major(128, NC, 1, 1);
-      const uint32_t kva = smem_addr(sm + C::KV), qa = smem_addr(sm + C::Q);
-      const uint32_t pa = smem_addr(sm + C::P);
-      constexpr int kSteps = D < 128 ? D / 16 : 8;        // K steps of S^T in one M tile
-      for (int it = 0; it < n; ++it) {
-#pragma unroll 1
-        for (int x = 0; x < C::kParts; ++x) {
-          if (!wait(&bar_kv[x], it & 1)) break;
-          fence_proxy_async_smem();
-          fence_after();
+    constexpr uint32_t idesc_s = idesc_bf16_f32_major(kSlots, NC, 0, 0);
+    constexpr uint32_t idesc_o = idesc_bf16_f32_major(128, NC, 1, 1);
+    const uint64_t kvd = sw128_desc(smem_addr(sm + C::KV)), qd_s = sw128_desc(smem_addr(sm + C::Q));
+    const uint64_t kvd_mn = sw128_desc_mn(smem_addr(sm + C::KV), kKvBlk);
+    const uint64_t pd_mn = sw128_desc_mn(smem_addr(sm + C::P), kKvBlk);
+    const uint32_t td = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+    };
+    constexpr int kSteps = D < 128 ? D / 16 : 8;          // K steps of S^T in one M tile
+    bool up = true;
+    for (int it = 0; up && it < n; ++it) {
+#pragma unroll
+      for (int x = 0; x < C::kParts; ++x) {
+        up = up && wait_warp(&bar_kv[x], it & 1);
+        fence_proxy_async_smem();
+        fence_after();
+        if (up && elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kSteps * C::kPart; ++kk) {
             const int k = x * 8 * C::kPart + kk;
-            mma_bf16_ss(tmem, sw128_desc(kva + (k >> 2) * kKvBlk + (k & 3) * 32),
-                        sw128_desc(qa + (k >> 2) * C::kQBlk + (k & 3) * 32), idesc_s,
+            mma_bf16_ss(td, kvd + (((k >> 2) * kKvBlk + (k & 3) * 32) >> 4),
+                        qd_s + (((k >> 2) * C::kQBlk + (k & 3) * 32) >> 4), idesc_s,
                         k > 0 ? 1u : 0u);
           }
+          if (x == C::kParts - 1) mma_commit(bar_s);
         }
-        if (*dead) break;
-        mma_commit(bar_s);
-        if (!wait(bar_p, it & 1)) break;
-        fence_proxy_async_smem();
-        fence_after();
-#pragma unroll 1
+        __syncwarp();
+      }
+      up = up && wait_warp(bar_p, it & 1);
+      fence_proxy_async_smem();
+      fence_after();
+      if (up && elect_one()) {
+#pragma unroll
         for (int x = 0; x < C::kParts; ++x) {
 #pragma unroll
           for (int mm = 0; mm < C::kPart; ++mm) {
             const int m = x * C::kPart + mm;
 #pragma unroll
             for (int k = 0; k < kSlots / 16; ++k)
-              mma_bf16_ss(tmem + C::kColO + m * NC,
-                          sw128_desc_mn(kva + 2 * m * kKvBlk + k * 2048, kKvBlk),
-                          sw128_desc_mn(pa + k * 2048, kKvBlk), idesc_o, (it > 0 || k > 0) ? 1u : 0u);
+              mma_bf16_ss(td + C::kColO + m * NC, kvd_mn + ((2 * m * kKvBlk + k * 2048) >> 4),
+                          pd_mn + ((k * 2048) >> 4), idesc_o, (it > 0 || k > 0) ? 1u : 0u);
           }
           mma_commit(&bar_o[x]);
         }
       }
+      __syncwarp();
     }
     __syncwarp();
   } else if (n > 0) {
@@ -564,7 +490,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
     } else if (tid < NC) {
       ml[tid] = mine;
     }
-    // O^T into shared memory as [column][channel]: the KV tile's place
+    // O^T to o or into shared memory as [column][channel]: the KV tile's place
     if (!*dead) {
 #pragma unroll 1
       for (int m = 0; m < C::kMT; ++m) {
@@ -572,14 +498,11 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
         uint32_t v[16];
         tmem_ld16_wait(tmem + lane_base + C::kColO + m * NC + hq * 16, v);
         if (p < D) {
-          const int ch = channel_of<BITS>(p);
           if (cs == 1) {
-            __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sm + C::STAGE);
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              stage[(hq * 16 + c) * D + ch] =
-                  __float2bfloat16_rn(__uint_as_float(v[c]) * m_run[hq * 16 + c]);
+            store_o16<D, BITS>(v, m_run, hq * 16, nq * heads,
+                               (__nv_bfloat16*)a.o + (row0 * a.H + h0) * D, p);
           } else {
+            const int ch = channel_of<BITS>(p);
             float* stage = reinterpret_cast<float*>(sm + C::STAGE);
 #pragma unroll
             for (int c = 0; c < 16; ++c) stage[(hq * 16 + c) * D + ch] = __uint_as_float(v[c]);
@@ -592,28 +515,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   // ---- join ----------------------------------------------------------------------
   if (cs > 1) cg::this_cluster().sync();
   else __syncthreads();
-  if (*dead) {
-    if (tid == 0) set_status(a.status, kDevTimeout, kSiteDecode);
-  } else if (cs == 1) {
-    // the columns' rows of o lie one behind the other
-    uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + (row0 * a.H + h0) * D);
-    const uint4* src = reinterpret_cast<const uint4*>(sm + C::STAGE);
-    const int chunks = nq * heads * (D / 8);
-#pragma unroll 4
-    for (int e = tid; e < chunks; e += C::kThreads)
-      dst[e] = n > 0 ? src[e] : make_uint4(0u, 0u, 0u, 0u);
-    if (n == 0 && tid < nq * heads) {                      // nothing to attend to
-      const int qi = tid / heads, h = tid - qi * heads;
-      a.lse[(row0 + qi) * a.H + h0 + h] = a.sink != nullptr ? a.sink[h0 + h] : -INFINITY;
-    }
-  } else {
-    const int part = split / cs;
-    switch (cs) {
-      case 2: join_cluster<D, NC, 2>(a, sm, rank, part, per_group, nq, heads, h0, row0); break;
-      case 4: join_cluster<D, NC, 4>(a, sm, rank, part, per_group, nq, heads, h0, row0); break;
-      default: join_cluster<D, NC, 8>(a, sm, rank, part, per_group, nq, heads, h0, row0); break;
-    }
-  }
+  finish_decode<C, D, NC>(a, sm, *dead != 0, n, cs, rank, split, per_group, nq, heads, h0, row0);
   if (warp == C::kWarps && n > 0) {
     fence_after();
     tmem_dealloc(tmem, C::kTmem);
@@ -664,7 +566,9 @@ cudaError_t launch_tc_width(const AttnDecodeArgs& a, int bits, const DecodePlan&
     case 64: return launch_tc_bits<64, NC>(a, bits, p, st);
     case 128: return launch_tc_bits<128, NC>(a, bits, p, st);
     case 256: return launch_tc_bits<256, NC>(a, bits, p, st);
-    default: return launch_tc_bits<512, NC>(a, bits, p, st);
+    default:
+      if constexpr (NC == 64) return launch_attn_decode_512(a, p, bits, st);
+      else return launch_tc_bits<512, NC>(a, bits, p, st);
   }
 }
 

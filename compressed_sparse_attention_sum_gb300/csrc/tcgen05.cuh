@@ -54,6 +54,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// One try of it, for up to 20 us.
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y) {
   asm volatile(
@@ -92,6 +105,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
          | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
 
+// True in one lane of a converged warp, always the same one.  Products issued in
+// its branch, from descriptors that are the same in all lanes, follow one another
+// in 55 to 70 cycles; behind a comparison of the lane, in 110 to 130.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(p)::"memory");
+  return p != 0;
+}
+
 __device__ __forceinline__ void mma_bf16_ss(uint32_t tmem_d, uint64_t a, uint64_t b,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -99,6 +125,16 @@ __device__ __forceinline__ void mma_bf16_ss(uint32_t tmem_d, uint64_t a, uint64_
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A from TMEM: lane = row, a 32-bit column = two of its K elements.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Instruction descriptor of kind::f8f6f4 with e4m3 A and B (K-major), fp32 D.
@@ -223,6 +259,31 @@ __device__ __forceinline__ uint32_t tmem_ld1_wait(uint32_t taddr) {
                : "memory");
   asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(v)::"memory");
   return v;
+}
+
+// Twice 16 consecutive 32-bit TMEM columns of this thread's lane, with one wait.
+__device__ __forceinline__ void tmem_ld16_pair_wait(uint32_t ta, uint32_t (&r)[16], uint32_t tb,
+                                                    uint32_t (&s)[16]) {
+#define CSA_TMEM_LD16(t, r)                                                                        \
+  asm volatile(                                                                                    \
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"   \
+      "%14,%15}, [%16];"                                                                           \
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),        \
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),    \
+        "=r"(r[14]), "=r"(r[15])                                                                   \
+      : "r"(t))
+  CSA_TMEM_LD16(ta, r);
+  CSA_TMEM_LD16(tb, s);
+#undef CSA_TMEM_LD16
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(s[0]), "+r"(s[1]),
+                 "+r"(s[2]), "+r"(s[3]), "+r"(s[4]), "+r"(s[5]), "+r"(s[6]), "+r"(s[7]),
+                 "+r"(s[8]), "+r"(s[9]), "+r"(s[10]), "+r"(s[11])
+               :
+               : "memory");
+  asm volatile("" : "+r"(s[12]), "+r"(s[13]), "+r"(s[14]), "+r"(s[15])::"memory");
 }
 
 // 16 consecutive 32-bit TMEM columns of this thread's lane, with the wait.
