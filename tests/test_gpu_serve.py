@@ -510,6 +510,52 @@ def test_attention_matches_oracle(case):
                       d ** -0.5, lens[s] - s_q + i, ratio, window, dtype)
 
 
+WIDE_CASES = [
+    # 512 channels and 33 to 64 columns: heads of one query, of several, in groups of 64
+    (2, 3, 16, 512, 4, 65, [515, 2], 0, 8, 16, BF, True),
+    (1, 2, 32, 512, 128, 128, [1300], 0, 4, 64, BF, False),
+    (2, 1, 96, 512, 4, 64, [300, 64], 40, 4, 16, BF, True),
+    (1, 1, 33, 512, 2, 17, [90], 70, 8, 48, BF, False),
+    (3, 2, 64, 512, 4, 200, [1, 0, 450], -1, 4, 64, BF, True),
+    (1, 1, 128, 512, 4, 1, [5], 0, 8, 16, BF, False),
+    (1, 5, 16, 512, 1, 3, [700], 0, 4, 32, BF, True),
+]
+
+
+@pytest.mark.parametrize("case", WIDE_CASES, ids=lambda c: f"b{c[0]}s{c[1]}H{c[2]}r{c[4]}K{c[7]}_{c[8]}bit")
+def test_attention_at_512_channels(case):
+    test_attention_matches_oracle(case)
+
+
+@pytest.mark.parametrize("H,d,s_q,K,bits", [(64, 512, 1, 1000, 4), (64, 512, 1, 0, 8), (16, 512, 4, 0, 4),
+                                             (32, 512, 1, 0, 4), (32, 128, 1, 1000, 8), (64, 256, 1, 0, 4)])
+def test_attention_whose_maximum_keeps_growing(H, d, s_q, K, bits):
+    """Rows along one direction, longer from slot to slot, up to logits of about
+    200: every tile's maximum is above those before, and the last few slots
+    have all the weight.  40 sequences: several tiles to a CTA."""
+    b, n = 40, 4400
+    case = (b, s_q, H, d, 4, 64, [n] * b, K, bits, 64, BF, True)
+    rng = np.random.default_rng(H + d + s_q)
+    n_pages, (raw_t, cmp_t) = tables(rng, b, 2, -(-(n // 4) // 64))
+    cache = empty_cache(n_pages, 64, d, bits)
+    u = np.sign(rng.standard_normal(d))
+    ramp = np.linspace(0.01, 1.0, n // 4)[:, None]
+    cmp = torch.from_numpy(ramp * u + 0.02 * rng.standard_normal((n // 4, d))).to(BF)[None]
+    raw = torch.from_numpy(0.01 * rng.standard_normal((128, d))).to(BF)[None]     # of the last positions
+    serve.csa_cache_write(raw.cuda().expand(b, -1, -1), cache, dev(raw_t), dev([n - 128] * b, I32), 64, bits)
+    serve.csa_cache_write(cmp.cuda().expand(b, -1, -1), cache, dev(cmp_t), dev([0] * b, I32), 64, bits)
+    idx = np.broadcast_to(np.arange(1100 - K, 1100, dtype=np.int32), (b, s_q, K)).copy() if K else None
+    q = torch.from_numpy(200 * d ** -0.5 * u + rng.standard_normal((b, s_q, H, d))).to(BF)
+    sink = rng.standard_normal(H).astype(np.float32)
+    o, lse = run_attn(case, (cache, raw_t, cmp_t, raw, cmp, idx, q, sink))
+    assert csa.csa_get_device_status() == 0
+    r, c = orc.held_rows(f64(raw[0]), bits), orc.held_rows(f64(cmp[0]), bits)
+    for s in (0, b - 1):
+        for i in range(s_q):
+            check_row(o[s, i], lse[s, i], f64(q[s, i]), lambda p: r[p - n + 128], lambda j: c[j],
+                      None if idx is None else idx[s, i], sink, d ** -0.5, n - s_q + i, 4, 64, BF)
+
+
 def test_attention_large_logits_and_dominant_sink():
     """Logits of several hundred: the running maximum carries them; a sink far
     above them leaves o near zero, far below it changes nothing."""
