@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kScoreThreads) index_scores_simt_kernel(
       for (int h = 0; h < kHeadChunk; ++h)
         if (h < nh) total = fmaf(a.w[row * a.H + h0 + h], fmaxf(dot[h], 0.f), total);
     }
+    if (total != total) total = -INFINITY;               // the select's order has no NaN
     if (j < vis) a.scores[row * a.slots + j] = total;
     float mn = j < vis ? total : INFINITY, mx = j < vis ? total : -INFINITY;
 #pragma unroll

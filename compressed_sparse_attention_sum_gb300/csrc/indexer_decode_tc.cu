@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
     __syncthreads();                                     // sums; K and S are free
     const int j = tile * kIdxTile + key_t;
     for (int q = half; q < nq; q += 2) {
-      const float score = sums[q * kIdxTile + key_t] + sums[(NC / 16 + q) * kIdxTile + key_t];
+      float score = sums[q * kIdxTile + key_t] + sums[(NC / 16 + q) * kIdxTile + key_t];
+      if (score != score) score = -INFINITY;             // the select's order has no NaN
       if (j < most && !*dead) a.scores[(row0 + q) * a.slots + j] = score;
       // the tile's range of scores, as ordered integers
       const int key = float_order(score);

@@ -353,6 +353,10 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   aw = warp_sum(aw);
   if (lane == 0) sh.part[warp] = aw;
   for (int e = tid; e < kBins; e += kSel) sh.hist[0][e] = 0;
+  if (tid == 0) {
+    sh.bin = sh.above = sh.in_bin = 0;
+    sh.tkey = 0u;
+  }
   __syncthreads();
   aw = warp_sum(sh.part[lane]);
   __syncthreads();
@@ -392,7 +396,9 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   const uint32_t lo0 = order_key(mn), hi0 = order_key(mx);
   uint32_t lo = lo0, hi = hi0;
   auto key = [&](int j) { return is_staged ? staged[j] : order_key(score[j0 + j]); };
-  const float eps2 = 2.f * a.err * aw * kmax;
+  // Inputs beyond fp32 (their row's blocks are unspecified) leave the fp32 scores.
+  float eps2 = 2.f * a.err * aw * kmax;
+  if (!(eps2 < 3e38f)) eps2 = 0.f;
 
   // ---- narrow [lo, hi] to a bin that holds the k-th largest key ------------------
   // Counts of the other CTAs' bins and this one's; returns the bin of the k-th
@@ -460,8 +466,12 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
   int k = K, in_range = vis;
   int m = 0, above = 0, before_me = 0;
   uint32_t list_hi = 0;
+  // One round by value, four by bits and the last list: whatever the scores' memory
+  // holds (a score kernel that gave up), the rounds end, and alike in all CTAs.
+  constexpr int kRounds = 16;
+  int rounds = 0;
   for (int limit = by_value ? vis : kNarrow;;) {
-    if (in_range > limit && lo < hi) {
+    if (in_range > limit && lo < hi && ++rounds < kRounds) {
       const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);   // (hi - lo) >> shift < 1024
       int* hist = sh.hist[buf];
 #pragma unroll 4
@@ -539,7 +549,7 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
       __syncthreads();
       break;
     }
-    if (lo == hi) break;                                 // a row of ties
+    if (lo >= hi || ++rounds >= kRounds) break;          // a row of ties
     // too many: narrow by keys, from the whole range, and at last to one key
     limit = by_value ? kNarrow : 0;
     if (by_value) {

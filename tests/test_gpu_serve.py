@@ -392,6 +392,29 @@ def test_indexer_rows_of_several_ctas(n, kind):
     assert torch.equal(got[0, 0].long(), want)
 
 
+@pytest.mark.parametrize("n,dtype,H,d", [(2000, BF, 16, 64), (40000, BF, 16, 64), (2000, F32, 4, 96),
+                                         (700, BF, 64, 128)])
+def test_indexer_rows_with_nan_and_infinite_inputs(n, dtype, H, d):
+    """Such a row gets blocks of its own in ascending order; the others are exact."""
+    b, page, topk = 6, 64, 300
+    rng = np.random.default_rng(n + d)
+    cache, table, keys, q, w = index_case(rng, b, 1, H, d, 1, [n] * b, 4, page, dtype)
+    w[0, 0, H // 2] = float("nan")
+    w[1, 0, 0] = float("inf")
+    q[2, 0, 1, 5] = float("nan")
+    q[3, 0] = float("inf")
+    w[3, 0, :] = -1.0
+    # keys that nothing has written: NaN codes and infinite scales
+    cache[dev(table[4, 1:3]).long()] = POISON
+    got = serve.csa_indexer_topk_decode(q.cuda(), cache, dev(table), w.cuda(), dev([n] * b, I32), topk, 1,
+                                        page, 4).cpu().numpy()
+    assert csa.csa_get_device_status() == 0
+    for s in range(b):
+        assert got[s, 0, 0] >= 0 and got[s, 0, -1] < n and (np.diff(got[s, 0]) > 0).all()
+    want = orc.index_row(f64(q)[5, 0], f64(w)[5, 0], orc.held_rows(f64(keys[5]), 4), n - 1, 1, topk)
+    assert np.array_equal(got[5, 0], want)
+
+
 def test_indexer_bad_page_and_length():
     rng = np.random.default_rng(15)
     n, page = 200, 16
