@@ -387,13 +387,12 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
       } else {
         ok = ok && (a.idx != nullptr || s - wext < my_vis);
       }
-      const float bias = ok ? 0.f : -INFINITY;
       float x[16];
       {
         uint32_t v[16];
         tmem_ld16_wait(tmem + lane_base + hq * 16, v);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) x[c] = fmaf(__uint_as_float(v[c]), sc2, bias);
+        for (int c = 0; c < 16; ++c) x[c] = ok ? __uint_as_float(v[c]) * sc2 : -INFINITY;
       }
       {
         float mx[16];

@@ -4,7 +4,8 @@
 // A group of 32 channels shares one power of two, kept as its exponent plus
 // 127 in a byte.  A code has at most four significant bits, so code * 2^e is
 // a bf16 value as long as it is a normal number; the exponents start at -110
-// so that the smallest non-zero code, 2^-9, stays one.
+// so that the smallest non-zero code, 2^-9, stays one, and end where the largest
+// does: a masked row's weight of 0 times what it holds is 0.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -97,7 +98,8 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   const int ex = (int)(u >> 23) - 127;
   const uint32_t man = u & 0x7fffffu;
   const int e = BITS == 4 ? ex - 2 + (man > 0x400000u ? 1 : 0) : ex - 8 + (man > 0x600000u ? 1 : 0);
-  return min(max(e, kCacheMinExp), 125);   // 125: an infinite amax
+  // at most what leaves the largest code (e4m3: its NaN code too, 480) a bf16 value
+  return min(max(e, kCacheMinExp), BITS == 4 ? 125 : 119);
 }
 
 // Eight values, already divided by the scale -> codes (4 bits: one word; 8

@@ -285,7 +285,7 @@ inline int rows_per_thread(int b, int s, int d) {
 }
 inline dim3 rows_grid(int b, int s, int d, int U, int channels = 8) {
   const int rows = kThreads / (d / channels) * U;
-  return dim3((unsigned)((s + rows - 1) / rows), (unsigned)b);
+  return dim3((unsigned)(((long long)s + rows - 1) / rows), (unsigned)b);
 }
 // Rows [b, s, d] of bf16 on 32-byte boundaries.
 inline bool wide_rows(const void* p, long long bs, long long rs) {

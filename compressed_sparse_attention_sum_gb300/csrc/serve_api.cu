@@ -1,6 +1,7 @@
 // C ABI entry points of the serving calls (include/csa_serve.h): argument
 // validation and dispatch.  Every check runs before the first CUDA call, so a
 // rejected call leaves the device untouched.
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/csa_serve.h"
@@ -109,7 +110,7 @@ csa_status_t csa_cache_read(const void* cache, const int32_t* table, const int32
   const csa_status_t st = check_cache_rows(out, out_batch_stride, out_row_stride, dt, table, pos0,
                                            cache, b, s, d, P, n_pages, page_size, bits);
   if (st != CSA_OK || b == 0 || s == 0) return st;
-  if (s > (long long)P * page_size) return CSA_ERR_INVALID_ARG;
+  if (s > (long long)P * page_size || (b > 1 && out_batch_stride < d)) return CSA_ERR_INVALID_ARG;
   return from_cuda(csa::launch_cache_read(
       cache, table, pos0, counts, out, out_batch_stride, out_row_stride, dt == CSA_BF16, b, s, d,
       P, n_pages, page_size, bits, csa::device_status_word(), (cudaStream_t)stream));
@@ -211,7 +212,7 @@ csa_status_t csa_attn_decode(const void* q, const void* cache, const int32_t* ra
       (K > 0 && P_cmp == 0))
     return CSA_ERR_INVALID_ARG;
   if ((long long)P_raw * page_size < (long long)window + s_q - 1) return CSA_ERR_INVALID_ARG;
-  if (!(scale == scale)) return CSA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
   const long long cmp_rows = K > 0 ? K : (long long)P_cmp * page_size;
   if (H > kMaxDecodeH || (long long)b * s_q > kMaxRows || K > kMaxSlots ||
       (long long)P_raw * page_size > kMaxSlots || (long long)P_cmp * page_size > kMaxSlots)

@@ -42,9 +42,10 @@
  * clamped and recorded (site 0x72).
  *
  * Limits: 32 <= d <= 512 and d % 32 == 0; page_size a multiple of 16, at most
- * 32768; bits 4 or 8; P * page_size at most 2^24 (UNSUPPORTED above);
- * positions below 2^31.  NaN and infinite inputs give
- * unspecified values in their own rows.
+ * 32768; bits 4 or 8; b at most 65535 and P * page_size at most 2^24
+ * (UNSUPPORTED above); positions below 2^31.  NaN and infinite inputs give
+ * unspecified values in their own rows, and in the results of the queries that
+ * see those; no other result changes, and chosen blocks are always visible ones.
  */
 #ifndef CSA_SERVE_H_
 #define CSA_SERVE_H_
@@ -63,12 +64,13 @@ size_t csa_cache_page_bytes(int page_size, int d, int bits);
  *
  * Row i < counts[s] of sequence s goes to position pos0[s] + i.  Per group of
  * 32 channels the scale is the smallest power of two 2^e with
- * max|x| <= 2^e * 6 (bits 4) or 2^e * 448 (bits 8) and e >= -110, and the
- * codes are x * 2^-e rounded to the nearest code, ties to even.  When more
+ * max|x| <= 2^e * 6 (bits 4) or 2^e * 448 (bits 8), within -110 <= e <= 125
+ * (bits 4) or 119 (bits 8), and the codes are x * 2^-e rounded to the nearest
+ * code, ties to even, the largest beyond it.  When more
  * rows than the table has slots are given, the last P * page_size are kept.
  * Rows i >= counts[s] are not read, and no other slot is touched.  A page may
  * be written for one sequence only in a call, and appear once in its row of
- * the table; otherwise the shared slots hold either row's bytes.
+ * the table; otherwise the shared slots' bytes are unspecified.
  *
  *   x       in   [b, s, d] of dt; strides in elements, rows contiguous
  *   table   in   [b, P] int32
@@ -88,9 +90,12 @@ csa_status_t csa_cache_write(const void* x, long long x_batch_stride, long long 
  * csa_cache_read - the rows at positions pos0[s] .. pos0[s] + counts[s] - 1,
  * as the values their codes stand for (exact in bf16 and in fp32).
  * Rows i >= counts[s] of out are left as they were.  s must not exceed
- * P * page_size.
- *   out  out  [b, s, d] of dt; strides in elements, rows contiguous
- * Other arguments and errors as csa_cache_write.
+ * P * page_size.  A position that the ring no longer keeps reads as the newer
+ * one that took its slot.
+ *   out  out  [b, s, d] of dt; strides in elements, rows contiguous; rows may
+ *             not overlap
+ * Other arguments and errors as csa_cache_write; also INVALID_ARG for a batch
+ * stride below d where b > 1.
  */
 csa_status_t csa_cache_read(const void* cache, const int32_t* table, const int32_t* pos0,
                             const int32_t* counts, void* out, long long out_batch_stride,
@@ -110,7 +115,8 @@ csa_status_t csa_cache_read(const void* cache, const int32_t* table, const int32
  * the lower block, in ascending order, then -1.  The set is that of the exact
  * scores: blocks whose fp32 score lies within the fp32 error of the topk-th
  * are scored again at twice fp32's precision.  The choice therefore depends
- * on the row's own inputs alone, not on the batch.
+ * on the row's own inputs alone, not on the batch.  (Keys above 2^60, whose
+ * squares leave fp32, leave their sequence to the fp32 scores.)
  *
  *   q_I        in   [b, s_q, H_I, d_I] of dt      w  in  [b, s_q, H_I] fp32
  *   table      in   [b, P] page table of the index keys (no ring: P *
@@ -154,7 +160,7 @@ csa_status_t csa_indexer_topk_decode(const void* q_I, const void* cache, const i
  *                   16-byte aligned, used by one call at a time
  * Errors: INVALID_ARG for null pointers (P_cmp == 0 allows a null cmp_table,
  * K must then be 0), misaligned q, cache, o, workspace, sizes outside the
- * limits, a ring smaller than the windows, a scale that is NaN; UNSUPPORTED
+ * limits, a ring smaller than the windows, a scale that is not finite; UNSUPPORTED
  * for H > 128 or b * s_q > 65535; WORKSPACE when too small.
  */
 size_t csa_attn_decode_workspace_size(int b, int s_q, int H, int d, int window, int cmp_rows);

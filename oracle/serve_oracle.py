@@ -4,7 +4,8 @@ no code with the CUDA path.
 
 The cache format: a group of 32 channels is codes times a power of two; bits 4:
 e2m1, bits 8: e4m3.  The power of two is the smallest that holds the group's
-largest magnitude (at least 2^-110); codes round to nearest, ties to even.
+largest magnitude (at least 2^-110, at most 2^125 or 2^119); codes round to
+nearest, ties to even.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import numpy as np
 
 GROUP = 32
 MIN_EXP = -110
+MAX_EXP = {4: 125, 8: 119}
 
 
 def code_grid(bits):
@@ -35,7 +37,7 @@ def quantize_rows(x, bits):
         g = x[at[:-1]][at[-1] * GROUP:(at[-1] + 1) * GROUP]
         amax = np.abs(g).max()
         e = MIN_EXP
-        while np.ldexp(grid[-1], int(e)) < amax:
+        while np.ldexp(grid[-1], int(e)) < amax and e < MAX_EXP[bits]:
             e += 1
         exps[at] = e
         for i, v in enumerate(g):

@@ -161,6 +161,24 @@ def test_long_ranges_equal_short_ones(bits, d):
     assert bool((odd[..., d:] == 7.0).all())
 
 
+@pytest.mark.parametrize("bits,top", [(4, 1.5 * 2.0 ** 127), (8, 1.75 * 2.0 ** 127)])
+def test_the_largest_magnitudes_saturate(bits, top):
+    """Groups up to the end of fp32: the scale stops where its largest code is a
+    bf16 value, and what lies beyond is that value."""
+    x = torch.zeros(1, 4, 64)
+    x[0, 0, 0], x[0, 0, 40], x[0, 1, 3] = 3.4e38, -3.4e38, 2.0 ** 127
+    x[0, 2, 5], x[0, 2, 63] = 1.5 * 2.0 ** 127, -1.25 * 2.0 ** 126
+    x[0, 3, 0], x[0, 3, 1] = float("inf"), 2.0 ** 126
+    cache = empty_cache(1, 16, 64, bits)
+    out = torch.empty(1, 4, 64, device="cuda")
+    args = (dev([[0]], I32), dev([0], I32))
+    serve.csa_cache_write(x.cuda(), cache, *args, 16, bits)
+    serve.csa_cache_read(cache, *args, out, 16, bits)
+    got = f64(out)[0]
+    assert np.array_equal(got[:3], orc.held_rows(x[0, :3].numpy(), bits))
+    assert got[0, 0] == top and got[0, 40] == -top and got[3, 0] == top and got[3, 1] == 2.0 ** 126
+
+
 def test_bad_pages_and_counts_are_skipped_and_recorded():
     bits, d, page = 4, 64, 16
     rng = np.random.default_rng(0)
@@ -577,6 +595,30 @@ def test_attention_whose_maximum_keeps_growing(H, d, s_q, K, bits):
         for i in range(s_q):
             check_row(o[s, i], lse[s, i], f64(q[s, i]), lambda p: r[p - n + 128], lambda j: c[j],
                       None if idx is None else idx[s, i], sink, d ** -0.5, n - s_q + i, 4, 64, BF)
+
+
+@pytest.mark.parametrize("H,d,bits", [(16, 128, 4), (16, 128, 8), (16, 512, 4), (16, 512, 8), (32, 64, 8),
+                                      (8, 96, 8)])
+def test_attention_rows_that_only_a_later_query_sees(H, d, bits):
+    """The newest token's row has NaN, infinities and magnitudes at the end of
+    fp32; the queries before it share its CTA, and do not see it."""
+    case = (1, 3, H, d, 4, 40, [600], 0, bits, 16, BF, True)
+    rng = np.random.default_rng(H + d + bits)
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = attn_case(rng, case)
+    n = 600
+    bad = torch.from_numpy(rng.standard_normal((1, 1, d))).float()
+    bad[0, 0, ::3] = float("inf")
+    bad[0, 0, 1::7] = float("nan")
+    bad[0, 0, 2::5] = -3.4e38
+    serve.csa_cache_write(bad.cuda(), cache, dev(raw_t), dev([n - 1], I32), 16, bits)
+    got = torch.empty(1, 1, d, dtype=BF, device="cuda")
+    serve.csa_cache_read(cache, dev(raw_t), dev([n - 1], I32), got, 16, bits)
+    assert bool(torch.isfinite(got).all())
+    o, lse = run_attn(case, (cache, raw_t, cmp_t, raw, cmp, idx, q, sink))
+    r, c = orc.held_rows(f64(raw[0]), bits), orc.held_rows(f64(cmp[0]), bits)
+    for i in range(2):
+        check_row(o[0, i], lse[0, i], f64(q)[0, i], lambda p: r[p], lambda j: c[j], None, sink, d ** -0.5,
+                  n - 3 + i, 4, 40, BF)
 
 
 def test_attention_large_logits_and_dominant_sink():

@@ -73,6 +73,19 @@ def test_read_longer_than_the_ring_is_refused(lib):
     assert _read(lib, s=129, bs=129 * 128) == INVALID
 
 
+def test_read_into_rows_that_overlap_is_refused(lib):
+    for bs in (0, 120):
+        assert _read(lib, b=2, bs=bs) == INVALID
+    # [s, b, d] rows and a stride that no row uses are not refused for it
+    assert _read(lib, b=2, bs=128, rs=256, P=1 << 19) == UNSUPPORTED
+    assert _read(lib, bs=0, P=1 << 19) == UNSUPPORTED
+
+
+def test_infinite_scales_are_refused(lib):
+    for x in (float("inf"), -float("inf")):
+        assert _attend(lib, scale=x) == INVALID
+
+
 def _index(lib, q=FAKE, cache=FAKE, table=FAKE, w=FAKE, lens=FAKE, out=FAKE, b=1, s_q=1, H=64, d=128,
            ratio=4, topk=16, P=2, n_pages=4, page=64, bits=4, dt=1, ws=FAKE, nbytes=1 << 30):
     return lib.csa_indexer_topk_decode(q, cache, table, w, lens, out, b, s_q, H, d, ratio, topk, P,
