@@ -42,10 +42,7 @@ __device__ __forceinline__ float order_float(int k) {
 
 template <int D, int NC>
 struct Cfg {
-  static constexpr int kGroups = D / 32;                 // scale groups of a key
-  static constexpr int kKeys = 8 * (32 / (8 * kGroups)); // keys a warp expands at once
-  static constexpr int kPass = kKeys * (kThreads / 32);
-  static constexpr int kKpt = kIdxTile / kPass;          // keys of a thread
+  static constexpr int kGpt = D / 64;                    // scale groups of a thread: every other of a key
   static constexpr uint32_t kQBlk = NC * 128;
   static constexpr uint32_t K = (D / 64) * kQBlk;
   static constexpr uint32_t W = K + (D / 64) * kBlk;     // [NC] head weights
@@ -92,32 +89,33 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
   if (warp == 0) tmem_alloc(tmem_slot, NC);
 
   const int32_t* pages = a.table + (long long)bi * a.P;
-  const int cg = (lane >> 3) % C::kGroups;
-  const int ckey = warp * C::kKeys + (lane / (8 * C::kGroups)) * 8 + (lane & 7);
+  // Two threads expand a key: lane l and l + 16 of a warp, 16 keys a warp.
+  const int cl = lane >> 4, ckey = warp * 16 + (lane & 15);
   // Page ids are read two tiles ahead and codes one, all of a step at once: a
   // dependent read of global memory takes as long as a tile's arithmetic.
-  Codes<BITS> cd[C::kKpt];
-  int page[C::kKpt];
+  Codes<BITS> cd[C::kGpt];
+  uint32_t scales = 0;                                   // of the key's groups, a byte each
+  int page = 0;
   auto fetch_pages = [&](int tile) {
-#pragma unroll
-    for (int k = 0; k < C::kKpt; ++k) {
-      const int j = tile * kIdxTile + ckey + k * C::kPass;
-      page[k] = __ldg(pages + page_index(a.cs, min(j, most - 1)));
-    }
+    page = __ldg(pages + page_index(a.cs, min(tile * kIdxTile + ckey, most - 1)));
   };
   auto fetch_codes = [&](int tile) {
+    const int j = tile * kIdxTile + ckey;
+    const bool ok = (unsigned)page < (unsigned)a.cs.n_pages;
+    if (!ok) set_status(a.status, kDevCheck, kSiteCachePage);
+    const int r = j - page_index(a.cs, j) * a.cs.page_size;
+    const uint8_t* base = a.cache + page_base(a.cs, page);
+    const bool live = ok && j < most;
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
+    const uint8_t* code = (live ? base + row_code(a.cs, r) : zero) + cl * (4 * BITS);
+    const uint8_t* scale = live ? base + row_scale(a.cs, r) : zero;
 #pragma unroll
-    for (int k = 0; k < C::kKpt; ++k) {
-      const int j = tile * kIdxTile + ckey + k * C::kPass;
-      const bool ok = (unsigned)page[k] < (unsigned)a.cs.n_pages;
-      if (!ok) set_status(a.status, kDevCheck, kSiteCachePage);
-      const int r = j - page_index(a.cs, j) * a.cs.page_size;
-      const uint8_t* base = a.cache + page_base(a.cs, page[k]);
-      const bool live = ok && j < most;
-      const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zero_row);
-      cd[k].load(live ? base + row_code(a.cs, r) + cg * (4 * BITS) : zero,
-                 live ? base + row_scale(a.cs, r) + cg : zero);
-    }
+    for (int k = 0; k < C::kGpt; ++k)
+#pragma unroll
+      for (int e = 0; e < BITS / 4; ++e)
+        cd[k].w[e] = __ldg(reinterpret_cast<const uint4*>(code + k * (8 * BITS)) + e);
+    if constexpr (D == 128) scales = __ldg(reinterpret_cast<const uint32_t*>(scale));
+    else scales = __ldg(reinterpret_cast<const uint16_t*>(scale));
   };
   // Q: column c is query c / hpad, head c % hpad; the others are zero
   constexpr int kQChunks = NC * (D / 8) / kThreads;
@@ -156,20 +154,19 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
   uint32_t parity = 0;
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     // ---- expand ----------------------------------------------------------------
-    float norm2 = 0.f;                                   // |k|^2, largest of this thread's keys
+    float norm2 = 0.f;                                   // |k|^2
 #pragma unroll
-    for (int k = 0; k < C::kKpt; ++k) {
-      const int key = ckey + k * C::kPass;
+    for (int k = 0; k < C::kGpt; ++k) {                  // group 2 k + cl
       uint32_t o[16];
+      cd[k].scale = (scales >> (16 * k + 8 * cl)) & 255u;
       expand_words<BITS>(cd[k], o);
-      store_words(o, sm + C::K + (cg >> 1) * kBlk + key * 128, (cg & 1) * 4, key & 7);
+      store_words(o, sm + C::K + k * kBlk + ckey * 128, cl * 4, ckey & 7);
       float s = words_norm2(o);
       // squares of groups below 2^-40 may underflow
       if (cd[k].scale < 87u) s = fmaxf(s, 32.f * (BITS == 4 ? 36.f : 448.f * 448.f) * 0x1p-80f);
-#pragma unroll
-      for (int o = 8; o < 8 * C::kGroups; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      norm2 = fmaxf(norm2, s);
+      norm2 += s;
     }
+    norm2 += __shfl_xor_sync(0xffffffffu, norm2, 16);
     norm2 = warp_max(norm2);
     // by parity: the tile before is still read after its last barrier
     float* bnd = reinterpret_cast<float*>(sm + C::BND) + parity * 8;
