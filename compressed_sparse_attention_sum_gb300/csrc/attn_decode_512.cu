@@ -20,10 +20,10 @@
 // row of S' is a column of the softmax: its maximum and sum stay within a thread
 // but for the four that share a row.
 //
-// 128 queries of 64 heads, 1152 slots each (18 tiles), 4 bits: 41 us, of which 9
+// 128 queries of 64 heads, 1152 slots each (18 tiles), 4 bits: 40 us, of which 9
 // are the prologue and the end.  With one tile of 128 slots and its chain: 52.7 us;
 // with two tiles of 64, Q in shared memory and slots as the rows of S': 49.9 us
-// (16 expanding warps instead of 8: 50.7 us).  What bounds it: 3.7k cycles a tile,
+// (16 expanding warps instead of 8: 50.7 us).  What bounds it: 3.6k cycles a tile,
 // of which the tensor core takes 2.1k (16 products of N = 128 and 16 of N = 64);
 // shared memory moves 224 KB, 1.75k cycles, and its queue delays the expansion
 // and the softmax, whose instructions fill about half of the issue slots.
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bar_kv = reinterpret_cast<uint64_t*>(sm + C::BARS);   // [3] tile expanded
   uint64_t* bar_o = bar_kv + 3;                                   // [3] O^T of the tile complete
-  uint64_t* bar_s = bar_kv + 6;                                   // S' complete
+  uint64_t* bar_s = bar_kv + 6;                                   // S' complete, oks of the tile
   uint64_t* bar_sfree = bar_kv + 7;                               // S' read
   uint64_t* bar_p = bar_kv + 8;                                   // P written
   uint64_t* bar_q = bar_kv + 9;                                   // Q written
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
       mbar_init(&bar_kv[i], kConv5);
       mbar_init(&bar_o[i], 1);
     }
-    mbar_init(bar_s, 1);
+    mbar_init(bar_s, 2);
     mbar_init(bar_sfree, kSoft5);
     mbar_init(bar_p, kSoft5);
     mbar_init(bar_q, kSoft5);
@@ -266,6 +266,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
             mma_bf16_ts(td + C::kColS, td + C::kColQ + k * 8,
                         ka + (((k >> 2) * C::kBlk + (k & 3) * 32) >> 4), idesc_s, k > 0 ? 1u : 0u);
           mma_commit(bar_s);
+          mbar_arrive(bar_s);                              // hands on what the expanding warps wrote
         }
         __syncwarp();
       }
@@ -356,10 +357,22 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     const int pair = 2 + hq * 2 + (qd & 1);                // barrier of those two warps
     const uint32_t ts = tmem + lane_base + C::kColS + upper * 64 + hq * 32;
     unsigned char* prow = sm + C::P + c1 * 128;
+    // whether any of the softmax threads has it; orders their shared memory
+    auto any_of_soft = [&](bool x) {
+      int any;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.b32 q, %1, 0;\n\t"
+          "bar.red.or.pred p, 1, %2, q;\n\t"
+          "selp.b32 %0, 1, 0, p;\n\t}"
+          : "=r"(any)
+          : "r"((int)x), "n"(kSoft5 * 32)
+          : "memory");
+      return any != 0;
+    };
     int buf = 0, bo = 0;                                   // of tile it, of tile it - 1
     uint32_t ph = 0, pho = 0;
     for (int it = 0; it < n; ++it) {
-      wait(&bar_kv[buf], ph);                              // orders oks; long complete
       wait(bar_s, it & 1);
       fence_after();
       // the slots that count, as bits
@@ -370,85 +383,98 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
       const unsigned live = *reinterpret_cast<const uint16_t*>(oks + buf * 8 + s0 / 8) &
                             ((below(hi) & ~below(lo)) | (below(end) & ~below(wext)));
       float x[16];
-      {
-        uint32_t v[16], y[16];
-        tmem_ld16_pair_wait(ts + upper * 16, v, ts + (upper ^ 1) * 16, y);
+      uint32_t v[16], y[16];
+      tmem_ld16_pair_wait(ts + upper * 16, v, ts + (upper ^ 1) * 16, y);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(xput + ((c ^ xs) << 4)) =
-              make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
-        fence_before();
-        arrive(bar_sfree);
-        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(xput + ((c ^ xs) << 4)) =
+            make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+      fence_before();
+      arrive(bar_sfree);
+      asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float4 z = *reinterpret_cast<const float4*>(xget + ((c ^ xs) << 4));
-          x[4 * c] = (__uint_as_float(v[4 * c]) + z.x) * sc2;
-          x[4 * c + 1] = (__uint_as_float(v[4 * c + 1]) + z.y) * sc2;
-          x[4 * c + 2] = (__uint_as_float(v[4 * c + 2]) + z.z) * sc2;
-          x[4 * c + 3] = (__uint_as_float(v[4 * c + 3]) + z.w) * sc2;
-        }
+      for (int c = 0; c < 4; ++c) {
+        const float4 z = *reinterpret_cast<const float4*>(xget + ((c ^ xs) << 4));
+        x[4 * c] = (__uint_as_float(v[4 * c]) + z.x) * sc2;
+        x[4 * c + 1] = (__uint_as_float(v[4 * c + 1]) + z.y) * sc2;
+        x[4 * c + 2] = (__uint_as_float(v[4 * c + 2]) + z.z) * sc2;
+        x[4 * c + 3] = (__uint_as_float(v[4 * c + 3]) + z.w) * sc2;
       }
       if (__any_sync(0xffffffffu, live != 0xffffu)) {
 #pragma unroll
         for (int c = 0; c < 16; ++c) x[c] = (live >> c) & 1u ? x[c] : -INFINITY;
       }
-      {
-        float mx = x[0];
+      float mx = x[0];
 #pragma unroll
-        for (int c = 1; c < 16; ++c) mx = fmaxf(mx, x[c]);
-        red[((it & 1) * NC + c1) * 4 + hq * 2 + upper] = mx;
+      for (int c = 1; c < 16; ++c) mx = fmaxf(mx, x[c]);
+      // P = 2^(x - m), masked slots 2^-inf = 0; a column without an unmasked
+      // slot so far has m = -inf and takes 0 instead
+      uint32_t pk[8];
+      float lt;
+      auto weights = [&]() {
+        const float m_use = m1 == -INFINITY ? 0.f : m1;
+        float l0 = 0.f, l2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float p0 = ex2(x[e] - m_use), p1 = ex2(x[e + 1] - m_use);
+          l0 += p0;
+          l2 += p1;
+          pk[e / 2] = pack_bf16x2(p0, p1);
+        }
+        lt = l0 + l2;
+      };
+      // A maximum moves where it grows by more than 2^kRescale, or from nothing.  Few
+      // tiles have one that does: P is formed with the present ones beforehand, and
+      // again, with the columns' new maxima, where any does.
+      weights();
+      const bool grow = any_of_soft(mx > m1 + kRescale);
+      unsigned left = 0;                                   // columns of O^T to be rescaled
+      float f2 = 1.f;
+      if (grow) {
+        float* rd = red + (it & 1) * 4 * NC;
+        rd[c1 * 4 + hq * 2 + upper] = mx;
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoft5 * 32) : "memory");
+        const float4 r1 = *reinterpret_cast<const float4*>(rd + c1 * 4);
+        const float4 r2 = *reinterpret_cast<const float4*>(rd + (hq * 32 + lane) * 4);
+        const float t1 = fmaxf(fmaxf(r1.x, r1.y), fmaxf(r1.z, r1.w));
+        const float t2 = fmaxf(fmaxf(r2.x, r2.y), fmaxf(r2.z, r2.w));
+        if (t1 > m1 + kRescale) {
+          l1 *= ex2(m1 - t1);                              // 0 when m1 = -inf
+          m1 = t1;
+        }
+        const bool g2 = t2 > m2 + kRescale;
+        if (g2) {
+          f2 = ex2(m2 - t2);
+          m2 = t2;
+        }
+        left = __ballot_sync(0xffffffffu, g2);
+        weights();
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(kSoft5 * 32) : "memory");   // red
-      const float4 r1 = *reinterpret_cast<const float4*>(red + ((it & 1) * NC + c1) * 4);
-      const float4 r2 = *reinterpret_cast<const float4*>(red + ((it & 1) * NC + hq * 32 + lane) * 4);
-      const float t1 = fmaxf(fmaxf(r1.x, r1.y), fmaxf(r1.z, r1.w));
-      const float t2 = fmaxf(fmaxf(r2.x, r2.y), fmaxf(r2.z, r2.w));
-      // a maximum moves where it grows by more than 2^kRescale, or from nothing
-      if (t1 > m1 + kRescale) {
-        l1 *= ex2(m1 - t1);                                // 0 when m1 = -inf
-        m1 = t1;
-      }
-      const bool g2 = t2 > m2 + kRescale;
-      const float f2 = g2 ? ex2(m2 - t2) : 1.f;
-      if (g2) m2 = t2;
-      const unsigned grow = __ballot_sync(0xffffffffu, g2);
       if (it > 0) {
         // P and, where a maximum grew, O^T are free once the tile before is done
         wait(&bar_o[bo], pho);
         fence_after();
-        // the warp's lane quarter of O^T, all M tiles, its 32 columns
+        if (left != 0) {
+          // the warp's lane quarter of O^T, all M tiles, its 32 columns
 #pragma unroll 1
-        for (unsigned left = grow; left != 0; left &= left - 1) {
-          const int c = __ffs(left) - 1;
-          const float fc = __shfl_sync(0xffffffffu, f2, c);
+          for (; left != 0; left &= left - 1) {
+            const int c = __ffs(left) - 1;
+            const float fc = __shfl_sync(0xffffffffu, f2, c);
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
-            const uint32_t ta = tmem + lane_base + C::kColO + m * NC + hq * 32 + c;
-            const uint32_t v = tmem_ld1_wait(ta);
-            tmem_st1(ta, __float_as_uint(__uint_as_float(v) * fc));
+            for (int m = 0; m < 4; ++m) {
+              const uint32_t ta = tmem + lane_base + C::kColO + m * NC + hq * 32 + c;
+              const uint32_t o = tmem_ld1_wait(ta);
+              tmem_st1(ta, __float_as_uint(__uint_as_float(o) * fc));
+            }
           }
+          tmem_wait_st();
         }
-        if (grow != 0) tmem_wait_st();
       }
-      // P = 2^(x - m), masked slots 2^-inf = 0; a column without an unmasked
-      // slot so far has m = -inf and takes 0 instead
-      const float m_use = m1 == -INFINITY ? 0.f : m1;
-      float lt[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c8 = 0; c8 < 2; ++c8) {
-        uint32_t pk[4];
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float p0 = ex2(x[c8 * 8 + e] - m_use), p1 = ex2(x[c8 * 8 + e + 1] - m_use);
-          lt[0] += p0;
-          lt[1] += p1;
-          pk[e / 2] = pack_bf16x2(p0, p1);
-        }
+      for (int c8 = 0; c8 < 2; ++c8)
         *reinterpret_cast<uint4*>(prow + (((s0 / 8 + c8) ^ (c1 & 7)) << 4)) =
-            make_uint4(pk[0], pk[1], pk[2], pk[3]);
-      }
-      l1 += lt[0] + lt[1];
+            make_uint4(pk[4 * c8], pk[4 * c8 + 1], pk[4 * c8 + 2], pk[4 * c8 + 3]);
+      l1 += lt;
       fence_before();
       arrive(bar_p);
       bo = buf;
