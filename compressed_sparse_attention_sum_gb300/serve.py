@@ -114,10 +114,26 @@ def _columns(t, name):
 def _workspace(ws, nbytes, dev):
     """Pointer and size of the workspace; the tensor is returned to be kept alive."""
     if ws is None:
-        ws = torch.empty(max(nbytes, 16), dtype=_U8, device=f"cuda:{dev}")
+        if nbytes == 0:
+            return None, None, 0
+        ws = torch.empty(nbytes, dtype=_U8, device=f"cuda:{dev}")
     elif not (ws.get_device() == dev and ws.is_contiguous()):
         _refuse(dev, workspace=(ws, ws.dtype, ws.shape))
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _elsewhere(stream, t):
+    """Whether `stream` is another stream of t's device than the current one."""
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, expected {t.device}")
+    return stream != torch.cuda.current_stream(t.device)
+
+
+def _on(stream, call, *args):
+    """The call with `stream` current: what it allocates belongs to that stream too,
+    and is not handed to another while its kernels run."""
+    with torch.cuda.stream(stream):
+        return call(*args, stream=stream)
 
 
 def _call(name, dev, stream, *args):
@@ -126,7 +142,12 @@ def _call(name, dev, stream, *args):
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, expected cuda:{dev}")
+    else:
+        s = stream.cuda_stream
     code = fn(*args, s)
     if code != 0:
         raise CSAError(name, code)
@@ -217,6 +238,9 @@ def csa_indexer_topk_decode(q_I: torch.Tensor, cache: torch.Tensor, table: torch
     pages (block j at position j).  Returns idx [b, s_q, topk] int32:
     ascending, -1 behind the min(topk, vis) blocks.
     """
+    if stream is not None and _elsewhere(stream, q_I):
+        return _on(stream, csa_indexer_topk_decode, q_I, cache, table, w, seq_lens, topk, ratio,
+                   page_size, bits, workspace, out_idx)
     dev, dt = _first(q_I, "q_I", ("b", "s_q", "H_I", "d_I"))
     b, s_q, H, d = q_I.shape
     want = csa_cache_page_bytes(page_size, d, bits)
@@ -266,6 +290,9 @@ def csa_attn_decode(q: torch.Tensor, cache: torch.Tensor, raw_table: torch.Tenso
     (None: every visible block), sink [H] fp32 or None, seq_lens [b] int32.
     Returns (O [b, s_q, H, d], lse [b, s_q, H] fp32).
     """
+    if stream is not None and _elsewhere(stream, q):
+        return _on(stream, csa_attn_decode, q, cache, raw_table, cmp_table, idx, sink, seq_lens,
+                   scale, ratio, window, page_size, bits, workspace, out, lse)
     dev, dt = _first(q, "q", ("b", "s_q", "H", "d"))
     b, s_q, H, d = q.shape
     want = csa_cache_page_bytes(page_size, d, bits)

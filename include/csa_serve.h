@@ -39,7 +39,9 @@
  * followed: the row is skipped (write), returned as zeros (read), scored as a
  * zero key (indexer) or masked (attention), and CSA_ERR_DEVICE_CHECK is
  * recorded (site 0x71).  A sequence length or count outside its range is
- * clamped and recorded (site 0x72).
+ * clamped and recorded (site 0x72).  A bounded wait that gives up records
+ * CSA_ERR_TIMEOUT (site 0x73 attention, 0x74 indexer); the call's outputs are
+ * then unspecified.
  *
  * Limits: 32 <= d <= 512 and d % 32 == 0; page_size a multiple of 16, at most
  * 32768; bits 4 or 8; b at most 65535 and P * page_size at most 2^24

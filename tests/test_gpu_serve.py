@@ -664,6 +664,32 @@ def test_attention_is_the_same_bits_every_time():
 
 # ---------------------------------------------- streams, graphs, together
 
+def test_allocations_of_a_call_on_a_given_stream_belong_to_it():
+    """While the call waits behind other work of its stream, tensors of the sizes that
+    it allocated are made and filled on the current one: they keep what they hold."""
+    rng = np.random.default_rng(32)
+    n, page, topk = 9000, 64, 100
+    icache, itable, keys, qi, w = index_case(rng, 2, 1, 64, 128, 1, [n, n], 4, page, BF)
+    case = (1, 1, 64, 128, 4, 64, [n], 0, 4, page, BF, True)
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = attn_case(rng, case)
+    i_args = [qi.cuda(), icache, dev(itable), w.cuda(), dev([n, n], I32), topk, 1, page, 4]
+    a_args = [q.cuda(), cache, dev(raw_t), dev(cmp_t), None, dev(sink), dev([n], I32), 128 ** -0.5, 4, 64, page, 4]
+    want = [serve.csa_indexer_topk_decode(*i_args), *serve.csa_attn_decode(*a_args)]
+    sizes = [serve.csa_indexer_topk_decode_workspace_size(2, 1, 64, 128, itable.shape[1] * page),
+             serve.csa_attn_decode_workspace_size(1, 1, 64, 128, 64, cmp_t.shape[1] * page)]
+    assert min(sizes) > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    got = [serve.csa_indexer_topk_decode(*i_args, stream=side), *serve.csa_attn_decode(*a_args, stream=side)]
+    mine = [torch.full((max(k, 16),), 7, dtype=U8, device="cuda") for k in sizes for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(bool((m == 7).all()) for m in mine)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 def test_calls_on_a_side_stream_and_in_two_graphs_that_share_workspaces():
     rng = np.random.default_rng(31)
     case = (2, 1, 32, 128, 4, 64, [500, 300], 50, 4, 16, BF, True)
