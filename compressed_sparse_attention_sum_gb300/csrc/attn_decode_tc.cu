@@ -76,7 +76,7 @@ struct Cfg {
 
 template <int D, int NC, int BITS>
 __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
-    const AttnDecodeArgs a, int per_group, int groups, int head_groups, int cs, int splits) {
+    const AttnDecodeArgs a, int per_group, int groups, int cs) {
   using C = Cfg<D, NC>;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -95,12 +95,13 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  // blockIdx.x: group of queries (per_group of one sequence) and of heads, and
-  // its split of the slots (the cs CTAs of a cluster are neighbours)
-  const int group = (int)blockIdx.x / splits, split = (int)blockIdx.x - group * splits;
-  const int rank = split % cs;
-  const int hg = group % head_groups, qg = group / head_groups;
-  const int bi = qg / groups, i0 = (qg - bi * groups) * per_group;
+  // blockIdx.x: split of the slots (the cs CTAs of a cluster are neighbours), y:
+  // group of queries (per_group of one sequence), z: group of heads.  Divisions
+  // only where there is something to divide: this code runs once, and fetching it
+  // takes longer than its arithmetic (one query 7.3 -> 7.0 us).
+  const int splits = gridDim.x, split = blockIdx.x, rank = split & (cs - 1);
+  const int hg = blockIdx.z, qg = blockIdx.y;
+  const int bi = groups == 1 ? qg : qg / groups, i0 = (qg - bi * groups) * per_group;
   const int nq = min(per_group, a.s_q - i0);
   const int h0 = hg * NC, heads = min(a.H - h0, per_group > 1 ? a.H : NC);   // heads of a query
   const long long row0 = (long long)bi * a.s_q + i0;
@@ -143,8 +144,11 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   const int ring0 = w0 >= 0 ? w0 % ring : ring - 1 - (int)((unsigned)(-1 - w0) % (unsigned)ring);
   const int slots = last.t < 0 ? 0 : wext + (a.idx != nullptr ? a.K : last.vis);
   const int tiles = (slots + kSlots - 1) / kSlots;
-  const int it0 = (unsigned)tiles * (unsigned)split / (unsigned)splits;   // tiles <= 2^18, splits <= 152
-  const int n = (int)((unsigned)tiles * (unsigned)(split + 1) / (unsigned)splits) - it0;
+  int it0 = 0, n = tiles;
+  if (splits > 1) {                                        // tiles <= 2^18, splits <= 152
+    it0 = (unsigned)tiles * (unsigned)split / (unsigned)splits;
+    n = (int)((unsigned)tiles * (unsigned)(split + 1) / (unsigned)splits) - it0;
+  }
 
   if (tid == 0) {
     mbar_init(bar_s, 1);
@@ -535,8 +539,7 @@ cudaError_t launch_tc(const AttnDecodeArgs& a, const DecodePlan& p, cudaStream_t
   const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  const int splits = p.cluster * p.parts;
-  cfg.gridDim = dim3((unsigned)splits * (unsigned)(a.b * p.groups * p.head_groups));
+  cfg.gridDim = dim3((unsigned)(p.cluster * p.parts), (unsigned)(a.b * p.groups), (unsigned)p.head_groups);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -548,8 +551,7 @@ cudaError_t launch_tc(const AttnDecodeArgs& a, const DecodePlan& p, cudaStream_t
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, k, a, p.per_group, p.groups, p.head_groups, p.cluster,
-                            splits);
+  return cudaLaunchKernelEx(&cfg, k, a, p.per_group, p.groups, p.cluster);
 }
 
 template <int D, int NC>

@@ -46,16 +46,6 @@ template <int BITS>
 struct Codes {
   uint4 w[BITS / 4];
   uint32_t scale;
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int e = 0; e < BITS / 4; ++e) w[e] = make_uint4(0u, 0u, 0u, 0u);
-    scale = 0;
-  }
-  __device__ __forceinline__ void load(const uint8_t* code, const uint8_t* s) {
-#pragma unroll
-    for (int e = 0; e < BITS / 4; ++e) w[e] = __ldg(reinterpret_cast<const uint4*>(code) + e);
-    scale = __ldg(s);
-  }
 };
 
 // Eight codes -> four words of two bf16, not yet scaled, in permuted order.
