@@ -48,13 +48,14 @@ struct Cfg512 {
   static constexpr uint32_t kColS = 0, kColQ = 128, kColO = 256;
   static constexpr uint32_t KV = 0;                        // [3] tiles
   static constexpr uint32_t P = KV + 3 * kBuf;             // [64 columns][128 B: 64 slots]
-  static constexpr uint32_t XCH = P + kNC5 * 128;          // [8 warps][32 lanes][16] halves of S to be added
+  static constexpr uint32_t XCH = P + kNC5 * 128;          // [8 warps][32 lanes][16] halves of S to be added; at the
+                                                           // end [64][4] sums as rounded
   static constexpr uint32_t BARS = XCH + kSoft5 * 2048;    // kv[3], o[3], s, sfree, p, q
   static constexpr uint32_t MISC = BARS + 10 * 8;          // TMEM slot, dead
   static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][64][4] column maxima
   static constexpr uint32_t MRUN = RED + 8 * kNC5 * 4;     // [64] at the end
-  static constexpr uint32_t ML = MRUN + kNC5 * 4;          // [64] (maximum, sum) of this CTA
-  static constexpr uint32_t SINK = ML + kNC5 * 8;          // [64] sink logits of the heads (log2 units)
+  static constexpr uint32_t ML = MRUN + kNC5 * 4;          // [64] (maximum, sum, O's factor) of this CTA
+  static constexpr uint32_t SINK = ML + kNC5 * 16;         // [64] sink logits of the heads (log2 units)
   static constexpr uint32_t OKS = SINK + kNC5 * 4;         // [3][8] bits of the slots
   static constexpr uint32_t kBytes = OKS + 3 * 8;
   static constexpr uint32_t STAGE = KV;                    // O after the last tile
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
   float* red = reinterpret_cast<float*>(sm + C::RED);
   float* m_run = reinterpret_cast<float*>(sm + C::MRUN);
-  float2* ml = reinterpret_cast<float2*>(sm + C::ML);
+  float4* ml = reinterpret_cast<float4*>(sm + C::ML);
   unsigned char* oks = sm + C::OKS;
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
   }
   if (warp == kConv5 + kSoft5 && n > 0) tmem_alloc(tmem_slot, 512);
   if (tid < NC) {
-    ml[tid] = make_float2(-INFINITY, 0.f);
+    ml[tid] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     reinterpret_cast<float*>(sm + C::SINK)[tid] = sink_v;
   }
 
@@ -238,7 +239,9 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
       ph ^= 1u;
     }
   };
-  float m1 = -INFINITY, l1 = 0.f;                          // of column c1 over this thread's slots
+  // Of column c1 over this thread's slots: the maximum, and the sum of P as computed
+  // and as rounded to bf16 (attn_decode_tc.cu).
+  float m1 = -INFINITY, l1 = 0.f, lr1 = 0.f;
 
   if (n == 0) {
   } else if (warp == kConv5 + kSoft5) {
@@ -410,18 +413,21 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
       // P = 2^(x - m), masked slots 2^-inf = 0; a column without an unmasked
       // slot so far has m = -inf and takes 0 instead
       uint32_t pk[8];
-      float lt;
+      float lt, lrt;
       auto weights = [&]() {
         const float m_use = m1 == -INFINITY ? 0.f : m1;
-        float l0 = 0.f, l2 = 0.f;
+        float l0 = 0.f, l2 = 0.f, r0 = 0.f, r2 = 0.f;
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float p0 = ex2(x[e] - m_use), p1 = ex2(x[e + 1] - m_use);
           l0 += p0;
           l2 += p1;
           pk[e / 2] = pack_bf16x2(p0, p1);
+          r0 += __uint_as_float(pk[e / 2] << 16);
+          r2 += __uint_as_float(pk[e / 2] & 0xffff0000u);
         }
         lt = l0 + l2;
+        lrt = r0 + r2;
       };
       // A maximum moves where it grows by more than 2^kRescale, or from nothing.  Few
       // tiles have one that does: P is formed with the present ones beforehand, and
@@ -439,7 +445,9 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
         const float t1 = fmaxf(fmaxf(r1.x, r1.y), fmaxf(r1.z, r1.w));
         const float t2 = fmaxf(fmaxf(r2.x, r2.y), fmaxf(r2.z, r2.w));
         if (t1 > m1 + kRescale) {
-          l1 *= ex2(m1 - t1);                              // 0 when m1 = -inf
+          const float f1 = ex2(m1 - t1);                   // 0 when m1 = -inf
+          l1 *= f1;
+          lr1 *= f1;
           m1 = t1;
         }
         const bool g2 = t2 > m2 + kRescale;
@@ -475,6 +483,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
         *reinterpret_cast<uint4*>(prow + (((s0 / 8 + c8) ^ (c1 & 7)) << 4)) =
             make_uint4(pk[4 * c8], pk[4 * c8 + 1], pk[4 * c8 + 2], pk[4 * c8 + 3]);
       l1 += lt;
+      lr1 += lrt;
       fence_before();
       arrive(bar_p);
       bo = buf;
@@ -482,6 +491,8 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
       next(buf, ph);
     }
     red[((n & 1) * NC + c1) * 4 + hq * 2 + upper] = l1;
+    // XCH was last read before the last tile's any_of_soft
+    reinterpret_cast<float*>(sm + C::XCH)[c1 * 4 + hq * 2 + upper] = lr1;
     if (hq == 0 && upper == 0) m_run[c1] = m1;
   }
   // ---- the end: O^T to o or into shared memory as [column][channel] ------------------
@@ -494,6 +505,9 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     if (tid < NC) {
       const float* rl = red + ((n & 1) * NC + tid) * 4;
       const float2 mine = make_float2(m_run[tid], (rl[0] + rl[1]) + (rl[2] + rl[3]));
+      const float4 rr = *reinterpret_cast<const float4*>(sm + C::XCH + tid * 16);
+      const float lr = (rr.x + rr.y) + (rr.z + rr.w);
+      const float even = lr > 0.f ? __fdividef(mine.y, lr) : 1.f;   // sum as computed over sum as rounded
       if (cs == 1) {
         // the whole query: its sums with the sink, and each column's factor
         const int qi = per_group > 1 ? tid / a.H : 0, h = per_group > 1 ? tid - qi * a.H : tid;
@@ -503,13 +517,13 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
         float f = 0.f, out = -INFINITY;
         if (m > -INFINITY) {
           const float fm = ex2(mine.x - m), total = fmaf(mine.y, fm, ex2(sink2 - m));
-          f = __fdividef(fm, total);
+          f = __fdividef(fm, total) * even;
           out = (m + log2f(total)) * kLn2;
         }
         m_run[tid] = f;
         if (live && !*dead) a.lse[(row0 + qi) * a.H + h0 + h] = out;
       } else {
-        ml[tid] = mine;
+        ml[tid] = make_float4(mine.x, mine.y, even, 0.f);
       }
     }
     __syncthreads();

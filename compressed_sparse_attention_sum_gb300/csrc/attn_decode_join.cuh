@@ -54,11 +54,11 @@ __device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned c
   for (int r = 0; r < CS; ++r) base[r] = cg::this_cluster().map_shared_rank(sm, r);
   for (int e = threadIdx.x; e < kCols * (D / 4); e += C::kThreads) {
     const int col = rank * kCols + e / (D / 4), c = e % (D / 4) * 4;
-    float2 ml[CS];
+    float4 ml[CS];                                         // maximum, sum, O's factor
     float4 v[CS];
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
-      ml[r] = *reinterpret_cast<const float2*>(base[r] + C::ML + col * 8);
+      ml[r] = *reinterpret_cast<const float4*>(base[r] + C::ML + col * 16);
       v[r] = *reinterpret_cast<const float4*>(base[r] + C::STAGE + (col * D + c) * 4);
     }
     const int qi = per_group > 1 ? col / a.H : 0, h = per_group > 1 ? col - qi * a.H : col;
@@ -71,12 +71,12 @@ __device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned c
 #pragma unroll
     for (int r = 0; r < CS; ++r) {
       if (ml[r].y > 0.f) {                                 // a CTA without a tile has no O
-        const float f = ex2(ml[r].x - m);
+        const float f = ex2(ml[r].x - m), fo = f * ml[r].z;
         total = fmaf(ml[r].y, f, total);
-        acc.x = fmaf(v[r].x, f, acc.x);
-        acc.y = fmaf(v[r].y, f, acc.y);
-        acc.z = fmaf(v[r].z, f, acc.z);
-        acc.w = fmaf(v[r].w, f, acc.w);
+        acc.x = fmaf(v[r].x, fo, acc.x);
+        acc.y = fmaf(v[r].y, fo, acc.y);
+        acc.z = fmaf(v[r].z, fo, acc.z);
+        acc.w = fmaf(v[r].w, fo, acc.w);
       }
     }
     const long long row = row0 + qi;
@@ -115,7 +115,7 @@ __device__ __forceinline__ void store_o16(const uint32_t (&v)[16], const float* 
 }
 
 // The end of a CTA with n tiles that shares its queries with others (cs > 1:
-// C::STAGE holds its O as [column][channel], C::ML its columns' (maximum, sum)) or
+// C::STAGE holds its O as [column][channel], C::ML its columns' (maximum, sum, factor)) or
 // had nothing to attend to.  Called by all threads.
 template <typename C, int D, int NC>
 __device__ __forceinline__ void finish_decode(const AttnDecodeArgs& a, unsigned char* sm, bool dead,

@@ -25,11 +25,16 @@
 //
 // What bounds it: the latency of the chain index - page - codes - S - softmax -
 // O - join (64 queries of 32 x 128, 8 bits: 11.7 us, 5 tiles each).  The
-// arithmetic follows attn_fwd_tc512:
-// probabilities in bf16 (a weight of the values, which the sum of 2^-9
-// relative errors of both signs moves by less than the rounding of o), their
-// sum and the running maximum in fp32, rescaling only when a column's maximum
-// grows by more than 2^8.
+// arithmetic is that of attn_tc512.cu: probabilities rounded to bf16 for the
+// product with the values (the tensor core takes them so; each errs by at most
+// 2^-8 of itself), two sums of them in fp32 and the running maximum in fp32,
+// rescaling only when a column's maximum grows by more than 2^8.  LSE takes the
+// sum as computed; O is divided by the sum as rounded, so that its weights add
+// up to the rows' share and rounding errors that the slots have in common
+// cancel.  The tensor core forms that sum: a product of P with ones, in the time
+// in which the next tile is expanded (100 queries of 32 x 512 over 8 bits: 38.2 us
+// with one sum, 38.7 with both; 41.7 with the second summed by the softmax
+// threads, which takes 16 more registers).
 #include "attn_decode.h"
 #include "attn_decode_join.cuh"
 #include "cache_expand.cuh"
@@ -58,7 +63,9 @@ struct Cfg {
   static constexpr int kSpt = kPass >= kSlots ? 1 : kSlots / kPass;   // slots of a thread
   static constexpr uint32_t kQBlk = NC * 128;
   static constexpr uint32_t kColO = 64;
-  static constexpr uint32_t kNeed = kColO + kMT * NC;
+  static constexpr uint32_t kColR = kColO + kMT * NC;      // sums of the rounded probabilities, alike in all lanes
+  static constexpr uint32_t kColA = kColR + NC;            // ones: 16 elements of K
+  static constexpr uint32_t kNeed = kColA + 8;
   static constexpr uint32_t kTmem = kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t KV = (D / 64) * kQBlk;
@@ -67,8 +74,8 @@ struct Cfg {
   static constexpr uint32_t MISC = BARS + (2 + 2 * kParts) * 8;   // TMEM slot, dead
   static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][4][NC] column maxima
   static constexpr uint32_t MRUN = RED + 8 * NC * 4;       // [2][NC]
-  static constexpr uint32_t ML = MRUN + 2 * NC * 4;        // [NC] (maximum, sum) of this CTA
-  static constexpr uint32_t SINK = ML + NC * 8;            // [NC] sink logits of the heads (log2 units)
+  static constexpr uint32_t ML = MRUN + 2 * NC * 4;        // [NC] (maximum, sum, O's factor) of this CTA
+  static constexpr uint32_t SINK = ML + NC * 16;           // [NC] sink logits of the heads (log2 units)
   static constexpr uint32_t OKS = SINK + NC * 4;           // [2][kSlots] bytes
   static constexpr uint32_t kBytes = OKS + 2 * kSlots;
   static constexpr uint32_t STAGE = KV;                    // [NC][D] O after the last tile
@@ -90,7 +97,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
   float* red = reinterpret_cast<float*>(sm + C::RED);
   float* m_run = reinterpret_cast<float*>(sm + C::MRUN);
-  float2* ml = reinterpret_cast<float2*>(sm + C::ML);
+  float4* ml = reinterpret_cast<float4*>(sm + C::ML);
   unsigned char* oks = sm + C::OKS;
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   if (warp == C::kWarps && n > 0) tmem_alloc(tmem_slot, C::kTmem);
   if (tid < NC) {
     m_run[tid] = -INFINITY;
-    ml[tid] = make_float2(-INFINITY, 0.f);
+    ml[tid] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     reinterpret_cast<float*>(sm + C::SINK)[tid] = sink_v;
   }
 
@@ -279,6 +286,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
     // executed by all 16 writing warps it takes about 600 cycles each time.
     constexpr uint32_t idesc_s = idesc_bf16_f32_major(kSlots, NC, 0, 0);
     constexpr uint32_t idesc_o = idesc_bf16_f32_major(128, NC, 1, 1);
+    constexpr uint32_t idesc_r = idesc_bf16_f32_major(128, NC, 0, 1);
     const uint64_t kvd = sw128_desc(smem_addr(sm + C::KV)), qd_s = sw128_desc(smem_addr(sm + C::Q));
     const uint64_t kvd_mn = sw128_desc_mn(smem_addr(sm + C::KV), kKvBlk);
     const uint64_t pd_mn = sw128_desc_mn(smem_addr(sm + C::P), kKvBlk);
@@ -287,6 +295,12 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
       return __all_sync(0xffffffffu, wait(bar, parity)) != 0;
     };
     constexpr int kSteps = D < 128 ? D / 16 : 8;          // K steps of S^T in one M tile
+    auto sum_p = [&](int it) {
+#pragma unroll
+      for (int k = 0; k < kSlots / 16; ++k)
+        mma_bf16_ts(td + C::kColR, td + C::kColA, pd_mn + ((k * 2048) >> 4), idesc_r,
+                    (it > 0 || k > 0) ? 1u : 0u);
+    };
     bool up = true;
     for (int it = 0; up && it < n; ++it) {
 #pragma unroll
@@ -320,8 +334,10 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
               mma_bf16_ss(td + C::kColO + m * NC, kvd_mn + ((2 * m * kKvBlk + k * 2048) >> 4),
                           pd_mn + ((k * 2048) >> 4), idesc_o, (it > 0 || k > 0) ? 1u : 0u);
           }
+          if (x == C::kParts - 1 && it == n - 1) sum_p(it);
           mma_commit(&bar_o[x]);
         }
+        if (it < n - 1) sum_p(it);                         // complete with the next tile's S
       }
       __syncwarp();
     }
@@ -370,6 +386,13 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
     float l_part[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) l_part[c] = 0.f;
+
+    if (hq == 0) {
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) tmem_st1(tmem + lane_base + C::kColA + c, 0x3f803f80u);
+      tmem_wait_st();
+      fence_before();
+    }
 
     convert(0);
     for (int it = 0; it < n; ++it) {
@@ -424,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
         for (int c = 0; c < 16; ++c) l_part[c] *= __shfl_sync(0xffffffffu, f, c);
         if (it > 0) {
 #pragma unroll 1
-          for (int m = 0; m < C::kMT; ++m) {
+          for (int m = 0; m <= C::kMT; ++m) {              // and the sums behind them
             const uint32_t ta = tmem + lane_base + C::kColO + m * NC + hq * 16;
 #pragma unroll 1
             for (int c = 0; c < 16; ++c) {
@@ -467,11 +490,26 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
       const float l = lane_reduce16<false>(l_part);
       if (lane < 16) red[((n & 1) * 4 + qd) * NC + hq * 16 + lane] = l;
     }
+    if (qd == 0) {
+      uint32_t v[16];
+      tmem_ld16_wait(tmem + C::kColR + hq * 16, v);
+      // in the place of the last tile's maxima, which were read before bar_p of it
+      float4* rr = reinterpret_cast<float4*>(red + ((n & 1) ^ 1) * 4 * NC + hq * 16);
+      if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          rr[c] = make_float4(__uint_as_float(v[4 * c]), __uint_as_float(v[4 * c + 1]),
+                              __uint_as_float(v[4 * c + 2]), __uint_as_float(v[4 * c + 3]));
+      }
+    }
     sync();
     float2 mine = make_float2(-INFINITY, 0.f);
+    float even = 1.f;                                      // sum as computed over sum as rounded
     if (tid < NC) {
       const float* rl = red + (n & 1) * 4 * NC + tid;
       mine = make_float2(m_run[(n & 1) * NC + tid], (rl[0] + rl[NC]) + (rl[2 * NC] + rl[3 * NC]));
+      const float lr = red[((n & 1) ^ 1) * 4 * NC + tid];
+      if (lr > 0.f) even = __fdividef(mine.y, lr);
     }
     if (cs == 1) {
       // the whole query: its sums with the sink, and each column's factor
@@ -483,7 +521,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
         float f = 0.f, out = -INFINITY;
         if (m > -INFINITY) {
           const float fm = ex2(mine.x - m), total = fmaf(mine.y, fm, ex2(sink2 - m));
-          f = __fdividef(fm, total);
+          f = __fdividef(fm, total) * even;
           out = (m + log2f(total)) * kLn2;
         }
         m_run[tid] = f;
@@ -491,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
       }
       sync();
     } else if (tid < NC) {
-      ml[tid] = mine;
+      ml[tid] = make_float4(mine.x, mine.y, even, 0.f);
     }
     // O^T to o or into shared memory as [column][channel]: the KV tile's place
     if (!*dead) {

@@ -150,6 +150,13 @@ csa_status_t csa_indexer_topk_decode(const void* q_I, const void* cache, const i
  * sink included.  A query with no row to attend to (t < 0) gets o = 0 and
  * lse = sink (-inf without one).
  *
+ * Arithmetic: fp32 queries, and widths other than those below, are computed in
+ * fp32 throughout.  bf16 queries of d 64, 128, 256 or 512 take the tensor cores:
+ * logits, maxima, sums and o are accumulated in fp32, and each probability is
+ * rounded to bf16 (2^-8 of itself) for its product with the row.  o is divided
+ * by the sum of the rounded probabilities, so its weights add up to the rows'
+ * share of the denominator; lse has the sum of the unrounded ones.
+ *
  *   q          in   [b, s_q, H, d] of dt           sink  in  [H] fp32 or NULL
  *   raw_table  in   [b, P_raw] page table of the raw rows (a ring:
  *                   P_raw * page_size >= window + s_q - 1)

@@ -1,0 +1,84 @@
+"""Numerics of the serving calls where an ordinary input does not reach them, on
+the GPU against the fp64 oracle or against values known by construction."""
+import numpy as np
+import pytest
+import torch
+
+from compressed_sparse_attention_sum_gb300 import csa, serve
+from test_gpu_serve import BF, F32, dev, empty_cache, f64, tables
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from compressed_sparse_attention_sum_gb300 import build
+    build.build()
+    serve.load_library()
+    csa.csa_get_device_status()
+    yield
+    assert csa.csa_get_device_status() == 0
+
+
+# --------------------------------------------------------------- attention
+
+# b, s_q, H, d, K (0: every visible block), bits, dtype: one CTA a query, clusters, parts
+# that a second kernel joins, several queries a CTA, CUDA cores
+EVEN_CASES = [
+    (1, 1, 32, 128, 600, 4, BF), (96, 1, 32, 128, 600, 8, BF), (2, 2, 16, 64, 0, 8, BF),
+    (1, 1, 32, 128, 0, 4, BF), (130, 1, 64, 256, 300, 4, BF), (2, 1, 8, 512, 300, 8, BF),
+    (130, 1, 64, 512, 300, 4, BF), (3, 1, 64, 512, 700, 8, BF), (2, 3, 16, 512, 0, 4, BF),
+    (80, 2, 64, 64, 0, 4, BF), (1, 1, 5, 96, 100, 4, BF), (2, 1, 16, 128, 200, 8, F32),
+]
+
+
+@pytest.mark.parametrize("case", EVEN_CASES, ids=lambda c: f"b{c[0]}s{c[1]}H{c[2]}d{c[3]}K{c[4]}_{c[5]}bit")
+def test_attention_weights_add_up_to_one(case):
+    """A channel that is 1 in every row comes out as exactly 1 (no sink), whatever the
+    weights.  Fifteen rows of sixteen have the probability 2^-1 (1 + 2^-8 - 2^-12)
+    relative to the others: rounded to bf16 it loses 2^-8 of itself, one step of the
+    output, which every row shares unless the weights are divided by their own sum.
+    What is left is fp32: with n = 64 to 2000 rows the sums err by less than
+    n 2^-23 < 2^-12 of themselves, an eighth of half the bf16 step below 1 (2^-9)."""
+    b, s_q, H, d, K, bits, dtype = case
+    page, window, n = 16, 50, 2000
+    rng = np.random.default_rng(d + H)
+    n_pages, (raw_t, cmp_t) = tables(rng, b, -(-(window + s_q - 1) // page), -(-n // page))
+    raw_t, cmp_t = dev(raw_t), dev(cmp_t)
+    cache = empty_cache(n_pages, page, d, bits)
+    rows = torch.zeros(b, n, d, device="cuda")
+    rows[..., 0] = 1.0                                  # the constant channel
+    rows[..., 33] = 1.0                                 # the one that q meets
+    rows[:, ::16, 33] = 2.0
+    zero = torch.zeros(b, dtype=torch.int32, device="cuda")
+    lens = torch.full_like(zero, n)
+    serve.csa_cache_write(rows, cache, raw_t, zero, page, bits)
+    serve.csa_cache_write(rows, cache, cmp_t, zero, page, bits)
+    p = 0.5 * (1 + 2.0 ** -8 - 2.0 ** -12)
+    q = torch.zeros(b, s_q, H, d, dtype=dtype, device="cuda")
+    q[..., 33] = 1.0
+    idx = None
+    if K:
+        idx = dev(np.stack([np.sort(rng.permutation(n - s_q)[:K]) for _ in range(b * s_q)]).reshape(b, s_q, K),
+                  torch.int32)
+    o, lse = serve.csa_attn_decode(q, cache, raw_t, cmp_t, idx, None, lens, -float(np.log(p)), 1, window, page,
+                                   bits)
+    assert csa.csa_get_device_status() == 0
+    # fp32 outputs keep what a bf16 one rounds away: the two sums of at most K + window terms (K > 0
+    # here), each addition rounded by 2^-24 of them, (K + window) 2^-23 together, and a few more roundings
+    # where parts are joined and divided
+    off = (o[..., 0].double() - 1.0).abs().max().item()
+    assert off <= ((K + window + 8) * 2.0 ** -23 if dtype == F32 else 0.0), off
+    # the log of the weights' sum as they are, not as rounded: 2 -> e^(2 s), 1 -> e^s
+    pos = torch.arange(n, device="cuda")
+    for i in range(s_q):
+        t = n - s_q + i
+        js = pos[:t + 1].expand(b, -1) if idx is None else idx[:, i].long()
+        twos = (js % 16 == 0).sum(1) + int((pos[t - window + 1:t + 1] % 16 == 0).sum())
+        total = js.shape[1] + window
+        s = -np.log(p)
+        want = torch.log(twos.double() * np.exp(2 * s) + (total - twos).double() * np.exp(s))
+        # logits are exact up to fp32 roundings of scale and of scale * log2 e (2^-23 of 2 s < 1.4), the
+        # sum as above and one rounding of lse
+        assert bool(((lse[:, i].double() - want[:, None]).abs() <= 2.0 ** -11).all())
