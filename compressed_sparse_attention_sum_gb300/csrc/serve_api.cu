@@ -168,7 +168,7 @@ csa_status_t csa_indexer_topk_decode(const void* q_I, const void* cache, const i
   const cudaStream_t s = (cudaStream_t)stream;
   const bool tc = dt == CSA_BF16 && csa::index_decode_tc_supported(H_I, d_I);
   // see indexer_select.cu: fp32 sums on the tensor cores and on CUDA cores
-  a.err = (tc ? (float)(d_I / 8 + H_I / 4 + 8) : (float)(d_I + H_I + 16)) * 0x1p-24f;
+  a.err = (tc ? (float)(11 * d_I / 16 + H_I / 4 + 8) : (float)(d_I + H_I + 16)) * 0x1p-24f;
   const cudaError_t e = tc ? csa::launch_index_scores_tc(a, bits, s)
                            : csa::launch_index_scores_simt(a, dt == CSA_BF16, bits, s);
   if (e != cudaSuccess) return CSA_ERR_CUDA;

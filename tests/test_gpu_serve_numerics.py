@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from compressed_sparse_attention_sum_gb300 import csa, serve
+from oracle import serve_oracle as orc
 from test_gpu_serve import BF, F32, dev, empty_cache, f64, tables
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +83,43 @@ def test_attention_weights_add_up_to_one(case):
         # logits are exact up to fp32 roundings of scale and of scale * log2 e (2^-23 of 2 s < 1.4), the
         # sum as above and one rounding of lse
         assert bool(((lse[:, i].double() - want[:, None]).abs() <= 2.0 ** -11).all())
+
+
+# ----------------------------------------------------------------- indexer
+
+def select(keys, q, w, topk, bits, page=64, dtype=BF):
+    """Indices of one row: keys [n, d], q [H, d], w [H] (ratio 1, every key visible), and the
+    oracle's on the rows held."""
+    n, d = keys.shape
+    P = -(-n // page)
+    cache = empty_cache(P, page, d, bits)
+    table = torch.arange(P, dtype=torch.int32, device="cuda")[None]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    serve.csa_cache_write(dev(keys, F32)[None].contiguous(), cache, table, zero, page, bits)
+    q = dev(q, dtype)[None, None].contiguous()
+    w = dev(w, F32)[None, None].contiguous()
+    got = serve.csa_indexer_topk_decode(q, cache, table, w, dev([n], torch.int32), topk, 1, page, bits)
+    held = serve.csa_cache_read(cache, table, zero, torch.zeros(1, n, d, device="cuda"), page, bits)
+    assert np.array_equal(f64(held)[0], keys), "the keys are meant to be held exactly"
+    assert csa.csa_get_device_status() == 0
+    return got.cpu().numpy()[0, 0], orc.index_row(f64(q)[0, 0], f64(w)[0, 0], keys, n - 1, 1, topk)
+
+
+@pytest.mark.parametrize("H", [1, 3, 16])
+@pytest.mark.parametrize("d,dtype", [(128, BF), (64, BF), (128, F32), (96, F32)])
+def test_indexer_small_products_next_to_a_large_one(H, d, dtype):
+    """Half of the blocks score 1 + (d - 2) 1.99 2^-26, in products of which a sum aligned to
+    the large one keeps nothing; the others 1 + x, x just below that: what fp32 says is
+    the wrong half, by nearly as much as a dot product can lose."""
+    n, u = 200, 2.0 ** -24
+    tail = 255 / 128 * 2.0 ** -26 * (d - 2)
+    x = np.floor(tail / u / 8 * 0.95) * 8 * u               # 56 u at d = 128
+    keys = np.zeros((n, d))
+    keys[:, 0] = 1.0
+    keys[0::2, 1] = 2.0 ** -6
+    keys[1::2, 2:] = 2.0 ** -13
+    q = np.zeros((H, d))
+    q[0, 0], q[0, 1], q[0, 2:] = 1.0, x * 2.0 ** 6, 255 / 128 * 2.0 ** -13
+    got, want = select(keys, q, np.ones(H), n // 2, 8, dtype=dtype)
+    assert np.array_equal(want, np.arange(1, n, 2)) and x < tail
+    assert np.array_equal(got, want)
