@@ -123,3 +123,78 @@ def test_indexer_small_products_next_to_a_large_one(H, d, dtype):
     got, want = select(keys, q, np.ones(H), n // 2, 8, dtype=dtype)
     assert np.array_equal(want, np.arange(1, n, 2)) and x < tail
     assert np.array_equal(got, want)
+
+
+def fp32_sets(keys, q, w, topk):
+    """What fp32 scores alone would choose: the products added one by one, and 16 at a time
+    (each step's exact sum added and rounded once)."""
+    n, d = keys.shape
+    k32, q32 = keys.astype(np.float32), q.astype(np.float32)
+    one, step = np.zeros((n, len(q)), np.float32), np.zeros((n, len(q)), np.float32)
+    for c in range(d):
+        one = (one.astype(np.float64) + k32[:, c:c + 1].astype(np.float64) * q32[:, c]).astype(np.float32)
+    for c in range(0, d, 16):
+        step = (step + keys[:, c:c + 16] @ q[:, c:c + 16].T).astype(np.float32)
+    out = []
+    for dots in (one, step):
+        score = np.zeros(n, np.float32)
+        for h in range(len(q)):
+            score = score + np.maximum(dots[:, h], 0) * np.float32(w[h])
+        out.append(np.sort(np.argsort(-score, kind="stable")[:topk]))
+    return out
+
+
+def cancelling(rng, n, n_close, n_high, H, lift=1.0):
+    """Rows [n, 128] and q, w: of n_close blocks a product of 6 2^14 comes first and leaves last,
+    and what decides between them, at most 6 2^-12, stands between; n_high blocks are far above,
+    the others at zero."""
+    keys = np.zeros((n, 128))
+    kind = np.zeros(n, int)
+    kind[rng.permutation(n)[:n_close + n_high]] = [1] * n_close + [2] * n_high
+    live = kind > 0
+    keys[live, 0], keys[live, 96], keys[live, 32] = 6.0, -6.0, 6.0
+    keys[live, 33] = rng.choice([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], live.sum())
+    keys[kind == 2, 64] = 6.0
+    q = np.zeros((H, 128))
+    q[:, 0], q[:, 96], q[:, 32], q[:, 33], q[:, 64] = 2.0 ** 14, 2.0 ** 14, 1.0, 2.0 ** -12, 4.0
+    w = (np.abs(rng.standard_normal(H)) + 0.1).astype(np.float32).astype(np.float64)
+    return keys, q * lift, w
+
+
+CLOSE_CASES = [
+    # n, close blocks, blocks above, topk: one CTA; eight warps a block and several rounds; a row of several
+    # CTAs; more close blocks than are ranked directly, in one CTA and in several
+    (300, 300, 0, 40), (1000, 200, 30, 131), (20000, 300, 50, 170), (2000, 2000, 0, 333), (20000, 3000, 100, 900),
+]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,H", [(BF, 32), (BF, 7), (F32, 8)])
+@pytest.mark.parametrize("case", CLOSE_CASES, ids=lambda c: f"n{c[0]}close{c[1]}")
+def test_indexer_close_blocks_are_chosen_by_their_exact_scores(case, dtype, H, bits):
+    n, n_close, n_high, topk = case
+    keys, q, w = cancelling(np.random.default_rng(n + H), n, n_close, n_high, H)
+    got, want = select(keys, q, w, topk, bits, dtype=dtype)
+    for wrong in fp32_sets(keys, q, w, topk):
+        assert not np.array_equal(wrong, want)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype,H", [(BF, 64), (F32, 5)])
+@pytest.mark.parametrize("n,topk", [(300, 101), (700, 211), (20000, 400)])
+def test_indexer_exact_ties_whose_fp32_scores_differ(n, topk, dtype, H, bits):
+    """All blocks score the same: their channels c and c + 64, at which q has equal values, are
+    exchanged at random, so that fp32 sums see them in another order.  (The products are
+    multiples of 2^-31 up to 2^5, which pairs of fp32 add without an error.)"""
+    rng = np.random.default_rng(n + H)
+    base = rng.choice([-6.0, -4, -3, -2, -1, 0, 1, 2, 3, 4, 6], (64, 2))
+    flip = rng.random((n, 64)) < 0.5
+    keys = np.where(flip[..., None], base[None, :, ::-1], base[None]).transpose(0, 2, 1).reshape(n, 128)
+    q = f64(torch.from_numpy(rng.standard_normal((H, 64))).bfloat16()) * 2.0 ** -rng.integers(0, 13, (H, 64))
+    q = np.tile(q, 2)
+    w = (np.abs(rng.standard_normal(H)) + 0.1).astype(np.float32).astype(np.float64)
+    got, _ = select(keys, q, w, topk, bits, dtype=dtype)
+    for wrong in fp32_sets(keys, q, w, topk):
+        assert not np.array_equal(wrong, np.arange(topk))
+    assert np.array_equal(got, np.arange(topk))
