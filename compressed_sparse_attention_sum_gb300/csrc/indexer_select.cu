@@ -16,6 +16,12 @@
 //     2^-23 is the step of the sum.  One product of 1 and 126 of 1.99 2^-26
 //     lose 63 2^-24 of the 96 2^-24 at one head of 128 channels; N(0, 1) inputs
 //     0.1 2^-24.
+// Underflow adds less than 2^-149 to each of these roundings; a head's |q_h| is
+// taken as at least 2^-84 for it (keys count as 2^-35 at least), and 2^-140 is
+// added for the sum over the heads.  The product is formed with its exponent
+// apart, as its factors may leave fp32 where it does not.  Where it does, and
+// for keys above 2^60, the fp32 scores decide.
+//
 // A close block's dot products are accumulated as pairs of fp32 (the rounding
 // error of every addition is itself summed, which leaves about 2^-40), as is
 // their sum over the heads; the best fill the places that the blocks above
@@ -35,7 +41,9 @@
 // finished by the first CTA alone, by radix selects over global lists.
 // Latency bounds it: barriers, dependent reads, reads of the other CTAs' shared
 // memory (all of a step are in flight at once) and the chain of dependent
-// additions of a dot product (d_I / 4 long: four threads share a head).
+// additions of a dot product (d_I / 4 long: four threads share a head).  They are
+// formed of q, k and w scaled by powers of two to about 1, where no error term
+// underflows.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -69,6 +77,15 @@ __device__ __forceinline__ unsigned long long order_key(double x) {
   return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
+// x = mantissa * 2^exponent for a normal x, the mantissa in [1, 2); a mantissa of 0 for 0
+// and NaN for NaN and the infinities.
+constexpr int kNoExp = -100000;      // below every exponent
+__device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255u) - 127; }
+__device__ __forceinline__ float mantissa(float x) {
+  if (!(fabsf(x) < INFINITY)) return NAN;
+  return x == 0.f ? 0.f : __uint_as_float((__float_as_uint(x) & 0x807fffffu) | 0x3f800000u);
+}
+
 struct __align__(16) SelShared {
   // read by the other CTAs of the cluster
   int hist[2][kBins];                // a round's counts; two, so that a round needs one barrier
@@ -86,6 +103,7 @@ struct __align__(16) SelShared {
   int warp_m[kSelWarps];
   float part[kSelWarps];
   float2 pair[kSelWarps];
+  int head_e[kMaxDecodeHI];          // exponents of |q_h|
   int bin, above, in_bin;
   uint32_t tkey;
   int digit, radix_above;            // the lone CTA's radix select
@@ -160,12 +178,12 @@ __device__ __forceinline__ unsigned long long pair_key(float2 a) {
   return order_key((double)a.x + (double)a.y);
 }
 
-// The dot product of n channels of q and k: a product is split by an fma (exact
+// The dot product of n channels of q, times qf (a power of two), and k: a product is split by an fma (exact
 // already for bf16 q), a sum by the exact error of an addition.  Eight channels
 // a step and no more unrolling: the code runs once a row, and fetching
 // instructions would take longer than the loop.
 template <typename T>
-__device__ __forceinline__ float2 dot_pair(const T* q, const float* k, int n) {
+__device__ __forceinline__ float2 dot_pair(const T* q, float qf, const float* k, int n) {
   float hi = 0.f, lo = 0.f;
 #pragma unroll 1
   for (int c = 0; c < n; c += 8) {
@@ -174,8 +192,8 @@ __device__ __forceinline__ float2 dot_pair(const T* q, const float* k, int n) {
     load8(k + c, kv);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float p = __fmul_rn(qv[e], kv[e]);
-      if (sizeof(T) == 4) lo += __fmaf_rn(qv[e], kv[e], -p);
+      const float x = qv[e] * qf, p = __fmul_rn(x, kv[e]);
+      if (sizeof(T) == 4) lo += __fmaf_rn(x, kv[e], -p);
       const float s = __fadd_rn(hi, p), t = __fsub_rn(s, hi);
       lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(p, t));
       hi = s;
@@ -185,19 +203,22 @@ __device__ __forceinline__ float2 dot_pair(const T* q, const float* k, int n) {
 }
 
 // Sums over the heads [h0, h0 + nh) of the exact scores of blocks block(0) ..
-// block(m - 1) on pages page(0) .. page(m - 1), each given to store(e, sum).
+// block(m - 1) on pages page(0) .. page(m - 1), each given to store(e, sum), all
+// times the same power of two: |w_h| |q_h| is at most about 2^we, |k| 2^ke.
 // Four threads a (block, head); scratch k_s holds the dequantised keys of a
 // round (up to 32 of them).  Called by the whole CTA.
 template <typename T, int BITS, typename B, typename P, typename S>
 __device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long row, float* k_s,
-                            int m, int h0, int nh, B block, P page, S store) {
+                            int m, int h0, int nh, int we, int ke, B block, P page, S store) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wpb = max(1, (nh + 7) / 8);                  // warps of a block
   const int per = kSelWarps / wpb;
   const int mine = warp / wpb, h = (warp - mine * wpb) * 8 + (lane >> 2), part = lane & 3;
   const int n4 = a.d / 4, pitch = a.d + 16;
   const T* qh = (const T*)a.q + (row * a.H + h0 + min(h, max(nh - 1, 0))) * a.d + part * n4;
-  const float w = h < nh ? a.w[row * a.H + h0 + h] : 0.f;
+  const int he = h < nh ? min(sh.head_e[h0 + h], 126) : 0;
+  const float w = h < nh ? ldexpf(a.w[row * a.H + h0 + h], he - we) : 0.f;
+  const float qf = pow2f(-he);
   for (int e0 = 0; e0 < m; e0 += per) {
     const int n = min(per, m - e0);
     // eight channels a thread: at most 32 keys of 256
@@ -216,7 +237,8 @@ __device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long r
       }
     }
     if (s < n) {
-      const float f = scale_value(scale);
+      const int se = (int)scale - ke;                    // below 1: nothing next to 2^ke
+      const float f = scale_value(se < 1 ? 0u : (uint32_t)min(se, 254));
       float v[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -229,7 +251,7 @@ __device__ void score_exact(SelShared& sh, const IndexDecodeArgs& a, long long r
     __syncthreads();
     if (mine < n) {                                      // warp-uniform
       float2 x = make_float2(0.f, 0.f);
-      if (h < nh) x = dot_pair(qh, k_s + mine * pitch + part * (n4 + 4), n4);
+      if (h < nh) x = dot_pair(qh, qf, k_s + mine * pitch + part * (n4 + 4), n4);
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {                 // the quarters, then the heads
         x = pair_add(x, pair_shfl(x, o));
@@ -334,34 +356,75 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     return;
   }
 
-  // error of a score per unit of |k_j|, from the row's own q and w: eight lanes a head
-  const T* q = (const T*)a.q + row * a.H * a.d;
+  // sum_h |w_h| |q_h| = aw * 2^ae, from the row's own q and w: eight lanes a head
+  static_assert(kSelWarps * 4 >= kMaxDecodeHI, "a head for every eight lanes");
   float aw = 0.f;
-  for (int h0 = warp * 4; h0 < a.H; h0 += kSelWarps * 4) {
-    const int h = h0 + (lane >> 3);
-    float n2 = 0.f;
+  int ae = kNoExp;
+  {
+    const int h = warp * 4 + (lane >> 3);
+    float n2 = 0.f, small = 0.f, big = 0.f;              // |q_h|^2, and times 2^160, 2^-160
     if (h < a.H) {
+      const T* q = (const T*)a.q + (row * a.H + h) * a.d;
 #pragma unroll 2
       for (int c = (lane & 7) * 8; c < a.d; c += 64) {
         float v[8];
-        load8(q + h * a.d + c, v);
+        load8(q + c, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n2 = fmaf(v[e], v[e], n2);
+        for (int e = 0; e < 8; ++e) {
+          const float s = v[e] * 0x1p80f, g = v[e] * 0x1p-80f;
+          n2 = fmaf(v[e], v[e], n2);
+          small = fmaf(s, s, small);
+          big = fmaf(g, g, big);
+        }
       }
     }
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-    if (h < a.H && (lane & 7) == 0) aw += fabsf(a.w[row * a.H + h]) * sqrtf(n2);
+    for (int o = 4; o > 0; o >>= 1) {
+      n2 += __shfl_xor_sync(0xffffffffu, n2, o);
+      small += __shfl_xor_sync(0xffffffffu, small, o);
+      big += __shfl_xor_sync(0xffffffffu, big, o);
+    }
+    if (h < a.H && (lane & 7) == 0) {
+      int e = 0;
+      if (!(n2 < 0x1p100f)) {
+        n2 = big;
+        e = 80;
+      } else if (n2 < 0x1p-80f) {
+        n2 = small > 0.f ? fmaxf(small, 0x1p-8f) : 0.f;
+        e = -80;
+      }
+      const float x = sqrtf(n2);                         // 0, or a normal number
+      e += exponent(x);
+      sh.head_e[h] = x > 0.f ? e : 0;
+      float w = fabsf(a.w[row * a.H + h]);
+      if (w < 0x1p-100f) {
+        w *= 0x1p49f;
+        e -= 49;
+      }
+      aw = mantissa(x) * mantissa(w);                    // NaN and infinite inputs: NaN
+      if (aw != 0.f) ae = e + exponent(w);
+    }
   }
-  aw = warp_sum(aw);
-  if (lane == 0) sh.part[warp] = aw;
+  auto align = [&]() {                                   // to the warp's largest exponent
+    const int top = __reduce_max_sync(0xffffffffu, ae);
+    aw *= ae - top < -126 ? 0.f : pow2f(ae - top);
+    aw = warp_sum(aw);
+    ae = top;
+  };
+  align();
+  if (lane == 0) {
+    sh.part[warp] = aw;
+    sh.warp_m[warp] = ae;
+  }
   for (int e = tid; e < kBins; e += kSel) sh.hist[0][e] = 0;
   if (tid == 0) {
     sh.bin = sh.above = sh.in_bin = 0;
     sh.tkey = 0u;
   }
   __syncthreads();
-  aw = warp_sum(sh.part[lane]);
+  aw = sh.part[lane];
+  ae = sh.warp_m[lane];
+  align();
   __syncthreads();
 
   asm volatile("griddepcontrol.wait;" ::: "memory");     // the scores
@@ -393,15 +456,16 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
     sh.pair[warp] = make_float2(mn, mx);
   }
   __syncthreads();
-  kmax = warp_max(sh.part[lane]);
+  kmax = fmaxf(warp_max(sh.part[lane]), 0x1p-35f);
   mn = -warp_max(-sh.pair[lane].x);
   mx = warp_max(sh.pair[lane].y);
   const uint32_t lo0 = order_key(mn), hi0 = order_key(mx);
   uint32_t lo = lo0, hi = hi0;
   auto key = [&](int j) { return is_staged ? staged[j] : order_key(score[j0 + j]); };
   // Inputs beyond fp32 (their row's blocks are unspecified) leave the fp32 scores.
-  float eps2 = 2.f * a.err * aw * kmax;
+  float eps2 = aw > 0.f ? ldexpf(2.f * a.err * aw * kmax, ae) + 0x1p-140f : 0.f;
   if (!(eps2 < 3e38f)) eps2 = 0.f;
+  const int ke = exponent(kmax);
 
   // ---- narrow [lo, hi] to a bin that holds the k-th largest key ------------------
   // Counts of the other CTAs' bins and this one's; returns the bin of the k-th
@@ -606,7 +670,7 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
       // does, otherwise over its share of the heads.
       const bool whole = CS == 1 || mc * ((a.H + 7) / 8) <= kSelWarps;
       const int share = whole ? a.H : (a.H + CS - 1) / CS, h0 = whole ? 0 : min(rank * share, a.H);
-      score_exact<T, BITS>(sh, a, row, k_s, mc, h0, min(share, a.H - h0),
+      score_exact<T, BITS>(sh, a, row, k_s, mc, h0, min(share, a.H - h0), ae, ke,
                            [&](int e) { return sh.close_j[e]; },
                            [&](int e) { return sh.close_page[e]; },
                            [&](int e, float2 v) { sh.exact[e] = v; });
@@ -679,7 +743,7 @@ __global__ void __launch_bounds__(kSel) index_select_kernel(const IndexDecodeArg
           [&](int j, int at) { list[at] = j; });
   if (need < m && eps2 > 0.f) {
     double* ex = a.exact + row * a.slots;
-    score_exact<T, BITS>(sh, a, row, k_s, m, 0, a.H, [&](int e) { return list[e]; },
+    score_exact<T, BITS>(sh, a, row, k_s, m, 0, a.H, ae, ke, [&](int e) { return list[e]; },
                          [&](int e) { return pages[page_index(a.cs, list[e])]; },
                          [&](int e, float2 v) { ex[e] = (double)v.x + (double)v.y; });
     int eq = 0;

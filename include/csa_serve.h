@@ -117,8 +117,10 @@ csa_status_t csa_cache_read(const void* cache, const int32_t* table, const int32
  * the lower block, in ascending order, then -1.  The set is that of the exact
  * scores: blocks whose fp32 score lies within the fp32 error of the topk-th
  * are scored again at twice fp32's precision.  The choice therefore depends
- * on the row's own inputs alone, not on the batch.  (Keys above 2^60, whose
- * squares leave fp32, leave their sequence to the fp32 scores.)
+ * on the row's own inputs alone, not on the batch.  This holds while no
+ * |q_I[h]| |k_j| and no sum of |w[h]| |q_I[h]| |k_j| reaches 2^126 and no key
+ * has a value above 2^60; a row beyond that is left to the fp32 scores, in
+ * which sums that overflow rank as infinite or, where they are NaN, last.
  *
  *   q_I        in   [b, s_q, H_I, d_I] of dt      w  in  [b, s_q, H_I] fp32
  *   table      in   [b, P] page table of the index keys (no ring: P *

@@ -144,7 +144,7 @@ def fp32_sets(keys, q, w, topk):
     return out
 
 
-def cancelling(rng, n, n_close, n_high, H, lift=1.0):
+def cancelling(rng, n, n_close, n_high, H):
     """Rows [n, 128] and q, w: of n_close blocks a product of 6 2^14 comes first and leaves last,
     and what decides between them, at most 6 2^-12, stands between; n_high blocks are far above,
     the others at zero."""
@@ -158,7 +158,7 @@ def cancelling(rng, n, n_close, n_high, H, lift=1.0):
     q = np.zeros((H, 128))
     q[:, 0], q[:, 96], q[:, 32], q[:, 33], q[:, 64] = 2.0 ** 14, 2.0 ** 14, 1.0, 2.0 ** -12, 4.0
     w = (np.abs(rng.standard_normal(H)) + 0.1).astype(np.float32).astype(np.float64)
-    return keys, q * lift, w
+    return keys, q, w
 
 
 CLOSE_CASES = [
@@ -198,3 +198,18 @@ def test_indexer_exact_ties_whose_fp32_scores_differ(n, topk, dtype, H, bits):
     for wrong in fp32_sets(keys, q, w, topk):
         assert not np.array_equal(wrong, np.arange(topk))
     assert np.array_equal(got, np.arange(topk))
+
+
+@pytest.mark.parametrize("dtype,H", [(BF, 32), (F32, 8)])
+@pytest.mark.parametrize("q_e,w_e,k_e", [(-70, 0, 0), (-90, 0, 0), (-110, 0, 0), (-90, 90, 0), (60, 0, 0), (85, 0, 0),
+                                         (85, -100, 0), (0, -110, 0), (0, -130, 0), (-60, 0, -60), (-100, 100, 30),
+                                         (20, 0, 50), (-60, 100, -80)])
+def test_indexer_is_exact_for_small_and_large_magnitudes(q_e, w_e, k_e, dtype, H):
+    """The same rows with q, w and the keys times powers of two: the choice is the same, though
+    squares of q, or products of w and q, leave fp32."""
+    n, n_close, n_high, topk = 600, 300, 40, 130
+    keys, q, w = cancelling(np.random.default_rng(H), n, n_close, n_high, H)
+    keys, q = np.ldexp(keys, k_e), np.ldexp(q, q_e)
+    w = np.ldexp(w, w_e).astype(np.float32).astype(np.float64)      # exponents below -126: rounded
+    got, want = select(keys, q, w, topk, 4, dtype=dtype)
+    assert np.array_equal(got, want)
