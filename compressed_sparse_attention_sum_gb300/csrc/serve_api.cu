@@ -53,6 +53,24 @@ bool valid_rows(const void* p, long long batch_stride, long long row_stride, csa
   return b == 1 || batch_stride >= 0;
 }
 
+// Whether rows [b, s] of d elements at these strides share elements (a row stride
+// below d is refused already where s > 1).  Only two batches can, in rows i and
+// i + m whose distance is within d of a multiple of the row stride.
+bool rows_overlap(long long bs, long long rs, int d, int s, int b) {
+  if (b < 2) return false;
+  if (bs < d) return true;
+  if (s < 2) return false;
+  using Wide = __int128;
+  const Wide last = (Wide)(s - 1) * rs;
+  if (bs >= last + d || rs >= (Wide)(b - 1) * bs + d) return false;
+  for (int m = 1; m < b && m * (Wide)bs < last + d; ++m) {
+    const Wide at = m * (Wide)bs, below = at / rs * rs, above = below + rs;
+    if (at - below < d && below <= last && below > 0) return true;
+    if (above - at < d && above <= last) return true;
+  }
+  return false;
+}
+
 csa_status_t check_cache_rows(const void* x, long long bs, long long rs, csa_dtype_t dt,
                               const int32_t* table, const int32_t* pos0, const void* cache, int b,
                               int s, int d, int P, int n_pages, int page_size, int bits) {
@@ -109,8 +127,11 @@ csa_status_t csa_cache_read(const void* cache, const int32_t* table, const int32
                             int n_pages, int page_size, int bits, csa_stream_t stream) {
   const csa_status_t st = check_cache_rows(out, out_batch_stride, out_row_stride, dt, table, pos0,
                                            cache, b, s, d, P, n_pages, page_size, bits);
-  if (st != CSA_OK || b == 0 || s == 0) return st;
-  if (s > (long long)P * page_size || (b > 1 && out_batch_stride < d)) return CSA_ERR_INVALID_ARG;
+  if (st == CSA_ERR_INVALID_ARG || b == 0 || s == 0) return st;
+  if (b <= kMaxRows && rows_overlap(out_batch_stride, out_row_stride, d, s, b))
+    return CSA_ERR_INVALID_ARG;
+  if (st != CSA_OK) return st;
+  if (s > (long long)P * page_size) return CSA_ERR_INVALID_ARG;
   return from_cuda(csa::launch_cache_read(
       cache, table, pos0, counts, out, out_batch_stride, out_row_stride, dt == CSA_BF16, b, s, d,
       P, n_pages, page_size, bits, csa::device_status_word(), (cudaStream_t)stream));

@@ -96,8 +96,8 @@ csa_status_t csa_cache_write(const void* x, long long x_batch_stride, long long 
  * one that took its slot.
  *   out  out  [b, s, d] of dt; strides in elements, rows contiguous; rows may
  *             not overlap
- * Other arguments and errors as csa_cache_write; also INVALID_ARG for a batch
- * stride below d where b > 1.
+ * Other arguments and errors as csa_cache_write; also INVALID_ARG for strides
+ * at which two rows of out share an element.
  */
 csa_status_t csa_cache_read(const void* cache, const int32_t* table, const int32_t* pos0,
                             const int32_t* counts, void* out, long long out_batch_stride,
