@@ -89,7 +89,10 @@ bool decode_sizes(int b, int s_q, int H, int d, int window, long long cmp_rows) 
   return b >= 1 && s_q >= 1 && H >= 1 && d >= 32 && d % 32 == 0 && window >= 1 && cmp_rows >= 0;
 }
 
-// Partial results of a call whose queries are cut into parts.
+// Partial results of a call whose queries are cut into parts: rows * parts * H of
+// them.  On CUDA cores rows * parts * ceil(H / 8) <= 304, so at most 2432; on the
+// tensor cores rows * H <= 64 c for c CTAs a split and parts <= (144 / c + 3) / 4
+// with c <= 12, so at most 2880: the bound that csa_serve.h gives.
 size_t attn_decode_layout(csa::AttnDecodeArgs* a, int parts, unsigned char* ws) {
   a->parts = parts;
   if (parts == 1) return 0;

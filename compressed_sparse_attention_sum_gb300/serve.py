@@ -272,7 +272,9 @@ def csa_indexer_topk_decode(q_I: torch.Tensor, cache: torch.Tensor, table: torch
 
 def csa_attn_decode_workspace_size(b: int, s_q: int, H: int, d: int, window: int,
                                    cmp_rows: int) -> int:
-    """Workspace bytes (0: none needed); cmp_rows = K, or P_cmp * page_size when idx is None."""
+    """Workspace bytes (0: none needed); cmp_rows = K, or P_cmp * page_size when idx is None.
+    Smaller calls may need more (they are cut into more parts), none more than
+    2880 * (4 * d + 8) + 16."""
     return int(load_library().csa_attn_decode_workspace_size(b, s_q, H, d, window, cmp_rows))
 
 

@@ -168,7 +168,13 @@ csa_status_t csa_indexer_topk_decode(const void* q_I, const void* cache, const i
  *   o          out  [b, s_q, H, d] of dt           lse   out [b, s_q, H] fp32
  *   workspace       csa_attn_decode_workspace_size bytes (K, or
  *                   P_cmp * page_size when idx is NULL, as its last argument),
- *                   16-byte aligned, used by one call at a time
+ *                   16-byte aligned, used by one call at a time.  The size is
+ *                   that of the kernels of either dt, and a call needs it
+ *                   whichever of them it takes; NULL where it is 0.  It does
+ *                   not grow with b, s_q or the rows: fewer queries are cut
+ *                   into more parts.  A workspace for calls of several sizes
+ *                   has the largest of theirs, or 2880 * (4 d + 8) + 16 bytes,
+ *                   which no size exceeds.
  * Errors: INVALID_ARG for null pointers (P_cmp == 0 allows a null cmp_table,
  * K must then be 0), misaligned q, cache, o, workspace, sizes outside the
  * limits, a ring smaller than the windows, a scale that is not finite; UNSUPPORTED

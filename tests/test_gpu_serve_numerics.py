@@ -85,6 +85,36 @@ def test_attention_weights_add_up_to_one(case):
         assert bool(((lse[:, i].double() - want[:, None]).abs() <= 2.0 ** -11).all())
 
 
+def test_attention_workspace_of_the_stated_bound_serves_every_batch():
+    """One buffer of the bound for batches of 64 to 1 sequences, with results as with a workspace of
+    the call's own; a buffer of the larger batch's size is refused by a smaller one."""
+    d, H, page, n, K = 128, 32, 64, 3000, 512
+    rng = np.random.default_rng(3)
+    n_pages, (raw_t, cmp_t) = tables(rng, 64, 2, -(-n // page))
+    raw_t, cmp_t = dev(raw_t), dev(cmp_t)
+    cache = empty_cache(n_pages, page, d, 4)
+    zero = torch.zeros(64, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rows = torch.randn(64, n, d, generator=g, device="cuda").to(BF)
+    serve.csa_cache_write(rows, cache, raw_t, zero, page, 4)
+    serve.csa_cache_write(rows, cache, cmp_t, zero, page, 4)
+    bound = torch.empty(2880 * (4 * d + 8) + 16, dtype=torch.uint8, device="cuda")
+    for dtype in (BF, F32):
+        for b in (64, 8, 1):
+            q = torch.randn(b, 1, H, d, generator=g, device="cuda").to(dtype)
+            idx = torch.randint(0, n, (b, 1, K), generator=g, device="cuda", dtype=torch.int32)
+            for ix in (idx, None):
+                args = (q, cache, raw_t[:b], cmp_t[:b], ix, None, zero[:b] + n, d ** -0.5, 1, 100, page, 4)
+                want = serve.csa_attn_decode(*args)
+                got = serve.csa_attn_decode(*args, workspace=bound)
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    small = serve.csa_attn_decode_workspace_size(64, 1, H, d, 100, K)
+    assert small < serve.csa_attn_decode_workspace_size(1, 1, H, d, 100, K)
+    with pytest.raises(serve.CSAError):
+        serve.csa_attn_decode(q, cache, raw_t[:1], cmp_t[:1], idx, None, zero[:1] + n, d ** -0.5, 1, 100, page, 4,
+                              workspace=bound[:max(small, 16)])
+
+
 # ----------------------------------------------------------------- indexer
 
 def select(keys, q, w, topk, bits, page=64, dtype=BF):

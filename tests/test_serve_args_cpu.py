@@ -26,3 +26,13 @@ def test_rows_of_a_read_that_share_elements_are_refused(lib):
         assert got == (INVALID if shared else UNSUPPORTED), (b, s, bs, rs)
         seen.add(shared)
     assert seen == {True, False}
+
+
+def test_no_attention_workspace_exceeds_the_stated_bound(lib):
+    """... and it does shrink as a batch grows, so the largest batch's size is not the bound."""
+    size = lib.csa_attn_decode_workspace_size
+    for d, H in itertools.product((32, 64, 96, 512), (1, 7, 8, 16, 32, 33, 64, 96, 128)):
+        for b, s_q in itertools.product((1, 2, 3, 5, 8, 11, 12, 13, 24, 36, 64, 76, 144, 152, 304, 400), (1, 2, 3, 4, 7)):
+            for window, rows in itertools.product((1, 128), (0, 512, 1100, 1 << 20)):
+                assert size(b, s_q, H, d, window, rows) <= 2880 * (4 * d + 8) + 16, (d, H, b, s_q, window, rows)
+    assert size(8, 1, 32, 128, 128, 512) > size(64, 1, 32, 128, 128, 512) == 0
