@@ -50,8 +50,8 @@ struct Cfg512 {
   static constexpr uint32_t P = KV + 3 * kBuf;             // [64 columns][128 B: 64 slots]
   static constexpr uint32_t XCH = P + kNC5 * 128;          // [8 warps][32 lanes][16] halves of S to be added; at the
                                                            // end [64][4] sums as rounded
-  static constexpr uint32_t BARS = XCH + kSoft5 * 2048;    // kv[3], o[3], s, sfree, p, q
-  static constexpr uint32_t MISC = BARS + 10 * 8;          // TMEM slot, dead
+  static constexpr uint32_t BARS = XCH + kSoft5 * 2048;    // kv[3], o[3], s, sfree, p, q, end
+  static constexpr uint32_t MISC = BARS + 11 * 8;          // TMEM slot, dead
   static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][64][4] column maxima
   static constexpr uint32_t MRUN = RED + 8 * kNC5 * 4;     // [64] at the end
   static constexpr uint32_t ML = MRUN + kNC5 * 4;          // [64] (maximum, sum, O's factor) of this CTA
@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
   uint64_t* bar_sfree = bar_kv + 7;                               // S' read
   uint64_t* bar_p = bar_kv + 8;                                   // P written
   uint64_t* bar_q = bar_kv + 9;                                   // Q written
+  uint64_t* bar_end = bar_kv + 10;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
   float* red = reinterpret_cast<float*>(sm + C::RED);
@@ -131,6 +132,8 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     CSA_TMEM_ST32(taddr, w);
   };
   if (!conv && warp < kConv5 + kSoft5) read_q(0);
+  int armed = 0;                                           // test hook (attn_decode_tc.cu)
+  if (warp == kConv5 + kSoft5) armed = armed_fault(a.status);
   float sink_v = -INFINITY;
   if (tid < heads && tid < NC && a.sink != nullptr) sink_v = __ldg(a.sink + h0 + tid) * kLog2e;
 
@@ -155,6 +158,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     mbar_init(bar_sfree, kSoft5);
     mbar_init(bar_p, kSoft5);
     mbar_init(bar_q, kSoft5);
+    mbar_init(bar_end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *dead = 0;
   }
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     const uint32_t td = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t kvd = sw128_desc(smem_addr(sm + C::KV)), pd = sw128_desc(smem_addr(sm + C::P));
     const uint64_t kvd_mn = sw128_desc_mn(smem_addr(sm + C::KV), C::kBlk);
-    bool up = wait_warp(bar_q, 0);
+    bool up = wait_warp(bar_q, 0) && (armed != kSiteDecode || split != splits - 1);
     int buf = 0, bo = 0;                                   // of tile it, of tile it - 1
     uint32_t ph = 0;
     for (int it = 0; up && it <= n; ++it) {
@@ -549,10 +553,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
   if (cs > 1) cg::this_cluster().sync();
   else __syncthreads();
   finish_decode<C, D, NC>(a, sm, *dead != 0, n, cs, rank, split, per_group, nq, heads, h0, row0);
-  if (warp == kConv5 + kSoft5 && n > 0) {
-    fence_after();
-    tmem_dealloc(tmem, 512);
-  }
+  if (warp == kConv5 + kSoft5 && n > 0) free_tmem(tmem, 512, *dead != 0, bar_end);
   if (cs > 1) cg::this_cluster().sync();                   // no CTA leaves while another reads it
 }
 

@@ -18,6 +18,20 @@ namespace cg = cooperative_groups;
 constexpr int kSiteDecode = 0x73;
 constexpr float kRescale = 8.f;               // a column's maximum may lag by 2^8
 
+// Frees the TMEM of a CTA, by the warp that allocated it and issued the products.
+// After a wait that gave up, products may still run: they are waited for first,
+// again with a limit.
+__device__ __forceinline__ void free_tmem(uint32_t tmem, uint32_t columns, bool dead, uint64_t* bar_end) {
+  if (dead) {
+    if (elect_one()) mma_commit(bar_end);
+    __syncwarp();
+    mbar_wait(bar_end, 0);
+    __syncwarp();
+  }
+  fence_after();
+  tmem_dealloc(tmem, columns);
+}
+
 // Transposing butterfly: v[c] holds this lane's value of column c; afterwards
 // lanes l and l + 16 hold op over all 32 lanes of column l % 16.
 template <bool kMax>

@@ -70,8 +70,8 @@ struct Cfg {
   static constexpr uint32_t Q = 0;
   static constexpr uint32_t KV = (D / 64) * kQBlk;
   static constexpr uint32_t P = KV + kBlocks * kKvBlk;
-  static constexpr uint32_t BARS = P + kSlots * 128;       // s, p, kv[kParts], o[kParts]
-  static constexpr uint32_t MISC = BARS + (2 + 2 * kParts) * 8;   // TMEM slot, dead
+  static constexpr uint32_t BARS = P + kSlots * 128;       // s, p, kv[kParts], o[kParts], end
+  static constexpr uint32_t MISC = BARS + (3 + 2 * kParts) * 8;   // TMEM slot, dead
   static constexpr uint32_t RED = (MISC + 8 + 15) / 16 * 16;   // [2][4][NC] column maxima
   static constexpr uint32_t MRUN = RED + 8 * NC * 4;       // [2][NC]
   static constexpr uint32_t ML = MRUN + 2 * NC * 4;        // [NC] (maximum, sum, O's factor) of this CTA
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   uint64_t* bar_p = bar_s + 1;
   uint64_t* bar_kv = bar_s + 2;
   uint64_t* bar_o = bar_kv + C::kParts;
+  uint64_t* bar_end = bar_o + C::kParts;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::MISC);
   volatile int* dead = reinterpret_cast<int*>(sm + C::MISC + 4);
   float* red = reinterpret_cast<float*>(sm + C::RED);
@@ -139,6 +140,11 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
     }
   };
   read_q(0);
+  // Test hook (csa_debug_arm_fault): with kSiteDecode armed the last split of each
+  // query issues no product, so that the waits for the first run out with none in
+  // flight.
+  int armed = 0;
+  if (warp == C::kWarps) armed = armed_fault(a.status);
   float sink_v = -INFINITY;
   if (tid < heads && tid < NC && a.sink != nullptr) sink_v = __ldg(a.sink + h0 + tid) * kLog2e;
 
@@ -160,6 +166,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   if (tid == 0) {
     mbar_init(bar_s, 1);
     mbar_init(bar_p, C::kWarps);
+    mbar_init(bar_end, 1);
     for (int m = 0; m < C::kParts; ++m) {
       mbar_init(&bar_kv[m], C::kWarps);
       mbar_init(&bar_o[m], 1);
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
         mma_bf16_ts(td + C::kColR, td + C::kColA, pd_mn + ((k * 2048) >> 4), idesc_r,
                     (it > 0 || k > 0) ? 1u : 0u);
     };
-    bool up = true;
+    bool up = armed != kSiteDecode || split != splits - 1;
     for (int it = 0; up && it < n; ++it) {
 #pragma unroll
       for (int x = 0; x < C::kParts; ++x) {
@@ -557,10 +564,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   if (cs > 1) cg::this_cluster().sync();
   else __syncthreads();
   finish_decode<C, D, NC>(a, sm, *dead != 0, n, cs, rank, split, per_group, nq, heads, h0, row0);
-  if (warp == C::kWarps && n > 0) {
-    fence_after();
-    tmem_dealloc(tmem, C::kTmem);
-  }
+  if (warp == C::kWarps && n > 0) free_tmem(tmem, C::kTmem, *dead != 0, bar_end);
   if (cs > 1) cg::this_cluster().sync();                   // no CTA leaves while another reads it
 }
 

@@ -47,7 +47,7 @@ struct Cfg {
   static constexpr uint32_t K = (D / 64) * kQBlk;
   static constexpr uint32_t W = K + (D / 64) * kBlk;     // [NC] head weights
   static constexpr uint32_t BAR = W + NC * 4;
-  static constexpr uint32_t MISC = BAR + 8;              // TMEM slot, dead
+  static constexpr uint32_t MISC = BAR + 16;             // after the tiles' barrier and the end's: TMEM slot, dead
   static constexpr uint32_t BND = MISC + 8;              // [2][8], by tile parity
   static constexpr uint32_t RNG = BND + 64;              // [NC / 16][4] score ranges of the warps
   static constexpr uint32_t SUM = RNG + NC / 16 * 32;    // [2][NC / 16][128] half the heads' sums
@@ -83,10 +83,15 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
 
   if (tid == 0) {
     mbar_init(bar, 1);
+    mbar_init(bar + 1, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     *dead = 0;
   }
   if (warp == 0) tmem_alloc(tmem_slot, NC);
+  // Test hook (csa_debug_arm_fault): with kSiteIndex armed the first CTA of each
+  // sequence issues no product, so that the wait for it runs out with none in flight.
+  int armed = 0;
+  if (tid == 0) armed = armed_fault(a.status);
 
   const int32_t* pages = a.table + (long long)bi * a.P;
   // Two threads expand a key: lane l and l + 16 of a warp, 16 keys a warp.
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
     fence_proxy_async_smem();
     fence_before();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0 && (armed != kSiteIndex || blockIdx.x != 0)) {
       fence_after();
       constexpr uint32_t idesc = idesc_bf16_f32_major(kIdxTile, NC, 0, 0);
       const uint32_t ka = smem_addr(sm + C::K), qa = smem_addr(sm);
@@ -239,7 +244,13 @@ __global__ void __launch_bounds__(kThreads, NC == 64 ? 4 : 3) index_scores_tc_ke
     parity ^= 1;
     if (*dead) break;
   }
-  if (tid == 0 && *dead) set_status(a.status, kDevTimeout, kSiteIndex);
+  if (tid == 0 && *dead) {
+    set_status(a.status, kDevTimeout, kSiteIndex);
+    // products may still run: wait for them, again with a limit, before TMEM is freed
+    mma_commit(bar + 1);
+    mbar_wait(bar + 1, 0);
+  }
+  __syncwarp();
   if (warp == 0) {
     fence_after();
     tmem_dealloc(tmem, NC);

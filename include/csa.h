@@ -584,8 +584,12 @@ csa_status_t csa_get_device_status(csa_stream_t stream, int* status_out, int* si
  * device never requests its Q tile, so its bounded wait runs out (about one
  * second) with no copy or MMA in flight and records CSA_ERR_TIMEOUT at 0x21;
  * with site = 0x25 its union-size check trips and records
- * CSA_ERR_DEVICE_CHECK at 0x25.  site = 0 disarms.  The call synchronizes
- * the device.  Use it only in tests.
+ * CSA_ERR_DEVICE_CHECK at 0x25.  With site = 0x73 (csa_serve.h) the last CTA of
+ * each query's split in every later tensor-core csa_attn_decode, with site =
+ * 0x74 the first CTA of each sequence in every later tensor-core
+ * csa_indexer_topk_decode, issues no product, and its wait for one runs out
+ * likewise.  site = 0 disarms.  The call synchronizes the device.  Use it only
+ * in tests.
  * Errors: INVALID_ARG for site < 0; CSA_ERR_CUDA if the device is unusable.
  */
 csa_status_t csa_debug_arm_fault(int site);
