@@ -94,13 +94,13 @@ __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(const AttnDe
     if (lane == 0) a.part_ml[at] = make_float2(m, l);
     return;
   }
-  const float sink2 = a.sink != nullptr ? a.sink[h] * kLog2e : -INFINITY;
+  const float sink2 = a.sink != nullptr ? sink_log2(a.sink[h]) : -INFINITY;
   const float mm = fmaxf(m, sink2);
   float f = 0.f, out_l = -INFINITY;
   if (mm > -INFINITY) {
     const float fm = exp2f(m - mm), total = fmaf(l, fm, exp2f(sink2 - mm));
     f = fm / total;
-    out_l = (mm + log2f(total)) * kLn2;
+    out_l = l * fm == 0.f ? a.sink[h] : (mm + log2f(total)) * kLn2;
   }
 #pragma unroll
   for (int k = 0; k < ND; ++k)
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(128) attn_decode_combine_kernel(const AttnDeco
   if (rh >= (long long)a.b * a.s_q * a.H) return;
   const long long row = rh / a.H;
   const int h = (int)(rh - row * a.H);
-  const float sink2 = a.sink != nullptr ? a.sink[h] * kLog2e : -INFINITY;
+  const float sink2 = a.sink != nullptr ? sink_log2(a.sink[h]) : -INFINITY;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float2* ml = a.part_ml + row * a.parts * a.H + h;
   float m = sink2;
@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(128) attn_decode_combine_kernel(const AttnDeco
     if (v.y > 0.f) total = fmaf(v.y, exp2f(v.x - m), total);
   }
   total = warp_sum(total);
+  const bool rows = total > 0.f;
   if (sink2 > -INFINITY) total += exp2f(sink2 - m);
   const float inv = total > 0.f ? 1.f / total : 0.f;
   for (int c = lane * 4; c < a.d; c += 128) {
@@ -162,7 +163,8 @@ __global__ void __launch_bounds__(128) attn_decode_combine_kernel(const AttnDeco
       *reinterpret_cast<float4*>(dst) = acc;
     }
   }
-  if (lane == 0) a.lse[rh] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
+  if (lane == 0)
+    a.lse[rh] = rows ? (m + log2f(total)) * kLn2 : sink2 > -INFINITY ? a.sink[h] : -INFINITY;
 }
 
 template <typename T, int BITS>

@@ -2,6 +2,7 @@
 // point (internal to the library).
 #pragma once
 
+#include <cfloat>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,6 +31,12 @@ struct AttnDecodeArgs {
   CacheShape cs;
   int* status;
 };
+
+// A sink in log2 units, always finite (a sink of -inf has no weight all the same).
+// Where the rows' part of the denominator is 0 next to it, LSE is the sink as given.
+__device__ __forceinline__ float sink_log2(float sink) {
+  return fminf(fmaxf(sink * kLog2e, -FLT_MAX), FLT_MAX);
+}
 
 // Slots of one query are numbered: the window's `window` positions, then the
 // K index entries (or the visible blocks).  Every slot is looked up on its

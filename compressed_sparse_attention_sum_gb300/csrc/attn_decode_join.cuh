@@ -100,11 +100,14 @@ __device__ __forceinline__ void join_cluster(const AttnDecodeArgs& a, unsigned c
       if (c == 0) a.part_ml[at] = make_float2(m, total);
       continue;
     }
+    const bool rows = total > 0.f;
     if (sink2 > -INFINITY) total += ex2(sink2 - m);
     const float inv = total > 0.f ? __fdividef(1.f, total) : 0.f;
     *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + (row * a.H + h0 + h) * D + c) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (c == 0) a.lse[row * a.H + h0 + h] = m > -INFINITY ? (m + log2f(total)) * kLn2 : -INFINITY;
+    if (c == 0)
+      a.lse[row * a.H + h0 + h] = rows ? (m + log2f(total)) * kLn2
+                                       : sink2 > -INFINITY ? a.sink[h0 + h] : -INFINITY;
   }
 }
 

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
   int armed = 0;
   if (warp == C::kWarps) armed = armed_fault(a.status);
   float sink_v = -INFINITY;
-  if (tid < heads && tid < NC && a.sink != nullptr) sink_v = __ldg(a.sink + h0 + tid) * kLog2e;
+  if (tid < heads && tid < NC && a.sink != nullptr) sink_v = sink_log2(__ldg(a.sink + h0 + tid));
 
   // The slots: the union window of the group's queries, then the index
   // entries (one query) or the blocks the last query sees.
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D, NC>::kBound, 1) attn_decode_tc_kernel(
         if (m > -INFINITY) {
           const float fm = ex2(mine.x - m), total = fmaf(mine.y, fm, ex2(sink2 - m));
           f = __fdividef(fm, total) * even;
-          out = (m + log2f(total)) * kLn2;
+          out = mine.y * fm == 0.f ? a.sink[h0 + h] : (m + log2f(total)) * kLn2;
         }
         m_run[tid] = f;
         if (live && !*dead) a.lse[(row0 + qi) * a.H + h0 + h] = out;

@@ -6,7 +6,7 @@ import torch
 
 from compressed_sparse_attention_sum_gb300 import csa, serve
 from oracle import serve_oracle as orc
-from test_gpu_serve import BF, F32, dev, empty_cache, f64, tables
+from test_gpu_serve import BF, F32, attn_case, check_row, dev, empty_cache, f64, run_attn, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -83,6 +83,40 @@ def test_attention_weights_add_up_to_one(case):
         # logits are exact up to fp32 roundings of scale and of scale * log2 e (2^-23 of 2 s < 1.4), the
         # sum as above and one rounding of lse
         assert bool(((lse[:, i].double() - want[:, None]).abs() <= 2.0 ** -11).all())
+
+
+# b, s_q, H, d, K (0: every visible block), bits, dtype
+SINK_CASES = [(2, 1, 32, 128, 200, 4, BF), (100, 1, 16, 128, 40, 8, BF), (2, 3, 16, 128, 0, 4, BF), (1, 2, 32, 128, 0, 8, BF),
+              (2, 1, 64, 512, 100, 4, BF), (100, 1, 64, 512, 40, 8, BF), (2, 2, 8, 512, 0, 4, BF), (2, 1, 5, 96, 60, 8, BF),
+              (130, 1, 16, 64, 20, 4, F32), (2, 2, 16, 128, 300, 4, F32)]
+
+
+@pytest.mark.parametrize("case", SINK_CASES, ids=lambda c: f"b{c[0]}s{c[1]}H{c[2]}d{c[3]}K{c[4]}_{c[5]}bit")
+def test_attention_sinks_at_the_ends_of_fp32_and_empty_queries(case):
+    """lse is the sink itself, to the bit, where a query has no row, and where the rows have no
+    part in the denominator; a sink of fp32's lowest value or -inf changes nothing."""
+    b, s_q, H, d, K, bits, dtype = case
+    n = 700
+    lens = [n] + [0] * (b - 1)
+    spec = (b, s_q, H, d, 1, 33, lens, K, bits, 16, dtype, True)
+    cache, raw_t, cmp_t, raw, cmp, idx, q, sink = attn_case(np.random.default_rng(H + d), spec)
+    top = np.finfo(np.float32).max
+    sink[:5] = [top, -top, -np.inf, 3e38, -2.5e38][:H]
+    if idx is not None:
+        idx[0] = np.arange(K)
+    o, lse = run_attn(spec, (cache, raw_t, cmp_t, raw, cmp, idx, q, sink))
+    assert csa.csa_get_device_status() == 0
+    want = torch.from_numpy(sink).cuda()
+    assert bool((o[1:] == 0).all()) and torch.equal(lse[1:], want.expand(b - 1, s_q, H))
+    for h in (0, 3):
+        assert bool((o[0, :, h] == 0).all()) and bool((lse[0, :, h] == want[h]).all())
+    # the others, and heads without a weight for the sink, against the oracle
+    r, c = orc.held_rows(f64(raw[0, :n]), bits), orc.held_rows(f64(cmp[0]), bits)
+    rest = [h for h in range(H) if h not in (0, 3)]
+    for i in range(s_q):
+        t = n - s_q + i
+        check_row(o[0, i, rest], lse[0, i, rest], f64(q)[0, i, rest], lambda p: r[p], lambda j: c[j],
+                  None if idx is None else idx[0, i], sink[rest], d ** -0.5, t, 1, 33, dtype)
 
 
 def test_attention_workspace_of_the_stated_bound_serves_every_batch():
