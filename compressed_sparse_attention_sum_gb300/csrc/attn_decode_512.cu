@@ -132,8 +132,6 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     CSA_TMEM_ST32(taddr, w);
   };
   if (!conv && warp < kConv5 + kSoft5) read_q(0);
-  int armed = 0;                                           // test hook (attn_decode_tc.cu)
-  if (warp == kConv5 + kSoft5) armed = armed_fault(a.status);
   float sink_v = -INFINITY;
   if (tid < heads && tid < NC && a.sink != nullptr) sink_v = sink_log2(__ldg(a.sink + h0 + tid));
 
@@ -257,6 +255,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
     const uint32_t td = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t kvd = sw128_desc(smem_addr(sm + C::KV)), pd = sw128_desc(smem_addr(sm + C::P));
     const uint64_t kvd_mn = sw128_desc_mn(smem_addr(sm + C::KV), C::kBlk);
+    const int armed = armed_fault(a.status);               // test hook (attn_decode_tc.cu)
     bool up = wait_warp(bar_q, 0) && (armed != kSiteDecode || split != splits - 1);
     int buf = 0, bo = 0;                                   // of tile it, of tile it - 1
     uint32_t ph = 0;
