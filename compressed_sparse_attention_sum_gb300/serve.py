@@ -73,14 +73,16 @@ def _refuse(dev, **tensors):
 
 
 # torch's allocation without its dispatcher, as its compiler's generated code
-# calls it: 2 us of a call instead of 4 (torch.empty) or 7 (new_empty).
+# calls it: 2 us of a call instead of 4 (torch.empty) or 7 (new_empty).  Only
+# where no dispatch mode is active, so that one sees every output's allocation.
+_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
 _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
-                         "_empty_strided_cuda", None)
+                         "_empty_strided_cuda", None) if _modes is not None else None
 
 
 def _empty(shape, stride, dtype, dev):
     """An uninitialised contiguous tensor on device dev."""
-    if _empty_strided is not None and torch._C._cuda_getDevice() == dev:
+    if _empty_strided is not None and _modes() == 0 and torch._C._cuda_getDevice() == dev:
         return _empty_strided(shape, stride, dtype)
     return torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
 
@@ -334,6 +336,7 @@ def csa_attn_decode(q: torch.Tensor, cache: torch.Tensor, raw_table: torch.Tenso
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
     _call("csa_attn_decode", dev, stream, q.data_ptr(), cache.data_ptr(), raw_table.data_ptr(),
-          cmp_ptr, idx_ptr, sink_ptr, seq_lens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), b, s_q, H, d, ratio, window,
-          K, P_raw, P_cmp, n_pages, page_size, bits, dt, ws, nbytes)
+          cmp_ptr, idx_ptr, sink_ptr, seq_lens.data_ptr(), float(scale), out.data_ptr(),
+          lse.data_ptr(), b, s_q, H, d, ratio, window, K, P_raw, P_cmp, n_pages, page_size, bits,
+          dt, ws, nbytes)
     return out, lse
