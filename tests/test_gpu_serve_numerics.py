@@ -277,3 +277,24 @@ def test_indexer_is_exact_for_small_and_large_magnitudes(q_e, w_e, k_e, dtype, H
     w = np.ldexp(w, w_e).astype(np.float32).astype(np.float64)      # exponents below -126: rounded
     got, want = select(keys, q, w, topk, 4, dtype=dtype)
     assert np.array_equal(got, want)
+
+
+# --------------------------------------------------- blocks as they complete
+
+@pytest.mark.parametrize("ratio", [4, 128])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_overlapping_blocks_pooled_as_they_complete(ratio, dtype):
+    """csa_compress_overlap of the last two blocks: its second entry is the sequence's.  Both pool
+    the same tokens in fp32 and cast once; the order of at most 256 terms may differ (2^-16 of
+    sum w |kv| each way), which may move a cast by one step (2^-8, 2^-24 in fp32)."""
+    g = torch.Generator(device="cuda").manual_seed(ratio)
+    b, n, d = 2, 5 * ratio, 128
+    kv = torch.randn(b, n, d, generator=g, device="cuda").to(dtype)
+    score = torch.randn(b, n, d, generator=g, device="cuda").to(dtype)
+    whole = csa.csa_compress_overlap(kv, score, ratio, 2)
+    top = kv.abs().max().item()
+    for j in range(1, n // ratio):
+        last = slice((j - 1) * ratio, (j + 1) * ratio)
+        got = csa.csa_compress_overlap(kv[:, last].contiguous(), score[:, last].contiguous(), ratio, 2)[:, 1]
+        tol = 2.0 ** -15 * top + (2.0 ** -7 * top if dtype == BF else 0.0)
+        assert (got.float() - whole[:, j].float()).abs().max().item() <= tol
