@@ -20,10 +20,12 @@
 // row of S' is a column of the softmax: its maximum and sum stay within a thread
 // but for the four that share a row.
 //
-// 128 queries of 64 heads, 1152 slots each (18 tiles), 4 bits: 40 us, of which 9
-// are the prologue and the end.  With one tile of 128 slots and its chain: 52.7 us;
-// with two tiles of 64, Q in shared memory and slots as the rows of S': 49.9 us
-// (16 expanding warps instead of 8: 50.7 us).  What bounds it: 3.6k cycles a tile,
+// 128 queries of 64 heads, 1152 slots each (18 tiles), 4 bits: 41.4 us in a graph
+// that finds the rows in L2 (45.8 us where it does not), of which 9 are the prologue
+// and the end.  40.4 us with one sum of P instead of two (attn_decode_tc.cu).
+// Compared with that, one tile of 128 slots and its chain: 52.7 us; two tiles of 64,
+// Q in shared memory and slots as the rows of S': 49.9 us (16 expanding warps
+// instead of 8: 50.7 us).  What bounds it: 3.6k cycles a tile,
 // of which the tensor core takes 2.1k (16 products of N = 128 and 16 of N = 64);
 // shared memory moves 224 KB, 1.75k cycles, and its queue delays the expansion
 // and the softmax, whose instructions fill about half of the issue slots.

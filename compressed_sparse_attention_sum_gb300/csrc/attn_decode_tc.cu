@@ -24,8 +24,10 @@
 // stored.
 //
 // What bounds it: the latency of the chain index - page - codes - S - softmax -
-// O - join (64 queries of 32 x 128, 8 bits: 11.7 us, 5 tiles each).  The
-// arithmetic is that of attn_tc512.cu: probabilities rounded to bf16 for the
+// O - join (64 queries of 32 x 128, 8 bits, 5 tiles each: 12.2 us in a graph that
+// finds its rows in L2, 14.4 us where it does not).
+//
+// The arithmetic is that of attn_tc512.cu: probabilities rounded to bf16 for the
 // product with the values (the tensor core takes them so; each errs by at most
 // 2^-8 of itself), two sums of them in fp32 and the running maximum in fp32,
 // rescaling only when a column's maximum grows by more than 2^8.  LSE takes the
