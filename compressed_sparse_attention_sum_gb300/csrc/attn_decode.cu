@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_simt_kernel(const AttnDe
   if (mm > -INFINITY) {
     const float fm = exp2f(m - mm), total = fmaf(l, fm, exp2f(sink2 - mm));
     f = fm / total;
-    out_l = l * fm == 0.f ? a.sink[h] : (mm + log2f(total)) * kLn2;
+    out_l = sink2 > -INFINITY && l * fm == 0.f ? a.sink[h] : (mm + log2f(total)) * kLn2;
   }
 #pragma unroll
   for (int k = 0; k < ND; ++k)

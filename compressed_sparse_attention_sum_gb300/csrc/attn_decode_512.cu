@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(640, 1) attn_decode_512_kernel(
         if (m > -INFINITY) {
           const float fm = ex2(mine.x - m), total = fmaf(mine.y, fm, ex2(sink2 - m));
           f = __fdividef(fm, total) * even;
-          out = mine.y * fm == 0.f ? a.sink[h0 + h] : (m + log2f(total)) * kLn2;
+          out = sink2 > -INFINITY && mine.y * fm == 0.f ? a.sink[h0 + h] : (m + log2f(total)) * kLn2;
         }
         m_run[tid] = f;
         if (live && !*dead) a.lse[(row0 + qi) * a.H + h0 + h] = out;

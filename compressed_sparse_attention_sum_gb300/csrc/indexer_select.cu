@@ -178,10 +178,10 @@ __device__ __forceinline__ unsigned long long pair_key(float2 a) {
   return order_key((double)a.x + (double)a.y);
 }
 
-// The dot product of n channels of q, times qf (a power of two), and k: a product is split by an fma (exact
-// already for bf16 q), a sum by the exact error of an addition.  Eight channels
-// a step and no more unrolling: the code runs once a row, and fetching
-// instructions would take longer than the loop.
+// The dot product of n channels of q, times qf (a power of two), and k: a product
+// is split by an fma (exact already for bf16 q), a sum by the exact error of an
+// addition.  Eight channels a step and no more unrolling: the code runs once a
+// row, and fetching instructions would take longer than the loop.
 template <typename T>
 __device__ __forceinline__ float2 dot_pair(const T* q, float qf, const float* k, int n) {
   float hi = 0.f, lo = 0.f;

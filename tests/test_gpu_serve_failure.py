@@ -43,6 +43,8 @@ CASES = {
     "clusters and a second kernel": (1, 2, 32, 128, 1, 128, [4000], 0, 4, 64, BF, False),
     "512 channels, one CTA a query": (100, 1, 64, 512, 4, 128, [600] * 100, 130, 4, 64, BF, True),
     "512 channels, a cluster": (1, 1, 64, 512, 4, 128, [3000], 500, 8, 64, BF, True),
+    "one CTA a query, no sink": (100, 1, 16, 128, 4, 64, [500] * 100, 40, 4, 16, BF, False),
+    "512 channels, one CTA a query, no sink": (100, 1, 64, 512, 4, 128, [600] * 100, 130, 4, 64, BF, False),
     "512 channels, few heads": (2, 1, 8, 512, 4, 128, [3000, 5], 500, 4, 64, BF, True),
 }
 
