@@ -243,7 +243,7 @@ def run(st):
 
 
 def _run_own(st):
-    from compressed_sparse_attention_sum_gb300 import rows, serve
+    from compressed_sparse_attention_sum_gb300 import rows
     op = st["op"]
     kind = {"rms": rows.CSA_NORM_RMS, "layer": rows.CSA_NORM_LAYER}[st["kind"]] if "kind" in st else 0
     if op == "norm":
@@ -260,7 +260,7 @@ def _run_own(st):
     if op == "norm_rope_bwd":
         return rows.csa_norm_rope_bwd(st["x"], st["dout"], kind, st["plan"], st["pos"], st["weight"], EPS,
                                       has_bias=st["bias"] is not None, dx=st["out"], workspace=st["ws"])
-    out, first, counts = serve.csa_compress_decode(
+    out, first, counts = rows.csa_compress_decode(
         st["kv"], st["score"], st["kv_ring"], st["score_ring"], st["lens"], st["ratio"], st["coff"], kind, st["weight"], st["bias"], EPS,
         st["plan"], out=st["out"])
     return out, first, counts, st["kv_ring"], st["score_ring"]
