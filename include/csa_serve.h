@@ -11,14 +11,11 @@
  *                            sink; returns O and LSE
  *
  * A decode step of one layer: csa_cache_write of the new tokens' raw rows;
- * where a token completes a block of `ratio` tokens, csa_compress of the block
- * and csa_cache_write of its pooled row and of its index key;
- * csa_indexer_topk_decode; csa_attn_decode.  A layer of csa_compress_overlap
- * with coff 2 gives it the last two blocks and keeps the second entry.  A layer
- * of csa_compress_norm_rope cannot pool its blocks as they complete: that call
- * turns entry j of the rows it is given to position (j + 1) * ratio - 1 of those
- * rows, so a block pooled alone is turned as block 0; its rows go into the cache
- * from calls on the whole sequence.  Conventions (ownership, streams,
+ * csa_compress_decode (csa_rows.h) of the compressor's new rows, and
+ * csa_cache_write of what it returns, also for the index keys;
+ * csa_indexer_topk_decode; csa_attn_decode.  No call needs the lengths on the
+ * host, so a step can be captured into a graph once.  csa_norm_rope and csa_rope
+ * (csa_rows.h) make the queries and raw rows.  Conventions (ownership, streams,
  * errors, status codes, dtypes) are those of csa.h: the caller owns every
  * buffer, no call synchronizes or allocates, argument errors are found before
  * any CUDA call, and conditions met on the device are recorded in the status
