@@ -184,10 +184,10 @@ __global__ void __launch_bounds__(kThreads) compress_decode_kernel(CompressDecod
       const bool second = r.half ? at >= half : (at & 1) != 0;
       const int pair = r.half ? (second ? at - half : at) : at / 2;
       const int apart = r.half ? half : 1;
-      float cs, sn;
-      turn_cos_sin(r.turns[pair], hi - 1, &cs, &sn);
-      cs *= r.scale;
-      sn *= r.scale;
+      const long long turn[2] = {r.turns[pair], 0};
+      float2 c2, s2;
+      turn_cos_sin(turn, hi - 1, &c2, &s2);
+      const float cs = c2.x * r.scale, sn = s2.x * r.scale;
       v = second ? s_y[c - apart] * sn + v * cs : v * cs - s_y[c + apart] * sn;
     }
     out[c] = from_f<T>(v);
