@@ -165,27 +165,6 @@ __device__ __forceinline__ void copies_wait() {   // all but the newest N groups
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Rows [b, s, H] one after another, heads first.
-struct RowCursor {
-  int h, t, bi;
-  long long off;           // elements to the row
-  __device__ __forceinline__ void start(const RowStrides& st, int row, int s, int H) {
-    const int tok = row / H;
-    h = row - tok * H;
-    bi = tok / s;
-    t = tok - bi * s;
-    off = bi * st.b + t * st.t + h * st.h;
-  }
-  __device__ __forceinline__ void next(const RowStrides& st, int s, int H) {
-    off += st.h;
-    if (++h == H) {
-      h = 0;
-      if (++t == s) t = 0, ++bi;
-      off = bi * st.b + t * st.t;
-    }
-  }
-};
-
 // A row's channels as d / V vectors, two of them (a unit) at a time on one lane.
 //   no rotation, interleaved pairs: unit u has the vectors u and u + ceil(n / 2);
 //     a pair lies within a vector, as V and `first` are even
@@ -274,12 +253,13 @@ __device__ __forceinline__ void turn_unit(float2 (&v)[2][V / 2], const float (&c
     for (int i = 0; i < 2; ++i) {
       const uint32_t all = ((1u << V / 2) - 1) << i * V / 2;
       if ((turns & all) == 0) continue;
+      const bool some = (turns & all) != all;     // first and dim are any even numbers
 #pragma unroll
       for (int e = 0; e < V / 2; ++e) {
         const int p = i * V / 2 + e;
+        if (some && (turns >> p & 1u) == 0) continue;
         const float2 x = v[i][e];
-        const float2 y = make_float2(x.x * cs[p] - x.y * sn[p], x.x * sn[p] + x.y * cs[p]);
-        if ((turns & all) == all || (turns >> p & 1u)) v[i][e] = y;   // first, dim: any even numbers
+        v[i][e] = make_float2(x.x * cs[p] - x.y * sn[p], x.x * sn[p] + x.y * cs[p]);
       }
     }
   }

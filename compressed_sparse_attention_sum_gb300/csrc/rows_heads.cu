@@ -26,8 +26,32 @@ struct Depth {
   static constexpr int kBatch = sizeof(T) == 2 ? 2 : 1, kStages = 4;
 };
 
+// The rows as runs of up to `run` of the inner dimension, dealt out in turn: the heads of
+// a token, which share its position, or (few heads) the tokens of a head.
+struct Walk {
+  int run, per_outer, runs, rounds;   // runs of an outer index, of all, of the lanes of a row
+  bool tokens;                        // the inner dimension is the tokens
+
+  struct At {
+    int run, slot, len;               // run, row in it, its rows
+    int t, bi;                        // of the run's first row
+    char* p;                          // the present row
+  };
+  __device__ __forceinline__ void open(At& x, const RowsFwd& a, const RowStrides& st, const void* base,
+                                       int esz) const {
+    x.slot = x.len = 0;
+    if (x.run >= runs) return;
+    const int o = x.run / per_outer, i0 = (x.run - o * per_outer) * run;
+    const int n = tokens ? a.H : a.s, q = o / n, r = o - q * n;
+    x.bi = q;
+    x.t = tokens ? i0 : r;
+    x.len = min(run, (tokens ? a.s : a.H) - i0);
+    x.p = (char*)base + (q * st.b + x.t * st.t + (tokens ? r : i0) * st.h) * esz;
+  }
+};
+
 template <typename TI, typename TO, int ROPE, int V, int KIND>
-__global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int lanes, int per) {
+__global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int lanes, Walk walk) {
   constexpr int NU = 8 / V, kBatch = Depth<TI>::kBatch, kStages = Depth<TI>::kStages;
   constexpr bool NORM = KIND != kNormNone;
   using Vec = Pack<TI, V>;
@@ -37,12 +61,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
   unsigned char* s_pos = s_raw + sizeof(Vec) * kStages * kBatch * NU * 2 * kThreads;
   __shared__ int64_t s_turns[ROPE == kRopeNone ? 1 : kMaxHeadWidth / 2];
   const int lane = threadIdx.x & (lanes - 1);
-  const int rows = a.b * a.s * a.H;
-  const long long r0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / lanes * per;
-  const int n_rows = (int)max(0ll, min((long long)per, rows - r0));   // rows of these lanes
-  RowCursor in = {0, 0, 0, 0};
-  if (n_rows > 0) in.start(a.xs, (int)r0, a.s, a.H);
-  RowCursor to = {in.h, in.t, in.bi, in.bi * a.os.b + in.t * a.os.t + in.h * a.os.h};
+  const int step = (int)gridDim.x * (kThreads / lanes);
+  const long long x_step = (walk.tokens ? a.xs.t : a.xs.h) * (int)sizeof(TI);
+  const long long o_step = (walk.tokens ? a.os.t : a.os.h) * (int)sizeof(TO);
+  Walk::At in, to;
+  in.run = to.run = (int)((blockIdx.x * kThreads + threadIdx.x) / lanes);
+  walk.open(in, a, a.xs, a.x, sizeof(TI));
+  walk.open(to, a, a.os, a.out, sizeof(TO));
   int at[NU][2];
   uint32_t turns[NU];                                   // pairs of this lane that turn
 #pragma unroll
@@ -56,27 +81,30 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
     for (int e = 0; e < V; ++e)
       if (u.index(e, a.rope.first, a.rope.dim) >= 0) turns[k] |= 1u << e;
   }
-  int asked = 0;                                        // rows whose copies have begun
   const auto ask = [&](int stage) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (asked < n_rows) {
-        const TI* x = (const TI*)a.x + in.off;
+      if (in.slot + u < in.len) {
+        const TI* x = reinterpret_cast<const TI*>(in.p + u * x_step);
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (at[k][i] >= 0)
               Slot::ask(s_raw, ((stage * kBatch + u) * NU + k) * 2 + i, x + at[k][i]);
-        if (ROPE != kRopeNone && a.pos != nullptr && (in.h == 0 || asked == 0))
-          PosSlot::ask(s_pos, stage * kBatch + u, a.pos + in.bi * a.pos_stride + in.t);
-        in.next(a.xs, a.s, a.H);
+        if (ROPE != kRopeNone && a.pos != nullptr && (walk.tokens || in.slot + u == 0))
+          PosSlot::ask(s_pos, stage * kBatch + u, a.pos + in.bi * a.pos_stride + in.t + in.slot + u);
       }
-      ++asked;
     }
     copies_commit();
+    in.p += kBatch * x_step;
+    in.slot += kBatch;
+    if (in.slot >= walk.run) {
+      in.run += step;
+      walk.open(in, a, a.xs, a.x, sizeof(TI));
+    }
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages; ++i) ask(i);
   float2 w[NU][2][V / 2], c[NU][2][V / 2];              // weight; bias (layer norm)
   float cs[NU][V], sn[NU][V];
@@ -102,21 +130,22 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
     __syncthreads();
   }
   const float inv_n = 1.f / a.d;
-  int stage = 0;
-  for (int k0 = 0; k0 < per; k0 += kBatch) {
+  const auto use = [&](int stage) {
     copies_wait<kStages - 1>();
-    Vec raw[kBatch][NU][2];
+    float2 v[kBatch][NU][2][V / 2];
     int pos[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       pos[u] = 0;
+      // where nothing was asked for, whatever the place holds: it is neither counted nor stored
 #pragma unroll
       for (int k = 0; k < NU; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          raw[u][k][i].clear();
-          if (k0 + u < n_rows && at[k][i] >= 0)
-            Slot::take(s_raw, ((stage * kBatch + u) * NU + k) * 2 + i, raw[u][k][i]);
+          Vec raw;
+          Slot::take(s_raw, ((stage * kBatch + u) * NU + k) * 2 + i, raw);
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) v[u][k][i][e] = raw.two(e);
         }
       if (ROPE != kRopeNone && a.pos != nullptr) {
         Word p;
@@ -125,52 +154,82 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
       }
     }
     ask(stage);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-    float mean[kBatch], rstd[kBatch];
     if constexpr (NORM) {
+      float sum[kBatch];
       if constexpr (KIND == kNormLayer) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-          float2 q = make_float2(0.f, 0.f);
+          sum[u] = 0.f;
+#pragma unroll
+          for (int k = 0; k < NU; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float2 q = v[u][k][i][0];
+#pragma unroll
+              for (int e = 1; e < V / 2; ++e) q = add2(q, v[u][k][i][e]);
+              sum[u] += at[k][i] >= 0 ? q.x + q.y : 0.f;
+            }
+        }
+        group_sums(sum, lanes);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const float m = -sum[u] * inv_n;
 #pragma unroll
           for (int k = 0; k < NU; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < V / 2; ++e) q = add2(q, raw[u][k][i].two(e));
-          mean[u] = q.x + q.y;
+              for (int e = 0; e < V / 2; ++e) v[u][k][i][e] = add2(v[u][k][i][e], make_float2(m, m));
         }
-        group_sums(mean, lanes);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) mean[u] *= inv_n;
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        float2 q = make_float2(0.f, 0.f);
+        sum[u] = 0.f;
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            if (KIND == kNormLayer && at[k][i] < 0) continue;
+            float2 q = mul2(v[u][k][i][0], v[u][k][i][0]);
+#pragma unroll
+            for (int e = 1; e < V / 2; ++e) q = fma2(v[u][k][i][e], v[u][k][i][e], q);
+            sum[u] += at[k][i] >= 0 ? q.x + q.y : 0.f;
+          }
+      }
+      group_sums(sum, lanes);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float r = rsqrtf(fmaf(sum[u], inv_n, a.eps));
+#pragma unroll
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
-              float2 v = raw[u][k][i].two(e);
-              if (KIND == kNormLayer) v = add2(v, make_float2(-mean[u], -mean[u]));
-              q = fma2(v, v, q);
+              const float2 y = mul2(v[u][k][i][e], make_float2(r, r));
+              v[u][k][i][e] =
+                  KIND == kNormLayer ? fma2(y, w[k][i][e], c[k][i][e]) : mul2(y, w[k][i][e]);
             }
-          }
-        rstd[u] = q.x + q.y;
       }
-      group_sums(rstd, lanes);
+      if (KIND == kNormRms && a.bias != nullptr) {      // rare: not kept in registers
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) rstd[u] = rsqrtf(fmaf(rstd[u], inv_n, a.eps));
+        for (int k = 0; k < NU; ++k)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (at[k][i] < 0) continue;
+            Pack<float, V> pc;
+            pc.load(a.bias + at[k][i]);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+              for (int e = 0; e < V / 2; ++e) v[u][k][i][e] = add2(v[u][k][i][e], pc.two(e));
+          }
+      }
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (k0 + u >= n_rows) break;
       if constexpr (ROPE != kRopeNone) {
-        if (to.h == 0 || k0 + u == 0) {                 // a token's first row here
-          const int p = a.pos != nullptr ? pos[u] : to.t;
+        if (walk.tokens || to.slot + u == 0) {          // another token
+          const int p = a.pos != nullptr ? pos[u] : to.t + to.slot + u;
 #pragma unroll
           for (int k = 0; k < NU; ++k) {
             const Unit<ROPE, V> un(lane + k * lanes, a.d, a.rope.first, a.rope.dim);
@@ -178,46 +237,33 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
           }
         }
       }
-      TO* out = (TO*)a.out + to.off;
-      to.next(a.os, a.s, a.H);
+      TO* out = reinterpret_cast<TO*>(to.p + u * o_step);
+      const bool live = to.slot + u < to.len;
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
-        float2 v[2][V / 2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) {
-            float2 y = raw[u][k][i].two(e);
-            if constexpr (NORM) {
-              if (KIND == kNormLayer) y = add2(y, make_float2(-mean[u], -mean[u]));
-              y = mul2(y, make_float2(rstd[u], rstd[u]));
-              y = KIND == kNormLayer ? fma2(y, w[k][i][e], c[k][i][e]) : mul2(y, w[k][i][e]);
-            }
-            v[i][e] = y;
-          }
-        if constexpr (KIND == kNormRms) {
-          if (a.bias != nullptr) {                      // rare: not kept in registers
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (at[k][i] < 0) continue;
-              Pack<float, V> pc;
-              pc.load(a.bias + at[k][i]);
-#pragma unroll
-              for (int e = 0; e < V / 2; ++e) v[i][e] = add2(v[i][e], pc.two(e));
-            }
-          }
-        }
-        turn_unit<ROPE, V>(v, cs[k], sn[k], turns[k]);
+        turn_unit<ROPE, V>(v[u][k], cs[k], sn[k], turns[k]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (at[k][i] < 0) continue;
+          if (at[k][i] < 0 || !live) continue;
           Pack<TO, V> o;
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) o.set(e, v[i][e]);
+          for (int e = 0; e < V / 2; ++e) o.set(e, v[u][k][i][e]);
           o.store(out + at[k][i]);
         }
       }
     }
+    to.p += kBatch * o_step;
+    to.slot += kBatch;
+    if (to.slot >= walk.run) {
+      to.run += step;
+      walk.open(to, a, a.os, a.out, sizeof(TO));
+    }
+  };
+  int stage = 0;
+#pragma unroll 1
+  for (int left = walk.rounds * walk.run; left > 0; left -= kBatch) {
+    use(stage);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 }
 
@@ -231,10 +277,21 @@ cudaError_t fwd(const RowsFwd& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int lanes = row_lanes<V>(a.d), groups = kThreads / lanes;
   const long long rows = (long long)a.b * a.s * a.H;
-  // two CTAs an SM, of which each goes through a share of the rows
-  const long long ctas = std::min((rows + groups - 1) / groups, 2ll * 152);
-  const int per = (int)((rows + ctas * groups - 1) / (ctas * groups));
-  k<<<(unsigned)ctas, kThreads, smem, st>>>(a, lanes, per);
+  // Two CTAs an SM, whose lanes take runs of up to 16 rows in turn: all read and write near
+  // one another, and a run's rows have one stride and, of heads, one position.
+  Walk w;
+  w.tokens = ROPE != kRopeNone && a.H < 4;
+  const int inner = w.tokens ? a.s : a.H, most = 2 * 152 * groups;
+  const long long outer = rows / inner;
+  const long long share = std::min<long long>(16, (rows + most - 1) / most);
+  const long long pieces = (inner + share - 1) / share;
+  constexpr int kBatch = Depth<TI>::kBatch;
+  w.run = (int)(((inner + pieces - 1) / pieces + kBatch - 1) / kBatch * kBatch);
+  w.per_outer = (inner + w.run - 1) / w.run;
+  w.runs = (int)(outer * w.per_outer);
+  const int ctas = (int)std::min<long long>((w.runs + groups - 1) / groups, 2 * 152);
+  w.rounds = (w.runs + ctas * groups - 1) / (ctas * groups);
+  k<<<(unsigned)ctas, kThreads, smem, st>>>(a, lanes, w);
   count_launches(1);
   return cudaGetLastError();
 }
