@@ -122,19 +122,21 @@ struct Pack {
 
 // A vector's copy into the thread's own place in shared memory: rows in flight take
 // no registers, and nobody else has to be waited for.  Its pieces of up to 16 bytes
-// are kThreads apart, so that neighbouring threads have neighbouring pieces.
+// are a CTA's threads apart, so that neighbouring threads have neighbouring pieces.
+// THREADS: of the CTA, 0: blockDim.x.
 template <typename VEC, int THREADS>
 struct VecSlot {
   static constexpr int kPiece = sizeof(VEC) < 16 ? (int)sizeof(VEC) : 16, kPieces = sizeof(VEC) / kPiece;
 
-  // slot i of this thread
-  static __device__ __forceinline__ unsigned char* place(unsigned char* base, int i) {
-    return base + ((size_t)i * kPieces * THREADS + threadIdx.x) * kPiece;
+  static __device__ __forceinline__ uint32_t threads() { return THREADS > 0 ? THREADS : blockDim.x; }
+  // piece k of slot i of this thread
+  static __device__ __forceinline__ unsigned char* place(unsigned char* base, int i, int k) {
+    return base + ((uint32_t)(i * kPieces + k) * threads() + threadIdx.x) * kPiece;
   }
   static __device__ __forceinline__ void ask(unsigned char* base, int i, const void* from) {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      const uint32_t to = (uint32_t)__cvta_generic_to_shared(place(base, i) + k * THREADS * kPiece);
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(place(base, i, k));
       const char* p = (const char*)from + k * kPiece;
       if constexpr (kPiece == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
@@ -145,7 +147,7 @@ struct VecSlot {
   static __device__ __forceinline__ void take(unsigned char* base, int i, VEC& v) {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {
-      const unsigned char* p = place(base, i) + k * THREADS * kPiece;
+      const unsigned char* p = place(base, i, k);
       if constexpr (kPiece == 16) {
         const uint4 x = *reinterpret_cast<const uint4*>(p);
         v.w[4 * k] = x.x; v.w[4 * k + 1] = x.y; v.w[4 * k + 2] = x.z; v.w[4 * k + 3] = x.w;

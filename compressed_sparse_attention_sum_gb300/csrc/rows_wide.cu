@@ -1,8 +1,11 @@
 // Layer and RMS norm of rows of up to 32768 channels, one CTA a row, and their
 // gradient (the formulas stand in rows_heads.cu); the sums of the CTAs' shares of
 // the weight's and the bias's gradient.
+#include <algorithm>
+
 #include "csa_kernels.h"
 #include "rows.cuh"
+#include "smem_once.h"
 
 namespace csa {
 namespace {
@@ -17,51 +20,158 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? s[lane] : 0.f);
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(1024) norm_wide_kernel(RowsFwd a) {
-  __shared__ float s_a[32], s_b[32];
-  const int n = a.d, nv = n / 8;
-  const T* x = (const T*)a.x + (long long)blockIdx.x * a.xs.h;
-  T* out = (T*)a.out + (long long)blockIdx.x * a.os.h;
-  float v[NV][8];
-  float m = 0.f, q = 0.f;
+// Forward.  A thread has NV vectors of 16 bytes of every row of its CTA, the next rows on
+// their way in its own places of shared memory, weight and bias in registers (beyond 32
+// channels a thread they are read again for each row).  BATCH rows share a barrier: a warp's
+// mean and its squares about that mean go to shared memory, and every thread joins the warps'
+// (squares about means, with the count of each: no cancellation at any mean).
+template <typename T, int NV, int KIND, int BATCH, int STAGES, int THREADS, int PER_SM>
+__global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
+  constexpr int V = 16 / sizeof(T);
+  using Vec = Pack<T, V>;
+  using Slot = VecSlot<Vec, 0>;                         // [stage][row][NV]
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  constexpr bool kKeep = NV * V <= 32;
+  __shared__ __align__(16) float2 s_part[2][BATCH][THREADS / 32];
+  __shared__ float s_count[THREADS / 32];               // elements of each warp
+  const int nv = a.d / V, threads = blockDim.x, warps = threads / 32;
+  const int v0 = threadIdx.x;                           // this thread's first vector
+  const int rows = a.H, row_step = gridDim.x;
+  const auto has = [&](int k) { return v0 + k * threads < nv; };
+  long long asked = blockIdx.x;                         // the next row to ask for
+  const auto ask = [&](int stage) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * blockDim.x;
-    if (i >= nv) continue;
-    load8(x + i * 8, v[k]);
+    for (int u = 0; u < BATCH; ++u) {
+      const T* x = (const T*)a.x + asked * a.xs.h;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m += v[k][e];
-  }
-  m = a.kind == kNormLayer ? block_sum(m, s_a) / n : 0.f;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * blockDim.x;
-    if (i >= nv) continue;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(v[k][e] - m, v[k][e] - m, q);
-  }
-  const float rstd = 1.f / sqrtf(block_sum(q, s_b) / n + a.eps);
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * blockDim.x;
-    if (i >= nv) continue;
-    float w[8], b[8];
-    if (a.weight != nullptr) load8(a.weight + i * 8, w);
-    if (a.bias != nullptr) load8(a.bias + i * 8, b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float y = (v[k][e] - m) * rstd;
-      if (a.weight != nullptr) y *= w[e];
-      if (a.bias != nullptr) y += b[e];
-      v[k][e] = y;
+      for (int k = 0; k < NV; ++k)
+        if (asked < rows && has(k))
+          Slot::ask(s_raw, (stage * BATCH + u) * NV + k, x + (v0 + k * threads) * V);
+      asked += row_step;
     }
-    store8(out + i * 8, v[k]);
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES; ++i) ask(i);
+  const auto affine = [&](int k, Pack<float, V>& w, Pack<float, V>& c) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) w.w[e] = __float_as_uint(1.f), c.w[e] = 0;
+    if (has(k) && a.weight != nullptr) w.load(a.weight + (v0 + k * threads) * V);
+    if (has(k) && a.bias != nullptr) c.load(a.bias + (v0 + k * threads) * V);
+  };
+  Pack<float, V> w[kKeep ? NV : 1], c[kKeep ? NV : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) affine(k, w[k], c[k]);
+  }
+  if (threadIdx.x < warps) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) n += min(32, max(0, nv - k * threads - (int)threadIdx.x * 32));
+    s_count[threadIdx.x] = (float)(n * V);
+  }
+  __syncthreads();
+  const float inv_n = 1.f / a.d, mine = s_count[threadIdx.x / 32];
+  const float inv_mine = mine > 0.f ? 1.f / mine : 0.f;
+  int stage = 0, turn = 0;
+#pragma unroll 1
+  for (long long row = blockIdx.x; row < rows; row += (long long)BATCH * row_step) {
+    copies_wait<STAGES - 1>();
+    Vec raw[BATCH][NV];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        Slot::take(s_raw, (stage * BATCH + u) * NV + k, raw[u][k]);
+        if (!has(k)) raw[u][k].clear();
+      }
+    ask(stage);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    float m[BATCH], q[BATCH];
+    if constexpr (KIND == kNormLayer) {
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int e = 0; e < V / 2; ++e) t = add2(t, raw[u][k].two(e));
+        m[u] = t.x + t.y;
+      }
+      group_sums(m, 32);
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) m[u] *= inv_mine;
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (KIND == kNormLayer && !has(k)) continue;
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          float2 y = raw[u][k].two(e);
+          if (KIND == kNormLayer) y = add2(y, make_float2(-m[u], -m[u]));
+          t = fma2(y, y, t);
+        }
+      }
+      q[u] = t.x + t.y;
+    }
+    group_sums(q, 32);
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u)
+        s_part[turn][u][threadIdx.x >> 5] = make_float2(KIND == kNormLayer ? m[u] : 0.f, q[u]);
+    }
+    __syncthreads();
+    float mean[BATCH], sq[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) mean[u] = sq[u] = 0.f;
+    if constexpr (KIND == kNormLayer) {
+#pragma unroll 4
+      for (int i = 0; i < warps; ++i)
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) mean[u] = fmaf(s_part[turn][u][i].x, s_count[i], mean[u]);
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) mean[u] *= inv_n;
+    }
+#pragma unroll 4
+    for (int i = 0; i < warps; ++i)
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        const float2 p = s_part[turn][u][i];
+        sq[u] += p.y;
+        if (KIND == kNormLayer) sq[u] = fmaf((p.x - mean[u]) * (p.x - mean[u]), s_count[i], sq[u]);
+      }
+    turn ^= 1;
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const float r = rsqrtf(fmaf(sq[u], inv_n, a.eps));
+      const long long at = row + (long long)u * row_step;
+      T* out = (T*)a.out + at * a.os.h;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        Vec o;
+        Pack<float, V> pw, pc;
+        if constexpr (kKeep)
+          pw = w[k], pc = c[k];
+        else
+          affine(k, pw, pc);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          float2 y = raw[u][k].two(e);
+          if (KIND == kNormLayer) y = add2(y, make_float2(-mean[u], -mean[u]));
+          y = mul2(y, make_float2(r, r));
+          o.set(e, fma2(y, pw.two(e), pc.two(e)));
+        }
+        if (has(k) && at < rows) o.store(out + (v0 + k * threads) * V);
+      }
+    }
   }
 }
 
 template <typename TX, typename TG, typename TD, int NV>
-__global__ void __launch_bounds__(1024) norm_wide_bwd_kernel(RowsBwd a) {
+__global__ void __launch_bounds__(1024, 1) norm_wide_bwd_kernel(RowsBwd a) {
   __shared__ float s_a[32], s_b[32], s_c[32], s_d[32];
   const int n = a.d, nv = n / 8;
   float dw[NV][8], db[NV][8];
@@ -189,18 +299,38 @@ cudaError_t wide_bwd_types(const RowsBwd& a, int ctas, cudaStream_t st) {
   return a.dx_bf16 ? wide_bwd<TX, float, bf>(a, ctas, st) : wide_bwd<TX, float, float>(a, ctas, st);
 }
 
-template <typename T>
+// C channels a thread, BATCH rows together, STAGES batches under way, at most THREADS threads
+// a CTA and PER_SM of these an SM.
+template <typename T, int C, int KIND, int BATCH, int STAGES, int THREADS, int PER_SM>
 cudaError_t wide_fwd(const RowsFwd& a, cudaStream_t st) {
-  const int nv = wide_vectors(a.d);
-  const int threads = wide_threads(a.d, nv);
-  if (nv == 1)
-    norm_wide_kernel<T, 1><<<(unsigned)a.H, threads, 0, st>>>(a);
-  else if (nv == 2)
-    norm_wide_kernel<T, 2><<<(unsigned)a.H, threads, 0, st>>>(a);
-  else
-    norm_wide_kernel<T, 4><<<(unsigned)a.H, threads, 0, st>>>(a);
+  constexpr size_t a_thread = (size_t)STAGES * BATCH * C * sizeof(T);
+  static SmemOnce once;
+  const auto k = norm_wide_kernel<T, C * (int)sizeof(T) / 16, KIND, BATCH, STAGES, THREADS, PER_SM>;
+  const cudaError_t e = once(k, a_thread * THREADS);
+  if (e != cudaSuccess) return e;
+  const int threads = (a.d + C * 32 - 1) / (C * 32) * 32;
+  const int ctas = std::min(a.H, THREADS * PER_SM / threads * 152);
+  k<<<(unsigned)ctas, threads, a_thread * threads, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
+}
+
+// Channels a thread by the width, measured for 64M bf16 channels (floor 39.6 us): more of them
+// mean fewer warps to join, fewer mean more CTAs that do not wait for one another's barriers.
+// 1024: 48.6 us (16 channels 48.8, one warp a row 57); 2048: 44.6 (8: 51, 32: 48);
+// 4096: 42.8 (16: 47, 8: 88); 8192: 42.8 (32: 44 to 50); 16384: 52.7 (16 with 1024 threads
+// 88, two CTAs of a cluster a row 114).
+template <typename T, int KIND>
+cudaError_t wide_fwd_width(const RowsFwd& a, cudaStream_t st) {
+  constexpr bool half = sizeof(T) == 2;
+  // rows for one CTA an SM, or two: nothing to overlap with, so as many threads as there are
+  if (a.H <= 2 * 152 && a.d <= 4096) return wide_fwd<T, 8, KIND, 1, 1, 512, 1>(a, st);
+  if (a.d <= 1024) return wide_fwd<T, 8, KIND, 2, 3, 128, 6>(a, st);
+  if (a.d <= 2048) return wide_fwd<T, 16, KIND, 2, 3, 128, 4>(a, st);
+  if (a.d <= 4096) return wide_fwd<T, 32, KIND, 2, 2, 128, 3>(a, st);
+  if (a.d <= 8192) return wide_fwd<T, 16, KIND, 2, half ? 3 : 2, 512, 1>(a, st);
+  if (a.d <= 16384) return wide_fwd<T, 32, KIND, 1, 3, 512, 1>(a, st);
+  return wide_fwd<T, 64, KIND, 1, half ? 2 : 1, 512, 1>(a, st);
 }
 
 }  // namespace
@@ -213,7 +343,10 @@ int rows_bwd_ctas(long long rows, int n) {
 }
 
 cudaError_t launch_norm_wide(const RowsFwd& a, cudaStream_t st) {
-  return a.x_bf16 ? wide_fwd<__nv_bfloat16>(a, st) : wide_fwd<float>(a, st);
+  using bf = __nv_bfloat16;
+  if (a.kind == kNormRms)
+    return a.x_bf16 ? wide_fwd_width<bf, kNormRms>(a, st) : wide_fwd_width<float, kNormRms>(a, st);
+  return a.x_bf16 ? wide_fwd_width<bf, kNormLayer>(a, st) : wide_fwd_width<float, kNormLayer>(a, st);
 }
 
 cudaError_t launch_norm_wide_bwd(const RowsBwd& a, int ctas, cudaStream_t st) {
