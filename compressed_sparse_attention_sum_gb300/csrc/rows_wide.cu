@@ -1,6 +1,6 @@
-// Layer and RMS norm of rows of up to 32768 channels, one CTA a row, and their
-// gradient (the formulas stand in rows_heads.cu); the sums of the CTAs' shares of
-// the weight's and the bias's gradient.
+// Layer and RMS norm of rows of up to 32768 channels, one CTA a row (the formulas stand
+// in rows_heads.cu), and the sums of the CTAs' shares of the weight's and the bias's
+// gradient.
 #include <algorithm>
 
 #include "csa_kernels.h"
@@ -9,16 +9,6 @@
 
 namespace csa {
 namespace {
-
-// Sum over the CTA; every thread gets it.  `s` has room for 32 floats, and a
-// barrier lies between two uses.
-__device__ __forceinline__ float block_sum(float v, float* s) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  return warp_sum(lane < (int)(blockDim.x >> 5) ? s[lane] : 0.f);
-}
 
 // Forward.  A thread has NV vectors of 16 bytes of every row of its CTA, the next rows on
 // their way in its own places of shared memory, weight and bias in registers (beyond 32
@@ -124,25 +114,26 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
         s_part[turn][u][threadIdx.x >> 5] = make_float2(KIND == kNormLayer ? m[u] : 0.f, q[u]);
     }
     __syncthreads();
+    // lane i has warp i's share; the row's sums are those over the lanes
     float mean[BATCH], sq[BATCH];
+    const int lane = threadIdx.x & 31;
+    const float cnt = lane < warps ? s_count[lane] : 0.f;
+    float2 p[BATCH];
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) mean[u] = sq[u] = 0.f;
-    if constexpr (KIND == kNormLayer) {
-#pragma unroll 4
-      for (int i = 0; i < warps; ++i)
-#pragma unroll
-        for (int u = 0; u < BATCH; ++u) mean[u] = fmaf(s_part[turn][u][i].x, s_count[i], mean[u]);
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) mean[u] *= inv_n;
+    for (int u = 0; u < BATCH; ++u) {
+      p[u] = lane < warps ? s_part[turn][u][lane] : make_float2(0.f, 0.f);
+      mean[u] = p[u].x * cnt;
+      sq[u] = p[u].y;
     }
-#pragma unroll 4
-    for (int i = 0; i < warps; ++i)
+    if constexpr (KIND == kNormLayer) {
+      group_sums(mean, 32);
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
-        const float2 p = s_part[turn][u][i];
-        sq[u] += p.y;
-        if (KIND == kNormLayer) sq[u] = fmaf((p.x - mean[u]) * (p.x - mean[u]), s_count[i], sq[u]);
+        mean[u] *= inv_n;
+        sq[u] = fmaf((p[u].x - mean[u]) * (p[u].x - mean[u]), cnt, sq[u]);
       }
+    }
+    group_sums(sq, 32);
     turn ^= 1;
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
@@ -170,133 +161,33 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
   }
 }
 
-template <typename TX, typename TG, typename TD, int NV>
-__global__ void __launch_bounds__(1024, 1) norm_wide_bwd_kernel(RowsBwd a) {
-  __shared__ float s_a[32], s_b[32], s_c[32], s_d[32];
-  const int n = a.d, nv = n / 8;
-  float dw[NV][8], db[NV][8];
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[k][e] = db[k][e] = 0.f;
-  for (int row = blockIdx.x; row < a.H; row += gridDim.x) {
-    const TX* x = (const TX*)a.x + row * a.xs.h;
-    const TG* g = (const TG*)a.dout + row * a.gs.h;
-    TD* dx = (TD*)a.dx + row * a.ds.h;
-    float v[NV][8], gy[NV][8];
-    float m = 0.f, q = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
-      if (i >= nv) continue;
-      load8(x + i * 8, v[k]);
-      load8(g + i * 8, gy[k]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m += v[k][e];
-    }
-    m = a.kind == kNormLayer ? block_sum(m, s_a) / n : 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
-      if (i >= nv) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q = fmaf(v[k][e] - m, v[k][e] - m, q);
-    }
-    const float rstd = 1.f / sqrtf(block_sum(q, s_b) / n + a.eps);
-    float sg = 0.f, sgx = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
-      if (i >= nv) continue;
-      float w[8];
-      if (a.weight != nullptr) load8(a.weight + i * 8, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = (v[k][e] - m) * rstd;
-        dw[k][e] = fmaf(gy[k][e], xh, dw[k][e]);
-        db[k][e] += gy[k][e];
-        v[k][e] = xh;
-        if (a.weight != nullptr) gy[k][e] *= w[e];
-        sg += gy[k][e];
-        sgx = fmaf(gy[k][e], xh, sgx);
-      }
-    }
-    sgx = block_sum(sgx, s_c) / n;
-    sg = block_sum(sg, s_d) / n;
-    if (a.kind != kNormLayer) sg = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x + k * blockDim.x;
-      if (i >= nv) continue;
-      float o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = rstd * (gy[k][e] - sg - v[k][e] * sgx);
-      store8(dx + i * 8, o);
-    }
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int wanted = (a.dweight != nullptr) + (a.dbias != nullptr);
-  float* to = a.parts + (size_t)blockIdx.x * wanted * n;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x + k * blockDim.x;
-    if (i >= nv) continue;
-    if (a.dweight != nullptr) store8(to + i * 8, dw[k]);
-    if (a.dbias != nullptr) store8(to + (size_t)(wanted - 1) * n + i * 8, db[k]);
-  }
-}
-
 // A programmatic dependent of the kernel that wrote the parts: 32 columns a CTA,
 // the parts dealt to its warps and joined in a fixed order.
-constexpr int kSumWarps = 8;
+constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(32 * kSumWarps) sum_parts_kernel(
     const float* __restrict__ parts, int ctas, float* __restrict__ dweight,
     float* __restrict__ dbias, int n) {
-  __shared__ float s[kSumWarps][32];
+  __shared__ float s[kSumWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cols = n * ((dweight != nullptr) + (dbias != nullptr)), c = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float x = 0.f;
-  if (c < cols)
+  if (c < cols) {
+#pragma unroll 8
     for (int p = warp; p < ctas; p += kSumWarps) x += parts[(size_t)p * cols + c];
+  }
   s[warp][lane] = x;
   __syncthreads();
-  if (warp != 0 || c >= cols) return;
-  x = 0.f;
-#pragma unroll
-  for (int w = 0; w < kSumWarps; ++w) x += s[w][lane];
+  // warp w sums column w
+  x = warp_sum(s[lane][warp]);
+  const int col = blockIdx.x * 32 + warp;
+  if (lane != 0 || col >= cols) return;
   if (dweight == nullptr)
-    dbias[c] = x;
-  else if (c < n)
-    dweight[c] = x;
+    dbias[col] = x;
+  else if (col < n)
+    dweight[col] = x;
   else
-    dbias[c - n] = x;
-}
-
-// Threads of a row of n channels (a multiple of 32, at most 1024) and its vectors of
-// 8 on each.
-int wide_threads(int n, int nv) { return ((n / 8 + nv - 1) / nv + 31) / 32 * 32; }
-int wide_vectors(int n) { return n <= 8192 ? 1 : n <= 16384 ? 2 : 4; }
-
-template <typename TX, typename TG, typename TD>
-cudaError_t wide_bwd(const RowsBwd& a, int ctas, cudaStream_t st) {
-  const int nv = wide_vectors(a.d);
-  const int threads = wide_threads(a.d, nv);
-  if (nv == 1)
-    norm_wide_bwd_kernel<TX, TG, TD, 1><<<ctas, threads, 0, st>>>(a);
-  else if (nv == 2)
-    norm_wide_bwd_kernel<TX, TG, TD, 2><<<ctas, threads, 0, st>>>(a);
-  else
-    norm_wide_bwd_kernel<TX, TG, TD, 4><<<ctas, threads, 0, st>>>(a);
-  count_launches(1);
-  return cudaGetLastError();
-}
-
-template <typename TX>
-cudaError_t wide_bwd_types(const RowsBwd& a, int ctas, cudaStream_t st) {
-  using bf = __nv_bfloat16;
-  if (a.g_bf16) return a.dx_bf16 ? wide_bwd<TX, bf, bf>(a, ctas, st) : wide_bwd<TX, bf, float>(a, ctas, st);
-  return a.dx_bf16 ? wide_bwd<TX, float, bf>(a, ctas, st) : wide_bwd<TX, float, float>(a, ctas, st);
+    dbias[col - n] = x;
 }
 
 // C channels a thread, BATCH rows together, STAGES batches under way, at most THREADS threads
@@ -335,22 +226,11 @@ cudaError_t wide_fwd_width(const RowsFwd& a, cudaStream_t st) {
 
 }  // namespace
 
-int rows_bwd_ctas(long long rows, int n) {
-  const long long most = n <= kMaxHeadWidth ? 152 * 4 : 152 * 2;
-  // rows of a CTA of the narrow kernel at once: at least 8 (32 lanes a row)
-  const long long need = n <= kMaxHeadWidth ? (rows + 7) / 8 : rows;
-  return (int)(need < most ? (need > 0 ? need : 1) : most);
-}
-
 cudaError_t launch_norm_wide(const RowsFwd& a, cudaStream_t st) {
   using bf = __nv_bfloat16;
   if (a.kind == kNormRms)
     return a.x_bf16 ? wide_fwd_width<bf, kNormRms>(a, st) : wide_fwd_width<float, kNormRms>(a, st);
   return a.x_bf16 ? wide_fwd_width<bf, kNormLayer>(a, st) : wide_fwd_width<float, kNormLayer>(a, st);
-}
-
-cudaError_t launch_norm_wide_bwd(const RowsBwd& a, int ctas, cudaStream_t st) {
-  return a.x_bf16 ? wide_bwd_types<__nv_bfloat16>(a, ctas, st) : wide_bwd_types<float>(a, ctas, st);
 }
 
 cudaError_t launch_sum_parts(const float* parts, int ctas, float* dweight, float* dbias, int n,
