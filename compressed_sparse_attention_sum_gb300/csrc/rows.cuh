@@ -2,6 +2,8 @@
 // how a row's channels lie on lanes so that both members of a pair do on one.
 #pragma once
 
+#include <algorithm>
+
 #include "csa_common.cuh"
 #include "rows.h"
 
@@ -265,6 +267,47 @@ __device__ __forceinline__ void turn_unit(float2 (&v)[2][V / 2], const float (&c
       }
     }
   }
+}
+
+// The rows as runs of up to `run` of the inner dimension, dealt out in turn: the heads of
+// a token, which share its position, or (few heads) the tokens of a head.
+struct Walk {
+  int run, per_outer, runs, rounds;   // runs of an outer index, of all, of the lanes of a row
+  bool tokens;                        // the inner dimension is the tokens
+
+  struct At {
+    int run, slot, len;               // run, row in it, its rows
+    int t, bi;                        // of the run's first row
+    char* p;                          // the present row
+  };
+  __device__ __forceinline__ void open(At& x, int s, int H, const RowStrides& st, const void* base,
+                                       int esz) const {
+    x.slot = x.len = 0;
+    if (x.run >= runs) return;
+    const int o = x.run / per_outer, i0 = (x.run - o * per_outer) * run;
+    const int n = tokens ? H : s, q = o / n, r = o - q * n;
+    x.bi = q;
+    x.t = tokens ? i0 : r;
+    x.len = min(run, (tokens ? s : H) - i0);
+    x.p = (char*)base + (q * st.b + x.t * st.t + (tokens ? r : i0) * st.h) * esz;
+  }
+};
+
+// The walk of `ctas` CTAs (on return no more than have a run), each with `groups` rows at a
+// time and `batch` of a run together.  Runs of up to 16 rows: all read and write near one
+// another, and a run's rows have one stride and, of heads, one position.
+inline Walk make_walk(int b, int s, int H, bool turned, int groups, int batch, int* ctas) {
+  Walk w;
+  w.tokens = turned && H < 4;
+  const long long rows = (long long)b * s * H, inner = w.tokens ? s : H, most = (long long)*ctas * groups;
+  const long long share = std::min<long long>(16, (rows + most - 1) / most);
+  const long long pieces = (inner + share - 1) / share;
+  w.run = (int)(((inner + pieces - 1) / pieces + batch - 1) / batch * batch);
+  w.per_outer = (int)((inner + w.run - 1) / w.run);
+  w.runs = (int)(rows / inner * w.per_outer);
+  *ctas = (int)std::min<long long>((w.runs + groups - 1) / groups, *ctas);
+  w.rounds = (w.runs + *ctas * groups - 1) / (*ctas * groups);
+  return w;
 }
 
 // Lanes of a row of d channels: a power of two, with 16 channels on each.

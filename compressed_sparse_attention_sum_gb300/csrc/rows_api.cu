@@ -49,7 +49,7 @@ RopeArgs rope_args(const csa_rope_t* r, bool back) {
   return a;
 }
 
-constexpr long long kMaxRowCount = 0x7fffffffll;
+constexpr long long kMaxRowCount = 1ll << 30;   // row and run indexes, with a step more, fit 32 bits
 
 // Rows [b, s, H] at these strides start on 16-byte boundaries.
 bool valid_in(const void* p, csa_row_strides_t st, csa_dtype_t dt, int b, int s, int H) {

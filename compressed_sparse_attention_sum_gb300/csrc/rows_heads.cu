@@ -26,30 +26,6 @@ struct Depth {
   static constexpr int kBatch = sizeof(T) == 2 ? 2 : 1, kStages = 4;
 };
 
-// The rows as runs of up to `run` of the inner dimension, dealt out in turn: the heads of
-// a token, which share its position, or (few heads) the tokens of a head.
-struct Walk {
-  int run, per_outer, runs, rounds;   // runs of an outer index, of all, of the lanes of a row
-  bool tokens;                        // the inner dimension is the tokens
-
-  struct At {
-    int run, slot, len;               // run, row in it, its rows
-    int t, bi;                        // of the run's first row
-    char* p;                          // the present row
-  };
-  __device__ __forceinline__ void open(At& x, const RowsFwd& a, const RowStrides& st, const void* base,
-                                       int esz) const {
-    x.slot = x.len = 0;
-    if (x.run >= runs) return;
-    const int o = x.run / per_outer, i0 = (x.run - o * per_outer) * run;
-    const int n = tokens ? a.H : a.s, q = o / n, r = o - q * n;
-    x.bi = q;
-    x.t = tokens ? i0 : r;
-    x.len = min(run, (tokens ? a.s : a.H) - i0);
-    x.p = (char*)base + (q * st.b + x.t * st.t + (tokens ? r : i0) * st.h) * esz;
-  }
-};
-
 template <typename TI, typename TO, int ROPE, int V, int KIND>
 __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int lanes, Walk walk) {
   constexpr int NU = 8 / V, kBatch = Depth<TI>::kBatch, kStages = Depth<TI>::kStages;
@@ -66,8 +42,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
   const long long o_step = (walk.tokens ? a.os.t : a.os.h) * (int)sizeof(TO);
   Walk::At in, to;
   in.run = to.run = (int)((blockIdx.x * kThreads + threadIdx.x) / lanes);
-  walk.open(in, a, a.xs, a.x, sizeof(TI));
-  walk.open(to, a, a.os, a.out, sizeof(TO));
+  walk.open(in, a.s, a.H, a.xs, a.x, sizeof(TI));
+  walk.open(to, a.s, a.H, a.os, a.out, sizeof(TO));
   int at[NU][2];
   uint32_t turns[NU];                                   // pairs of this lane that turn
 #pragma unroll
@@ -101,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
     in.slot += kBatch;
     if (in.slot >= walk.run) {
       in.run += step;
-      walk.open(in, a, a.xs, a.x, sizeof(TI));
+      walk.open(in, a.s, a.H, a.xs, a.x, sizeof(TI));
     }
   };
 #pragma unroll 1
@@ -256,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
     to.slot += kBatch;
     if (to.slot >= walk.run) {
       to.run += step;
-      walk.open(to, a, a.os, a.out, sizeof(TO));
+      walk.open(to, a.s, a.H, a.os, a.out, sizeof(TO));
     }
   };
   int stage = 0;
@@ -276,21 +252,8 @@ cudaError_t fwd(const RowsFwd& a, cudaStream_t st) {
   const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
   const int lanes = row_lanes<V>(a.d), groups = kThreads / lanes;
-  const long long rows = (long long)a.b * a.s * a.H;
-  // Two CTAs an SM, whose lanes take runs of up to 16 rows in turn: all read and write near
-  // one another, and a run's rows have one stride and, of heads, one position.
-  Walk w;
-  w.tokens = ROPE != kRopeNone && a.H < 4;
-  const int inner = w.tokens ? a.s : a.H, most = 2 * 152 * groups;
-  const long long outer = rows / inner;
-  const long long share = std::min<long long>(16, (rows + most - 1) / most);
-  const long long pieces = (inner + share - 1) / share;
-  constexpr int kBatch = Depth<TI>::kBatch;
-  w.run = (int)(((inner + pieces - 1) / pieces + kBatch - 1) / kBatch * kBatch);
-  w.per_outer = (inner + w.run - 1) / w.run;
-  w.runs = (int)(outer * w.per_outer);
-  const int ctas = (int)std::min<long long>((w.runs + groups - 1) / groups, 2 * 152);
-  w.rounds = (w.runs + ctas * groups - 1) / (ctas * groups);
+  int ctas = 2 * 152;
+  const Walk w = make_walk(a.b, a.s, a.H, ROPE != kRopeNone, groups, Depth<TI>::kBatch, &ctas);
   k<<<(unsigned)ctas, kThreads, smem, st>>>(a, lanes, w);
   count_launches(1);
   return cudaGetLastError();

@@ -292,9 +292,11 @@ cudaError_t bwd_kind(const RowsBwd& a, int ctas, cudaStream_t st) {
 }  // namespace
 
 int rows_bwd_ctas(long long rows, int n) {
-  if (n <= kMaxHeadWidth) {
-    // rows of a CTA of the narrow kernel at once: at least 8 (32 lanes a row)
-    return (int)std::max(1ll, std::min<long long>((rows + 7) / 8, 152 * 4));
+  if (n <= kMaxHeadWidth) {                             // 256 threads, 16 channels on each
+    int lanes = 1;
+    while (lanes * 16 < n) lanes *= 2;
+    const long long at_once = 256 / lanes;
+    return (int)std::max(1ll, std::min<long long>((rows + at_once - 1) / at_once, 2 * 152));
   }
   // with four rows a CTA or more its sums are a small part of what it moves
   const WideShape w = wide_shape(n);

@@ -56,7 +56,7 @@ typedef enum { CSA_NORM_RMS = 1, CSA_NORM_LAYER = 2 } csa_norm_kind_t;
  *   out     out  [rows, n] of dt, row stride out_stride
  * Errors: INVALID_ARG for null or misaligned pointers, n % 8 != 0, n < 8,
  * strides (above), an unknown kind or dtype, a bad eps; UNSUPPORTED for n >
- * 32768 or rows >= 2^31.
+ * 32768 or rows > 2^30.
  */
 csa_status_t csa_norm(const void* x, long long x_stride, csa_dtype_t dt, int kind,
                       const float* weight, const float* bias, float eps, void* out,
@@ -153,7 +153,7 @@ typedef struct {
  *             sequences), or NULL
  * Errors: INVALID_ARG for null or misaligned pointers, d % 8 != 0, d < 8,
  * strides (above), a rotation outside its limits or the row, an unknown dtype;
- * UNSUPPORTED for d > 512 or b * s * H >= 2^31.
+ * UNSUPPORTED for d > 512 or b * s * H > 2^30.
  */
 csa_status_t csa_rope(const void* x, const csa_row_strides_t* x_strides, csa_dtype_t dt,
                       const int32_t* pos, long long pos_stride, const csa_rope_t* rope,
