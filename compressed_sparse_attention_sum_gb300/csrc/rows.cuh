@@ -257,13 +257,21 @@ __device__ __forceinline__ void turn_unit(float2 (&v)[2][V / 2], const float (&c
     for (int i = 0; i < 2; ++i) {
       const uint32_t all = ((1u << V / 2) - 1) << i * V / 2;
       if ((turns & all) == 0) continue;
-      const bool some = (turns & all) != all;     // first and dim are any even numbers
+      if ((turns & all) == all) {
 #pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        const int p = i * V / 2 + e;
-        if (some && (turns >> p & 1u) == 0) continue;
-        const float2 x = v[i][e];
-        v[i][e] = make_float2(x.x * cs[p] - x.y * sn[p], x.x * sn[p] + x.y * cs[p]);
+        for (int e = 0; e < V / 2; ++e) {
+          const int p = i * V / 2 + e;
+          const float2 x = v[i][e];
+          v[i][e] = make_float2(x.x * cs[p] - x.y * sn[p], x.x * sn[p] + x.y * cs[p]);
+        }
+      } else {                                    // first and dim are any even numbers
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+          const int p = i * V / 2 + e;
+          const float2 x = v[i][e];
+          if (turns >> p & 1u)
+            v[i][e] = make_float2(x.x * cs[p] - x.y * sn[p], x.x * sn[p] + x.y * cs[p]);
+        }
       }
     }
   }
@@ -295,19 +303,29 @@ struct Walk {
 
 // The walk of `ctas` CTAs (on return no more than have a run), each with `groups` rows at a
 // time and `batch` of a run together.  Runs of up to 16 rows: all read and write near one
-// another, and a run's rows have one stride and, of heads, one position.
+// another, and a run's rows have one stride and, of heads, one position; shorter ones where
+// they can be dealt out more evenly (opening one costs as much as a part of a row).
 inline Walk make_walk(int b, int s, int H, bool turned, int groups, int batch, int* ctas) {
-  Walk w;
-  w.tokens = turned && H < 4;
-  const long long rows = (long long)b * s * H, inner = w.tokens ? s : H, most = (long long)*ctas * groups;
-  const long long share = std::min<long long>(16, (rows + most - 1) / most);
-  const long long pieces = (inner + share - 1) / share;
-  w.run = (int)(((inner + pieces - 1) / pieces + batch - 1) / batch * batch);
-  w.per_outer = (int)((inner + w.run - 1) / w.run);
-  w.runs = (int)(rows / inner * w.per_outer);
-  *ctas = (int)std::min<long long>((w.runs + groups - 1) / groups, *ctas);
-  w.rounds = (w.runs + *ctas * groups - 1) / (*ctas * groups);
-  return w;
+  Walk best{};
+  best.tokens = turned && H < 4;
+  const long long rows = (long long)b * s * H, inner = best.tokens ? s : H, most = (long long)*ctas * groups;
+  const double open = turned && !best.tokens ? 0.6 : 0.2;
+  double least = 0;
+  for (int run = 16; run >= batch; run -= batch) {
+    Walk w = best;
+    const long long pieces = (inner + run - 1) / run;
+    w.run = (int)(((inner + pieces - 1) / pieces + batch - 1) / batch * batch);
+    w.per_outer = (int)((inner + w.run - 1) / w.run);
+    w.runs = (int)(rows / inner * w.per_outer);
+    w.rounds = (int)((w.runs + most - 1) / most);
+    const double cost = w.rounds * (w.run + open);
+    if (least > 0 && cost >= least) continue;
+    least = cost;
+    best = w;
+  }
+  *ctas = (int)std::min<long long>((best.runs + groups - 1) / groups, *ctas);
+  best.rounds = (best.runs + *ctas * groups - 1) / (*ctas * groups);
+  return best;
 }
 
 // Lanes of a row of d channels: a power of two, with 16 channels on each.

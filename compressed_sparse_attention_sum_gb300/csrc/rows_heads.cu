@@ -19,16 +19,20 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Rows that are used together (their sums are shuffled side by side), and batches
-// under way: 256 bytes a thread, 128 KB an SM.
-template <typename T>
-struct Depth {
-  static constexpr int kBatch = sizeof(T) == 2 ? 2 : 1, kStages = 4;
-};
+// Rows that are used together, their sums shuffled side by side: two bf16 rows of a norm
+// alone (1M x 512: 337 us, one at a time 354); a rotation has as much to do meanwhile.
+template <typename T, int ROPE, int KIND>
+constexpr int batch_rows() {
+  return sizeof(T) == 2 && KIND != kNormNone && ROPE == kRopeNone ? 2 : 1;
+}
+constexpr int kStages = 4;                              // batches under way
 
-template <typename TI, typename TO, int ROPE, int V, int KIND>
-__global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int lanes, Walk walk) {
-  constexpr int NU = 8 / V, kBatch = Depth<TI>::kBatch, kStages = Depth<TI>::kStages;
+// PER_SM: CTAs an SM; with three the weight stays in shared memory.
+template <typename TI, typename TO, int ROPE, int V, int KIND, int PER_SM>
+__global__ void __launch_bounds__(kThreads, PER_SM)
+rows_fwd_kernel(RowsFwd a, int lanes, Walk walk) {
+  constexpr int NU = 8 / V, kBatch = batch_rows<TI, ROPE, KIND>();
+  constexpr bool kKeep = PER_SM < 3;
   constexpr bool NORM = KIND != kNormNone;
   using Vec = Pack<TI, V>;
   extern __shared__ __align__(16) unsigned char s_raw[];
@@ -36,6 +40,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
   using PosSlot = VecSlot<Word, kThreads>;              // [stage][row] of s_pos
   unsigned char* s_pos = s_raw + sizeof(Vec) * kStages * kBatch * NU * 2 * kThreads;
   __shared__ int64_t s_turns[ROPE == kRopeNone ? 1 : kMaxHeadWidth / 2];
+  __shared__ __align__(16) float s_w[NORM && !kKeep ? kMaxHeadWidth : 1];
   const int lane = threadIdx.x & (lanes - 1);
   const int step = (int)gridDim.x * (kThreads / lanes);
   const long long x_step = (walk.tokens ? a.xs.t : a.xs.h) * (int)sizeof(TI);
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
   for (int k = 0; k < NU; ++k) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if constexpr (NORM) {
+      if constexpr (NORM && kKeep) {
         Pack<float, V> pw, pc;
 #pragma unroll
         for (int e = 0; e < V; ++e) pw.w[e] = __float_as_uint(1.f), pc.w[e] = 0;
@@ -101,6 +106,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
 #pragma unroll
     for (int e = 0; e < V; ++e) cs[k][e] = 1.f, sn[k][e] = 0.f;
   }
+  static_assert(kKeep || (KIND == kNormRms && ROPE != kRopeNone), "");
+  if constexpr (!kKeep)
+    for (int i = threadIdx.x; i < a.d; i += kThreads) s_w[i] = a.weight != nullptr ? a.weight[i] : 1.f;
   if constexpr (ROPE != kRopeNone) {
     for (int i = threadIdx.x; i < a.rope.dim / 2; i += kThreads) s_turns[i] = a.rope.turns[i];
     __syncthreads();
@@ -178,13 +186,16 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
 #pragma unroll
         for (int k = 0; k < NU; ++k)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < 2; ++i) {
+            Pack<float, V> pw;
+            if constexpr (!kKeep) pw.load(s_w + max(at[k][i], 0));
 #pragma unroll
             for (int e = 0; e < V / 2; ++e) {
               const float2 y = mul2(v[u][k][i][e], make_float2(r, r));
-              v[u][k][i][e] =
-                  KIND == kNormLayer ? fma2(y, w[k][i][e], c[k][i][e]) : mul2(y, w[k][i][e]);
+              const float2 we = kKeep ? w[k][i][e] : pw.two(e);
+              v[u][k][i][e] = KIND == kNormLayer ? fma2(y, we, c[k][i][e]) : mul2(y, we);
             }
+          }
       }
       if (KIND == kNormRms && a.bias != nullptr) {      // rare: not kept in registers
 #pragma unroll
@@ -243,23 +254,26 @@ __global__ void __launch_bounds__(kThreads, 2) rows_fwd_kernel(RowsFwd a, int la
   }
 }
 
-template <typename TI, typename TO, int ROPE, int V, int KIND>
+template <typename TI, typename TO, int ROPE, int V, int KIND, int PER_SM = 2>
 cudaError_t fwd(const RowsFwd& a, cudaStream_t st) {
-  constexpr size_t smem = (size_t)Depth<TI>::kStages * Depth<TI>::kBatch * kThreads *
+  constexpr int kBatch = batch_rows<TI, ROPE, KIND>();
+  constexpr size_t smem = (size_t)kStages * kBatch * kThreads *
                           (16 * sizeof(TI) + (ROPE != kRopeNone ? sizeof(int) : 0));
   static SmemOnce once;
-  const auto k = rows_fwd_kernel<TI, TO, ROPE, V, KIND>;
+  const auto k = rows_fwd_kernel<TI, TO, ROPE, V, KIND, PER_SM>;
   const cudaError_t e = once(k, smem);
   if (e != cudaSuccess) return e;
-  const int lanes = row_lanes<V>(a.d), groups = kThreads / lanes;
-  int ctas = 2 * 152;
-  const Walk w = make_walk(a.b, a.s, a.H, ROPE != kRopeNone, groups, Depth<TI>::kBatch, &ctas);
+  const int lanes = row_lanes<V>(a.d);
+  int ctas = PER_SM * 152;
+  const Walk w = make_walk(a.b, a.s, a.H, ROPE != kRopeNone, kThreads / lanes, kBatch, &ctas);
   k<<<(unsigned)ctas, kThreads, smem, st>>>(a, lanes, w);
   count_launches(1);
   return cudaGetLastError();
 }
 
 // Vectors of 16 bytes; the half layout's pairs on smaller ones where dim or first ask for it.
+// bf16 rows of many heads, normed and turned, are bound by the warps' latency: three CTAs an SM
+// (2 x 8192 tokens of 64 heads x 512 in 343 us, two CTAs 377; one head 44.7, two 38.6).
 template <typename TI, typename TO, int KIND>
 cudaError_t fwd_rope(const RowsFwd& a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(TI);
@@ -267,9 +281,14 @@ cudaError_t fwd_rope(const RowsFwd& a, cudaStream_t st) {
     if constexpr (KIND != kNormNone) return fwd<TI, TO, kRopeNone, V, KIND>(a, st);
     return cudaErrorInvalidValue;
   }
-  if (!a.rope.half) return fwd<TI, TO, kRopeInter, V, KIND>(a, st);
-  if (half_by(V, a.rope)) return fwd<TI, TO, kRopeHalf, V, KIND>(a, st);
-  return fwd<TI, TO, kRopeHalf, 2, KIND>(a, st);
+  if (a.rope.half && !half_by(V, a.rope)) return fwd<TI, TO, kRopeHalf, 2, KIND>(a, st);
+  if constexpr (KIND == kNormRms && sizeof(TI) == 2) {
+    if (a.H >= 4)
+      return a.rope.half ? fwd<TI, TO, kRopeHalf, V, KIND, 3>(a, st)
+                         : fwd<TI, TO, kRopeInter, V, KIND, 3>(a, st);
+  }
+  return a.rope.half ? fwd<TI, TO, kRopeHalf, V, KIND>(a, st)
+                     : fwd<TI, TO, kRopeInter, V, KIND>(a, st);
 }
 
 }  // namespace
