@@ -5,18 +5,20 @@
 // call's rows: per channel the softmax of the scores weighs the rows.  The pooled
 // row is cast once, normalised, turned by its position and cast again.
 //
-// One CTA a block: d / 8 threads have 8 channels each of one token at a time, the
-// other threads other tokens, each with a running maximum and sum; they are joined
-// through shared memory.
+// Pooling: a thread has 8 channels and every `slices`-th token of a block, kTokens of them
+// read together, with a running maximum, sum and weighted sum; the slices are joined through
+// shared memory.  Blocks of few tokens have one slice, several of them share a CTA; long ones
+// have as many slices as 512 threads allow (a block of 128 tokens x 512 channels is 256 KB:
+// 8 slices of 16 tokens).  How a block is cut depends on ratio, coff and d alone, so its row
+// does not depend on the calls that its tokens came in.  Then a warp takes a row.
 #include "cache_format.cuh"
 #include "compress_decode.h"
 #include "csa_kernels.h"
 #include "rows.cuh"
+#include "smem_once.h"
 
 namespace csa {
 namespace {
-
-constexpr int kThreads = 256;
 
 struct Place {        // of a CTA's sequence
   int n, t0;          // its tokens; the first new position (may be negative)
@@ -34,187 +36,289 @@ __device__ __forceinline__ Place place_of(const CompressDecodeArgs& a, int i, bo
   return p;
 }
 
-// New rows k in [k0, k1) of sequence i into the rings.
+// `rows` new rows from row k0 of sequence i on into the rings.
 template <typename T>
 __device__ __forceinline__ void store_ring(const CompressDecodeArgs& a, int i, int t0, int k0,
-                                           int k1) {
+                                           int rows) {
   const T* kv = (const T*)a.kv + i * a.kv_bs;
   const T* sc = (const T*)a.score + i * a.sc_bs;
   T* kr = (T*)a.kv_ring + (long long)i * a.R * a.d;
   T* sr = (T*)a.score_ring + (long long)i * a.R * a.sw;
-  k0 = max(k0, a.s_q - a.R);                    // of more than R tokens the last
-  const int per = a.d / 8;
-  for (int x = (int)threadIdx.x; x < (k1 - k0) * per; x += kThreads) {
-    // Padding is skipped here and not by a bound max(k0, -t0): nvcc 13.0 was seen to take
-    // that maximum of t0 instead of -t0 (next to max(t0, 0)), and no token was stored.
-    const int k = k0 + x / per, c = x % per * 8, t = t0 + k;
-    if (t < 0) continue;
-    const int slot = t % a.R;
-    float v[8];
-    load8(kv + k * a.kv_rs + c, v);
-    store8(kr + (long long)slot * a.d + c, v);
-    if (a.sw != 1) {
-      load8(sc + k * a.sc_rs + c, v);
-      store8(sr + (long long)slot * a.d + c, v);
-    } else if (c == 0) {
-      sr[slot] = sc[k * a.sc_rs];
+  const int per = a.d / 8, vecs = a.sw == 1 ? per + 1 : 2 * per;   // of a row (a score of width 1: one)
+  constexpr int kAtOnce = 4;
+  for (int x0 = (int)threadIdx.x; x0 < rows * vecs; x0 += kAtOnce * (int)blockDim.x) {
+    Pack<T, 8> v[kAtOnce];
+    T* to[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      // Padding is skipped here and not by a bound max(k0, -t0): nvcc 13.0 was seen to take
+      // that maximum of t0 instead of -t0 (next to max(t0, 0)), and no token was stored.
+      const int x = x0 + u * (int)blockDim.x, row = x / vecs, e = x - row * vecs, k = k0 + row, t = t0 + k;
+      to[u] = nullptr;
+      if (x >= rows * vecs || t < 0) continue;
+      const long long slot = t % a.R;
+      if (e >= per && a.sw == 1) {
+        sr[slot] = sc[k * a.sc_rs];
+        continue;
+      }
+      const T* from = e < per ? kv + k * a.kv_rs + e * 8 : sc + k * a.sc_rs + (e - per) * 8;
+      to[u] = e < per ? kr + slot * a.d + e * 8 : sr + slot * a.d + (e - per) * 8;
+      v[u].load(from);
     }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u)
+      if (to[u] != nullptr) v[u].store(to[u]);
   }
 }
 
-// Sum over the CTA, of a value of every thread; s has room for the warps.
-__device__ __forceinline__ float cta_sum(float v, float* s) {
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float x = 0.f;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) x += s[w];
-  return x;
+// 2^((z - m) log2 e); m = -inf (nothing but scores of -inf so far) counts as 0, so that
+// such scores have no weight.
+__device__ __forceinline__ float minus_log2(float m) { return m == -INFINITY ? 0.f : -m * kLog2e; }
+// (ex2.approx is within 2^-22 of itself; weights below 2^-126 are 0)
+__device__ __forceinline__ float weight_of(float z, float m2) {
+  float w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(z, kLog2e, m2)));
+  return w;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) compress_decode_kernel(CompressDecodeArgs a) {
-  __shared__ float s_m[kThreads * 8], s_l[kThreads * 8], s_o[kThreads * 8];
-  __shared__ float s_y[kMaxHeadWidth], s_r[2][kThreads / 32];
-  const int i = blockIdx.y, tid = threadIdx.x, d = a.d;
+template <typename T, int kTokens, int THREADS>
+__global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecodeArgs a, int slices,
+                                                                  int groups, int pool_ctas, int rows) {
+  extern __shared__ __align__(16) float s_mem[];
+  const int i = blockIdx.y, tid = threadIdx.x, d = a.d, per = d / 8, size = per * slices;
+  if ((int)blockIdx.x >= pool_ctas) {            // the rings' new rows, beside the pooling
+    const Place p = place_of(a, i, false);
+    const int k0 = ((int)blockIdx.x - pool_ctas) * rows;
+    store_ring<T>(a, i, p.t0, k0, min(rows, a.s_q - k0));
+    return;
+  }
+  const RopeArgs& r = a.rope;
+  const int dim = r.turns != nullptr ? r.dim : 0;
+  const bool norm = a.kind != kNormNone;
+  float* s_w = s_mem;                            // [d] weight, [d] bias
+  int64_t* s_turns = reinterpret_cast<int64_t*>(s_mem + 2 * d);   // [d / 2]
+  float* s_row = s_mem + 3 * d;                  // [groups][d]
+  float* s_part = s_row + groups * d;            // [3][groups][slices][d]
+  const int part = groups * slices * d;
+  // what the end needs is under way while the lengths and the rows are read
+  const auto fetch = [&](void* to, const void* from, int bytes) {
+    for (int x = tid * 16; x < bytes; x += (int)blockDim.x * 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared((char*)to + x)),
+                   "l"((const char*)from + x)
+                   : "memory");
+  };
+  if (norm && a.weight != nullptr) fetch(s_w, a.weight, d * 4);
+  if (norm && a.bias != nullptr) fetch(s_w + d, a.bias, d * 4);
+  if (dim > 0) fetch(s_turns, r.turns, dim / 2 * 8 & ~15);
+  copies_commit();
+  if (tid == 0 && dim % 4 != 0) s_turns[dim / 2 - 1] = r.turns[dim / 2 - 1];
   const Place p = place_of(a, i, blockIdx.x == 0 && tid == 0);
   if (blockIdx.x == 0 && tid == 0) {
     a.first[i] = p.first;
     a.counts[i] = p.count;
   }
-  if (a.store_here)
-    store_ring<T>(a, i, p.t0, (int)blockIdx.x * a.ratio,
-                  min(a.s_q, ((int)blockIdx.x + 1) * a.ratio));
-  if ((int)blockIdx.x >= p.count) return;
-  const int j = p.first + (int)blockIdx.x;
-  const int lo = max(0, (j + 1 - a.coff) * a.ratio), hi = (j + 1) * a.ratio;
-  const int per = d / 8, slices = kThreads / per, slice = tid / per, c0 = (tid - slice * per) * 8;
-  const T* kv = (const T*)a.kv + i * a.kv_bs;
-  const T* sc = (const T*)a.score + i * a.sc_bs;
-  const T* kr = (const T*)a.kv_ring + (long long)i * a.R * d;
-  const T* sr = (const T*)a.score_ring + (long long)i * a.R * a.sw;
-  if (slice < slices) {
+  const int b0 = (int)blockIdx.x * groups;       // this CTA's blocks of the call
+  if (b0 >= p.count) return;
+  const int g = tid / size, in_g = tid - g * size, slice = in_g / per, c0 = (in_g - slice * per) * 8;
+  const bool live = g < groups && b0 + g < p.count;
+  if (live) {
+    const int j = p.first + b0 + g;
+    const int lo = max(0, (j + 1 - a.coff) * a.ratio), hi = (j + 1) * a.ratio;
+    const T* kv = (const T*)a.kv + i * a.kv_bs;
+    const T* sc = (const T*)a.score + i * a.sc_bs;
+    const T* kr = (const T*)a.kv_ring + (long long)i * a.R * d;
+    const T* sr = (const T*)a.score_ring + (long long)i * a.R * a.sw;
     float m[8], l[8], o[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) { m[e] = -INFINITY; l[e] = o[e] = 0.f; }
-    for (int t = lo + slice; t < hi; t += slices) {
-      const bool fresh = t >= p.t0;
-      const int slot = fresh ? 0 : t % a.R;
-      const T* row = fresh ? kv + (t - p.t0) * a.kv_rs : kr + (long long)slot * d;
-      const T* srow = fresh ? sc + (t - p.t0) * a.sc_rs : sr + (long long)slot * a.sw;
-      float v[8], z[8];
-      load8(row + c0, v);
-      if (a.sw == 1) {
-        const float z1 = to_f(srow[0]);
+    int slot = (lo + slice) % a.R;
+#pragma unroll 1
+    for (int t0 = lo + slice; t0 < hi; t0 += slices * kTokens) {
+      Pack<T, 8> v[kTokens], z[kTokens];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = z1;
-      } else {
-        load8(srow + c0, z);
+      for (int k = 0; k < kTokens; ++k) {
+        const int t = t0 + k * slices;
+        if (t >= hi) continue;
+        const bool fresh = t >= p.t0;
+        const T* row = fresh ? kv + (t - p.t0) * a.kv_rs : kr + (long long)slot * d;
+        const T* srow = fresh ? sc + (t - p.t0) * a.sc_rs : sr + (long long)slot * a.sw;
+        v[k].load(row + c0);
+        if (a.sw == 1) {
+          const float z1 = to_f(srow[0]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[k].set(e, make_float2(z1, z1));
+        } else {
+          z[k].load(srow + c0);
+        }
+        slot += slices;                          // (slices <= coff * ratio / 8 < R)
+        if (slot >= a.R) slot -= a.R;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float mn = fmaxf(m[e], z[e]);
-        // a score of -inf has no weight, also in front of the first finite one
-        const float w = z[e] == -INFINITY ? 0.f : expf(z[e] - mn);
-        const float old = m[e] == -INFINITY ? 0.f : expf(m[e] - mn);
-        l[e] = fmaf(l[e], old, w);
-        o[e] = fmaf(o[e], old, w * v[e]);
-        m[e] = mn;
+      for (int e = 0; e < 8; e += 2) {
+        float2 top = make_float2(m[e], m[e + 1]);
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k)
+          if (t0 + k * slices < hi) {
+            const float2 x = z[k].two(e / 2);
+            top.x = fmaxf(top.x, x.x);
+            top.y = fmaxf(top.y, x.y);
+          }
+        const float2 m2 = make_float2(minus_log2(top.x), minus_log2(top.y));
+        const float2 old = make_float2(weight_of(m[e], m2.x), weight_of(m[e + 1], m2.y));
+        l[e] *= old.x, l[e + 1] *= old.y;
+        o[e] *= old.x, o[e + 1] *= old.y;
+        m[e] = top.x, m[e + 1] = top.y;
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k)
+          if (t0 + k * slices < hi) {
+            const float2 x = z[k].two(e / 2), y = v[k].two(e / 2);
+            const float2 w = make_float2(weight_of(x.x, m2.x), weight_of(x.y, m2.y));
+            l[e] += w.x, l[e + 1] += w.y;
+            o[e] = fmaf(w.x, y.x, o[e]), o[e + 1] = fmaf(w.y, y.y, o[e + 1]);
+          }
       }
     }
+    if (slices == 1) {
+      float4* to = reinterpret_cast<float4*>(s_row + g * d + c0);
+      float y[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      s_m[slice * d + c0 + e] = m[e];
-      s_l[slice * d + c0 + e] = l[e];
-      s_o[slice * d + c0 + e] = o[e];
+      for (int e = 0; e < 8; ++e) y[e] = to_f(from_f<T>(o[e] / l[e]));   // the pooled row's one cast
+      to[0] = make_float4(y[0], y[1], y[2], y[3]);
+      to[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+      float4* to = reinterpret_cast<float4*>(s_part + (g * slices + slice) * d + c0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        to[h] = make_float4(m[4 * h], m[4 * h + 1], m[4 * h + 2], m[4 * h + 3]);
+        to[h + part / 4] = make_float4(l[4 * h], l[4 * h + 1], l[4 * h + 2], l[4 * h + 3]);
+        to[h + part / 2] = make_float4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+      }
     }
   }
+  copies_wait<0>();
   __syncthreads();
-  constexpr int kPer = kMaxHeadWidth / kThreads;
-  float y[kPer];
-  float sum = 0.f;
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int c = tid + k * kThreads;
-    y[k] = 0.f;
-    if (c >= d) continue;
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int s = 0; s < slices; ++s) m = fmaxf(m, s_m[s * d + c]);
-    for (int s = 0; s < slices; ++s) {
-      const float ms = s_m[s * d + c];
-      const float w = ms == -INFINITY ? 0.f : expf(ms - m);
-      l = fmaf(s_l[s * d + c], w, l);
-      o = fmaf(s_o[s * d + c], w, o);
+  if (slices > 1) {
+    for (int x = tid; x < groups * d; x += (int)blockDim.x) {
+      const int gr = x / d, c = x - gr * d;
+      if (b0 + gr >= p.count) break;
+      const float* from = s_part + gr * slices * d + c;
+      float top = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll 8
+      for (int s = 0; s < slices; ++s) top = fmaxf(top, from[s * d]);
+      const float m2 = minus_log2(top);
+#pragma unroll 8
+      for (int s = 0; s < slices; ++s) {
+        const float w = weight_of(from[s * d], m2);
+        l = fmaf(from[part + s * d], w, l);
+        o = fmaf(from[2 * part + s * d], w, o);
+      }
+      s_row[x] = to_f(from_f<T>(o / l));         // the pooled row's one cast
     }
-    y[k] = to_f(from_f<T>(o / l));               // the pooled row's one cast
-    sum += y[k];
-  }
-  if (a.kind != kNormNone) {
-    const float mean = a.kind == kNormLayer ? cta_sum(sum, s_r[0]) / d : 0.f;
-    float q = 0.f;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (tid + k * kThreads < d) q = fmaf(y[k] - mean, y[k] - mean, q);
-    const float rstd = 1.f / sqrtf(cta_sum(q, s_r[1]) / d + a.eps);
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int c = tid + k * kThreads;
-      if (c >= d) continue;
-      y[k] = (y[k] - mean) * rstd;
-      if (a.weight != nullptr) y[k] *= a.weight[c];
-      if (a.bias != nullptr) y[k] += a.bias[c];
-    }
-  }
-  T* out = (T*)a.out + i * a.out_bs + (long long)blockIdx.x * d;
-  const RopeArgs& r = a.rope;
-  if (r.turns != nullptr) {
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (tid + k * kThreads < d) s_y[tid + k * kThreads] = y[k];
     __syncthreads();
   }
+  const int lane = tid & 31;
+  constexpr int kQuads = kMaxHeadWidth / 128;    // float4 of a lane
+  for (int gr = tid >> 5; gr < groups && b0 + gr < p.count; gr += (int)blockDim.x / 32) {
+    float4* y = reinterpret_cast<float4*>(s_row + gr * d);
+    if (norm) {
+      float4 v[kQuads];
+      float mean = 0.f, q = 0.f;
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int c = tid + k * kThreads, at = c - r.first;
-    if (c >= d) continue;
-    float v = y[k];
-    if (r.turns != nullptr && at >= 0 && at < r.dim) {
-      const int half = r.dim / 2;
-      const bool second = r.half ? at >= half : (at & 1) != 0;
-      const int pair = r.half ? (second ? at - half : at) : at / 2;
-      const int apart = r.half ? half : 1;
-      const long long turn[2] = {r.turns[pair], 0};
-      float2 c2, s2;
-      turn_cos_sin(turn, hi - 1, &c2, &s2);
-      const float cs = c2.x * r.scale, sn = s2.x * r.scale;
-      v = second ? s_y[c - apart] * sn + v * cs : v * cs - s_y[c + apart] * sn;
+      for (int k = 0; k < kQuads; ++k) {
+        v[k] = lane + 32 * k < d / 4 ? y[lane + 32 * k] : make_float4(0.f, 0.f, 0.f, 0.f);
+        mean += v[k].x + v[k].y + v[k].z + v[k].w;
+      }
+      mean = a.kind == kNormLayer ? warp_sum(mean) / d : 0.f;
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        v[k].x -= mean, v[k].y -= mean, v[k].z -= mean, v[k].w -= mean;
+        if (lane + 32 * k < d / 4)
+          q += v[k].x * v[k].x + v[k].y * v[k].y + v[k].z * v[k].z + v[k].w * v[k].w;
+      }
+      const float rstd = rsqrtf(warp_sum(q) / d + a.eps);
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        if (lane + 32 * k >= d / 4) continue;
+        float4 w = make_float4(1.f, 1.f, 1.f, 1.f), c = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.weight != nullptr) w = reinterpret_cast<const float4*>(s_w)[lane + 32 * k];
+        if (a.bias != nullptr) c = reinterpret_cast<const float4*>(s_w + d)[lane + 32 * k];
+        y[lane + 32 * k] = make_float4(fmaf(v[k].x * rstd, w.x, c.x), fmaf(v[k].y * rstd, w.y, c.y),
+                                       fmaf(v[k].z * rstd, w.z, c.z), fmaf(v[k].w * rstd, w.w, c.w));
+      }
+      __syncwarp();
     }
-    out[c] = from_f<T>(v);
+    if (dim > 0) {
+      const int pos = (p.first + b0 + gr + 1) * a.ratio - 1;
+      float* x = s_row + gr * d + r.first;
+      for (int e = lane; e < dim / 2; e += 32) {
+        const long long turn[2] = {s_turns[e], 0};
+        float2 c2, s2;
+        turn_cos_sin(turn, pos, &c2, &s2);
+        const float cs = c2.x * r.scale, sn = s2.x * r.scale;
+        float &u = x[r.half ? e : 2 * e], &v = x[r.half ? e + dim / 2 : 2 * e + 1];
+        const float u0 = u, v0 = v;
+        u = u0 * cs - v0 * sn;
+        v = u0 * sn + v0 * cs;
+      }
+      __syncwarp();
+    }
+    T* out = (T*)a.out + i * a.out_bs + (long long)(b0 + gr) * d;
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+      const int c = lane + 32 * k;
+      if (c >= d / 4) continue;
+      const float4 v = y[c];
+      Pack<T, 4> o;
+      o.set(0, make_float2(v.x, v.y));
+      o.set(1, make_float2(v.z, v.w));
+      o.store(out + 4 * c);
+    }
   }
 }
 
-// The rings' new rows, behind a pooling kernel that still read what they overwrite.
+// The rings' new rows, of more than a ring has the last, behind a pooling kernel that still
+// read what they overwrite.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) compress_decode_store_kernel(CompressDecodeArgs a,
-                                                                         int rows) {
+__global__ void __launch_bounds__(256) compress_decode_store_kernel(CompressDecodeArgs a, int rows) {
   const Place p = place_of(a, (int)blockIdx.y, false);
   const int k0 = max(0, a.s_q - a.R) + (int)blockIdx.x * rows;
-  store_ring<T>(a, (int)blockIdx.y, p.t0, k0, min(a.s_q, k0 + rows));
+  store_ring<T>(a, (int)blockIdx.y, p.t0, k0, min(rows, a.s_q - k0));
+}
+
+// Rows of a CTA that stores: 8 vectors for each of 256 threads.
+int store_rows(int d) { return std::max(1, 2048 / (d / 4)); }
+
+template <typename T, int kTokens, int THREADS>
+cudaError_t launch_pool(const CompressDecodeArgs& a, int slices, cudaStream_t st) {
+  const int size = a.d / 8 * slices, blocks = (a.s_q - 1) / a.ratio + 1;
+  const int groups = std::max(1, std::min(blocks, THREADS / size));
+  const int threads = (groups * size + 31) / 32 * 32;
+  const size_t smem = (size_t)a.d * sizeof(float) * (3 + groups * (slices > 1 ? 1 + 3 * slices : 1));
+  static SmemOnce once;
+  const auto k = compress_decode_kernel<T, kTokens, THREADS>;
+  const cudaError_t e = once(k, (size_t)(3 * kMaxHeadWidth + THREADS * (8 + 24)) * sizeof(float));
+  if (e != cudaSuccess) return e;
+  const int pool = (blocks + groups - 1) / groups, rows = store_rows(a.d);
+  const int store = a.store_here ? (a.s_q + rows - 1) / rows : 0;
+  k<<<dim3((unsigned)(pool + store), (unsigned)a.b), threads, smem, st>>>(a, slices, groups, pool, rows);
+  count_launches(1);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch(CompressDecodeArgs a, cudaStream_t st) {
   // no slot that a pooled block reads is one that the new rows take
   a.store_here = a.R >= (long long)a.coff * a.ratio - 1 + a.s_q;
-  const unsigned blocks = (unsigned)((a.s_q - 1) / a.ratio + 1);
-  compress_decode_kernel<T><<<dim3(blocks, (unsigned)a.b), kThreads, 0, st>>>(a);
-  count_launches(1);
-  const cudaError_t e = cudaGetLastError();
+  constexpr int kTokens = sizeof(T) == 2 ? 8 : 4;
+  int slices = 1;
+  while (slices * 2 * 8 <= a.coff * a.ratio && a.d / 8 * slices * 2 <= 512 && slices < 32) slices *= 2;
+  const cudaError_t e = a.d / 8 * slices <= 256 ? launch_pool<T, kTokens, 256>(a, slices, st)
+                                                : launch_pool<T, kTokens, 512>(a, slices, st);
   if (e != cudaSuccess || a.store_here) return e;
-  const int rows = 16, n = a.s_q < a.R ? a.s_q : a.R;
+  const int rows = store_rows(a.d), n = a.s_q < a.R ? a.s_q : a.R;
   compress_decode_store_kernel<T>
-      <<<dim3((unsigned)((n + rows - 1) / rows), (unsigned)a.b), kThreads, 0, st>>>(a, rows);
+      <<<dim3((unsigned)((n + rows - 1) / rows), (unsigned)a.b), 256, 0, st>>>(a, rows);
   count_launches(1);
   return cudaGetLastError();
 }
