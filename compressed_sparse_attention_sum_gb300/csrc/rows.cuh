@@ -310,8 +310,10 @@ inline Walk make_walk(int b, int s, int H, bool turned, int groups, int batch, i
   best.tokens = turned && H < 4;
   const long long rows = (long long)b * s * H, inner = best.tokens ? s : H, most = (long long)*ctas * groups;
   const double open = turned && !best.tokens ? 0.6 : 0.2;
+  // one round: the shortest runs; very many: the longest
+  const int longest = rows <= most ? batch : 16, shortest = rows > 64 * most ? 16 : batch;
   double least = 0;
-  for (int run = 16; run >= batch; run -= batch) {
+  for (int run = longest; run >= shortest; run -= batch) {
     Walk w = best;
     const long long pieces = (inner + run - 1) / run;
     w.run = (int)(((inner + pieces - 1) / pieces + batch - 1) / batch * batch);

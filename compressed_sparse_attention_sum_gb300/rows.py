@@ -15,8 +15,7 @@ import torch
 
 from . import csa
 from .csa import CSAError  # noqa: F401  (re-exported)
-from .serve import (_DT, _F32, _I32, _call, _elsewhere, _empty, _on, _optional, _refuse,
-                    _workspace)
+from .serve import _DT, _F32, _I32, _elsewhere, _empty, _on, _optional, _refuse, _workspace
 
 _c_int, _c_ll, _c_p, _c_f, _c_sz, _c_d = (ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p,
                                           ctypes.c_float, ctypes.c_size_t, ctypes.c_double)
@@ -72,6 +71,28 @@ def load_library():
             fn.argtypes = args
         _declared = lib
     return lib
+
+
+_entries = {}
+
+
+def _call(name, dev, stream, *args):
+    """Call an entry point with device dev current, on `stream` or on dev's current stream."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(load_library(), name)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, *args)
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, expected cuda:{dev}")
+    else:
+        s = stream.cuda_stream
+    code = fn(*args, s)
+    if code != 0:
+        raise CSAError(name, code)
 
 
 class CsaRope:
@@ -132,6 +153,15 @@ def csa_rope_turns(freqs, device="cuda") -> torch.Tensor:
     if code != 0:
         raise CSAError("csa_rope_turns", code)
     return out.to(device)
+
+
+def _new(shape, dtype, dev):
+    """An uninitialised contiguous tensor on device dev."""
+    strides, n = [], 1
+    for size in reversed(shape):
+        strides.append(n)
+        n *= size
+    return _empty(tuple(shape), tuple(reversed(strides)), dtype, dev)
 
 
 def _first(t, name):
@@ -198,7 +228,8 @@ def _strides(t, name):
 def _vector(t, name, n, dev):
     if t is None:
         return None
-    _optional(t, name, _F32, (n,), dev)
+    if not (t.get_device() == dev and t.dtype is _F32 and t.shape == (n,) and t.is_contiguous()):
+        _refuse(dev, **{name: (t, _F32, (n,))})
     return t.data_ptr()
 
 
@@ -245,11 +276,11 @@ def csa_norm(x: torch.Tensor, kind: int, weight: Optional[torch.Tensor] = None,
         raise ValueError("x must be [..., n]")
     n = x.shape[-1]
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x.shape, x.dtype, dev)
     elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
         _refuse(dev, out=(out, x.dtype, x.shape))
-    _call_rows("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind,
-               _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), float(eps),
+    _call("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind,
+               _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), eps,
                out.data_ptr(), _row_stride(out, "out"), x.numel() // n if n else 0, n)
     return out
 
@@ -266,11 +297,11 @@ def _sums(weight, has_bias, dweight, dbias, n, dev):
     if dweight is not None:
         _optional(dweight, "dweight", _F32, (n,), dev)
     elif weight is not None:
-        dweight = torch.empty(n, dtype=_F32, device=f"cuda:{dev}")
+        dweight = _empty((n,), (1,), _F32, dev)
     if dbias is not None:
         _optional(dbias, "dbias", _F32, (n,), dev)
     elif has_bias:
-        dbias = torch.empty(n, dtype=_F32, device=f"cuda:{dev}")
+        dbias = _empty((n,), (1,), _F32, dev)
     return dweight, dbias
 
 
@@ -296,15 +327,15 @@ def csa_norm_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int,
     rows = x.numel() // n if n else 0
     g_dt = _like(dout, "dout", x.shape, dev)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _new(x.shape, x.dtype, dev)
     dx_dt = _like(dx, "dx", x.shape, dev)
     w = _vector(weight, "weight", n, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, n, dev)
     nbytes = (csa_norm_bwd_workspace_size(rows, n, dweight is not None, dbias is not None)
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
-    _call_rows("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind, w,
-               float(eps), dout.data_ptr(), _row_stride(dout, "dout"), g_dt, dx.data_ptr(),
+    _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind, w,
+               eps, dout.data_ptr(), _row_stride(dout, "dout"), g_dt, dx.data_ptr(),
                _row_stride(dx, "dx"), dx_dt, None if dweight is None else dweight.data_ptr(),
                None if dbias is None else dbias.data_ptr(), rows, n, ws, nbytes)
     return dx, dweight, dbias
@@ -322,11 +353,11 @@ def csa_rope(x: torch.Tensor, rope: CsaRope, pos: Optional[torch.Tensor] = None,
     dev, dt = _first(x, "x")
     b, s, H, d = _heads(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x.shape, x.dtype, dev)
     elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
         _refuse(dev, out=(out, x.dtype, x.shape))
     p, ps = _positions(pos, b, s, dev)
-    _call_rows("csa_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, p, ps,
+    _call("csa_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, p, ps,
                _rope(rope, dev), 1 if inverse else 0, out.data_ptr(), _strides(out, "out"), b, s,
                H, d)
     return out
@@ -342,10 +373,10 @@ def csa_rope_bwd(dout: torch.Tensor, rope: CsaRope, pos: Optional[torch.Tensor] 
     dev, dt = _first(dout, "dout")
     b, s, H, d = _heads(dout, "dout")
     if dx is None:
-        dx = torch.empty(dout.shape, dtype=dout.dtype, device=dout.device)
+        dx = _new(dout.shape, dout.dtype, dev)
     dx_dt = _like(dx, "dx", dout.shape, dev)
     p, ps = _positions(pos, b, s, dev)
-    _call_rows("csa_rope_bwd", dev, stream, dout.data_ptr(), _strides(dout, "dout"), dt, p, ps,
+    _call("csa_rope_bwd", dev, stream, dout.data_ptr(), _strides(dout, "dout"), dt, p, ps,
                _rope(rope, dev), 1 if inverse else 0, dx.data_ptr(), _strides(dx, "dx"), dx_dt, b,
                s, H, d)
     return dx
@@ -362,12 +393,12 @@ def csa_norm_rope(x: torch.Tensor, kind: int, rope: CsaRope, pos: Optional[torch
     dev, dt = _first(x, "x")
     b, s, H, d = _heads(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = _new(x.shape, x.dtype, dev)
     elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
         _refuse(dev, out=(out, x.dtype, x.shape))
     p, ps = _positions(pos, b, s, dev)
-    _call_rows("csa_norm_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind,
-               _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), float(eps), p, ps,
+    _call("csa_norm_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind,
+               _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), eps, p, ps,
                _rope(rope, dev), out.data_ptr(), _strides(out, "out"), b, s, H, d)
     return out
 
@@ -388,7 +419,7 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
     b, s, H, d = _heads(x, "x")
     g_dt = _like(dout, "dout", x.shape, dev)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = _new(x.shape, x.dtype, dev)
     dx_dt = _like(dx, "dx", x.shape, dev)
     w = _vector(weight, "weight", d, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, d, dev)
@@ -396,8 +427,8 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
     p, ps = _positions(pos, b, s, dev)
-    _call_rows("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind, w,
-               float(eps), p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
+    _call("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind, w,
+               eps, p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
                dx.data_ptr(), _strides(dx, "dx"), dx_dt,
                None if dweight is None else dweight.data_ptr(),
                None if dbias is None else dbias.data_ptr(), b, s, H, d, ws, nbytes)
@@ -432,32 +463,33 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
     b, s_q, d = kv.shape
     if score.ndim != 3 or kv_ring.ndim != 3 or ratio < 1:
         raise ValueError("score and kv_ring must have three dimensions, ratio be at least 1")
-    sw, R = score.shape[2], kv_ring.shape[1]
-    if not (score.dtype is kv.dtype and kv_ring.dtype is kv.dtype and score_ring.dtype is kv.dtype
+    dtype, sw, R = kv.dtype, score.shape[2], kv_ring.shape[1]
+    if not (score.dtype is dtype and kv_ring.dtype is dtype and score_ring.dtype is dtype
             and seq_lens.dtype is _I32 and score.get_device() == dev
             and kv_ring.get_device() == dev and score_ring.get_device() == dev
-            and seq_lens.get_device() == dev and score.shape[:2] == kv.shape[:2]
+            and seq_lens.get_device() == dev and score.shape == (b, s_q, sw)
             and kv_ring.shape == (b, R, d) and score_ring.shape == (b, R, sw)
             and seq_lens.shape == (b,) and kv_ring.is_contiguous() and score_ring.is_contiguous()
             and seq_lens.is_contiguous()):
-        for t, name, shape in ((kv, "kv", kv.shape), (score, "score", (b, s_q, sw))):
-            if t.dtype is not kv.dtype or t.shape != shape or t.get_device() != dev:
-                _refuse(dev, **{name: (t, kv.dtype, shape)})
-        _refuse(dev, kv_ring=(kv_ring, kv.dtype, (b, R, d)),
-                score_ring=(score_ring, kv.dtype, (b, R, sw)), seq_lens=(seq_lens, _I32, (b,)))
+        if score.dtype is not dtype or score.shape != (b, s_q, sw) or score.get_device() != dev:
+            _refuse(dev, score=(score, dtype, (b, s_q, sw)))
+        _refuse(dev, kv_ring=(kv_ring, dtype, (b, R, d)), score_ring=(score_ring, dtype, (b, R, sw)),
+                seq_lens=(seq_lens, _I32, (b,)))
     kb, kr, kc = kv.stride()
     sb, sr, sc = score.stride()
-    if b and s_q and ((d > 1 and kc != 1) or (sw > 1 and sc != 1)):
+    if ((kc != 1 and d > 1) or (sc != 1 and sw > 1)) and b and s_q:
         raise ValueError("rows of kv and score must be contiguous")
     w, bp = _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev)
     turned = None if rope is None else _rope(rope, dev)
     blocks = -(-s_q // ratio)
     if out is None:
-        out = _empty((b, blocks, d), (blocks * d, d, 1), kv.dtype, dev)
-    elif not (out.dtype is kv.dtype and out.shape == (b, blocks, d) and out.get_device() == dev):
-        _refuse(dev, out=(out, kv.dtype, (b, blocks, d)))
-    elif blocks and (out.stride(2) != 1 or (blocks > 1 and out.stride(1) != d)):
-        raise ValueError("out rows must be packed")
+        out, ob = _empty((b, blocks, d), (blocks * d, d, 1), dtype, dev), blocks * d
+    else:
+        if not (out.dtype is dtype and out.shape == (b, blocks, d) and out.get_device() == dev):
+            _refuse(dev, out=(out, dtype, (b, blocks, d)))
+        ob, orow, oc = out.stride()
+        if blocks and b and (oc != 1 or (blocks > 1 and orow != d)):
+            raise ValueError("out rows must be packed")
     if first is None:
         first = _empty((b,), (1,), _I32, dev)
     else:
@@ -466,14 +498,8 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
         counts = _empty((b,), (1,), _I32, dev)
     else:
         _optional(counts, "counts", _I32, (b,), dev)
-    _call_rows("csa_compress_decode", dev, stream, kv.data_ptr(), kb, kr, score.data_ptr(),
+    _call("csa_compress_decode", dev, stream, kv.data_ptr(), kb, kr, score.data_ptr(),
           sb, sr, sw, kv_ring.data_ptr(), score_ring.data_ptr(), R, seq_lens.data_ptr(), kind, w,
-          bp, float(eps), turned, out.data_ptr(), out.stride(0), first.data_ptr(),
+          bp, eps, turned, out.data_ptr(), ob, first.data_ptr(),
           counts.data_ptr(), b, s_q, d, ratio, coff, dt)
     return out, first, counts
-
-
-def _call_rows(name, dev, stream, *args):
-    if _declared is None:
-        load_library()
-    _call(name, dev, stream, *args)
