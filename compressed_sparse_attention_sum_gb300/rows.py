@@ -217,11 +217,14 @@ def _strides(t, name):
         key = (*key[:2], 0, key[2])
     got = _strides_of.get(key)
     if got is None:
-        if key[3] != 1 and t.numel():
-            raise ValueError(f"{name} rows must be contiguous")
+        got = ctypes.byref(_Strides(*key[:3]))
+        if key[3] != 1:
+            if t.numel():
+                raise ValueError(f"{name} rows must be contiguous")
+            return got
         if len(_strides_of) >= 4096:
             _strides_of.clear()
-        got = _strides_of[key] = ctypes.byref(_Strides(*key[:3]))
+        _strides_of[key] = got
     return got
 
 
@@ -280,7 +283,7 @@ def csa_norm(x: torch.Tensor, kind: int, weight: Optional[torch.Tensor] = None,
     elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
         _refuse(dev, out=(out, x.dtype, x.shape))
     _call("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind,
-               _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), eps,
+               _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), float(eps),
                out.data_ptr(), _row_stride(out, "out"), x.numel() // n if n else 0, n)
     return out
 
@@ -335,7 +338,7 @@ def csa_norm_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int,
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
     _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind, w,
-               eps, dout.data_ptr(), _row_stride(dout, "dout"), g_dt, dx.data_ptr(),
+               float(eps), dout.data_ptr(), _row_stride(dout, "dout"), g_dt, dx.data_ptr(),
                _row_stride(dx, "dx"), dx_dt, None if dweight is None else dweight.data_ptr(),
                None if dbias is None else dbias.data_ptr(), rows, n, ws, nbytes)
     return dx, dweight, dbias
@@ -398,7 +401,7 @@ def csa_norm_rope(x: torch.Tensor, kind: int, rope: CsaRope, pos: Optional[torch
         _refuse(dev, out=(out, x.dtype, x.shape))
     p, ps = _positions(pos, b, s, dev)
     _call("csa_norm_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind,
-               _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), eps, p, ps,
+               _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), float(eps), p, ps,
                _rope(rope, dev), out.data_ptr(), _strides(out, "out"), b, s, H, d)
     return out
 
@@ -428,7 +431,7 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
     p, ps = _positions(pos, b, s, dev)
     _call("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind, w,
-               eps, p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
+               float(eps), p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
                dx.data_ptr(), _strides(dx, "dx"), dx_dt,
                None if dweight is None else dweight.data_ptr(),
                None if dbias is None else dbias.data_ptr(), b, s, H, d, ws, nbytes)
@@ -500,6 +503,6 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
         _optional(counts, "counts", _I32, (b,), dev)
     _call("csa_compress_decode", dev, stream, kv.data_ptr(), kb, kr, score.data_ptr(),
           sb, sr, sw, kv_ring.data_ptr(), score_ring.data_ptr(), R, seq_lens.data_ptr(), kind, w,
-          bp, eps, turned, out.data_ptr(), ob, first.data_ptr(),
+          bp, float(eps), turned, out.data_ptr(), ob, first.data_ptr(),
           counts.data_ptr(), b, s_q, d, ratio, coff, dt)
     return out, first, counts

@@ -238,6 +238,15 @@ def test_strided_inputs_and_streams():
     assert torch.equal(a, b[:, :7])
 
 
+def test_rings_beyond_32_bits():
+    """Sequences whose rings start behind 2^31 elements."""
+    L = Layer(73, 5, 24, 512, 4, 2, "d", BF, orc.RMS, 64)
+    want = L.run(L.rings(8), [24])
+    rings = tuple(torch.full((5, (1 << 20) + 7, 512), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    assert torch.equal(L.run(rings, [9, 1, 1, 1, 12]), want)
+    assert torch.equal(rings[0][:, :24], L.kv) and torch.equal(rings[1][:, :24], L.score)
+
+
 def test_the_binding_refuses():
     L = Layer(67, 2, 8, 64, 4, 1, "d", BF)
     kr, sr = L.rings(8)

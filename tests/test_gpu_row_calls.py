@@ -1,6 +1,9 @@
 """The row calls on the GPU against the fp64 oracle (oracle/rows_oracle.py, which also
 derives how far fp32 arithmetic may be off): norms, rotary positions and both in one
 pass, their gradients, strides, types, positions, streams and graphs."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -356,6 +359,102 @@ def test_other_streams_and_replayed_graphs():
         torch.cuda.synchronize()
         for _, res in graphs:
             assert all(torch.equal(p, q) for p, q in zip(res, want[i % 3]))
+
+
+FIRST_CALLS = """
+import sys
+sys.path[:0] = {path!r}
+import torch
+from compressed_sparse_attention_sum_gb300 import csa, rows
+g = torch.Generator(device="cuda").manual_seed(0)
+f = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+half = rows.CsaRope(rows.csa_rope_turns(rows.csa_rope_freqs(128)), 0, "half")
+inter = rows.CsaRope(rows.csa_rope_turns(rows.csa_rope_freqs(64)), 64)
+x, h, wide, w = f(2, 30, 8, 128).bfloat16(), f(300, 4096).bfloat16(), f(4096), f(128)
+kv, score, rings = f(2, 9, 128).bfloat16(), f(2, 9, 128).bfloat16(), [torch.zeros(2, 16, 128, device="cuda").bfloat16() for _ in range(2)]
+lens = torch.full((2,), 9, dtype=torch.int32, device="cuda")
+out = torch.zeros(2, 3, 128, device="cuda").bfloat16()
+def step():
+    y = rows.csa_norm_rope(x, 1, half, None, w)
+    r = rows.csa_compress_decode(kv, score, *rings, lens, 4, 2, 1, w, None, 1e-6, inter, out=out)
+    return [y, rows.csa_rope(y, inter), rows.csa_rope_bwd(y, inter), *rows.csa_norm_rope_bwd(x, y, 2, half, None, w, has_bias=True),
+            rows.csa_norm(h, 2, wide), *rows.csa_norm_bwd(h, h, 1, wide)[:2], *(t.clone() for t in r)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert csa.csa_get_device_status() == 0
+assert all(torch.equal(x, y) for x, y in zip(got, step()))
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(path=sys.path)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2^31 elements and more apart, in and out."""
+    rng = np.random.default_rng(29)
+    far = (1 << 31) + 64
+    big = torch.empty(3 * far, dtype=BF, device="cuda")
+    rope, w = plan(orc.freqs(64), 64, True), draw(rng, 4096)[0]
+    for n in (128, 4096):
+        src, _ = draw(rng, 2, n, dtype=BF)
+        x, y = big.as_strided((2, n), (far, 1)), big.as_strided((2, n), (far, 1), 8192)
+        x.copy_(src)
+        rows.csa_norm(x, orc.LAYER, w[:n], None, EPS, out=y)
+        assert torch.equal(y, rows.csa_norm(src, orc.LAYER, w[:n], None, EPS))
+        got = rows.csa_norm_bwd(x, x, orc.LAYER, w[:n], EPS, has_bias=True, dx=y)
+        assert all(torch.equal(p, q) for p, q in zip(got, rows.csa_norm_bwd(src, src, orc.LAYER, w[:n], EPS, has_bias=True)))
+    src, _ = draw(rng, 2, 3, 5, 128, dtype=BF)
+    pos = torch.tensor([7, 1 << 30, 9], dtype=I32, device="cuda")
+    for strides in ((far, 640, 128), (128, far // 2, 256), (640, 128 * 16, far // 4)):
+        x, y = big.as_strided((2, 3, 5, 128), (*strides, 1)), big.as_strided((2, 3, 5, 128), (*strides, 1), 8192 * 4)
+        x.copy_(src)
+        rows.csa_norm_rope(x, orc.RMS, rope, pos, w[:128], out=y)
+        want = rows.csa_norm_rope(src, orc.RMS, rope, pos, w[:128])
+        assert torch.equal(y, want)
+        got = rows.csa_norm_rope_bwd(x, x, orc.RMS, rope, pos, w[:128], dx=y)
+        assert all(torch.equal(p, q) for p, q in zip(got[:2], rows.csa_norm_rope_bwd(src, src, orc.RMS, rope, pos, w[:128])[:2]))
+
+
+def test_two_streams_at_once():
+    """The same calls on two streams, each with a workspace of its own."""
+    rng = np.random.default_rng(31)
+    rope = plan(orc.freqs(128), 0, False)
+    w, _ = draw(rng, 128)
+    wide, _ = draw(rng, 2056)
+    sets = [(draw(rng, 4, 200, 8, 128, dtype=BF)[0], draw(rng, 700, 2056)[0]) for _ in range(2)]
+
+    def step(x, h):
+        return [*rows.csa_norm_rope_bwd(x, x, orc.LAYER, rope, None, w, has_bias=True), *rows.csa_norm_bwd(h, h, orc.LAYER, wide, has_bias=True),
+                rows.csa_norm_rope(x, orc.RMS, rope, None, w), rows.csa_norm(h, orc.RMS, wide)]
+
+    want = [[t.clone() for t in step(*s)] for s in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for res in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(res, want[i]))
+
+
+def test_strides_of_an_empty_tensor_are_not_taken_for_anothers():
+    rope = plan(orc.freqs(8), 0, False)
+    base = torch.zeros(4, 4, 16, 8, dtype=BF, device="cuda")
+    turned = base.transpose(2, 3)                  # rows of 16 channels, 8 apart
+    rows.csa_rope(turned[:0], rope, out=turned[:0].contiguous())
+    with pytest.raises(ValueError, match="contiguous"):
+        rows.csa_rope(turned, rope)
 
 
 def test_the_binding_refuses():
