@@ -184,9 +184,8 @@ def _like(t, name, shape, dev):
     return dt
 
 
-def _row_stride(t, name):
+def _row_stride(t, name, n):
     """Row stride of [..., n] rows that one stride reaches."""
-    n = t.shape[-1]
     if t.is_contiguous():
         return n
     strides, shape = t.stride(), t.shape
@@ -240,20 +239,21 @@ def _positions(pos, b, s, dev):
     """Pointer and batch stride of positions [b, s] or [s]."""
     if pos is None:
         return None, 0
+    shape, strides = pos.shape, pos.stride()
     if (pos.get_device() != dev or pos.dtype is not _I32
-            or (pos.shape != (b, s) and pos.shape != (s,))):
-        _refuse(dev, pos=(pos, _I32, (s,) if pos.ndim == 1 else (b, s)))
-    if s > 1 and pos.stride(-1) != 1:
+            or (shape != (b, s) and shape != (s,))):
+        _refuse(dev, pos=(pos, _I32, (s,) if len(shape) == 1 else (b, s)))
+    if s > 1 and strides[-1] != 1:
         raise ValueError("pos must be contiguous along the tokens")
-    return pos.data_ptr(), (pos.stride(0) if pos.ndim == 2 and b > 1 else 0)
+    return pos.data_ptr(), (strides[0] if len(shape) == 2 and b > 1 else 0)
 
 
-def _heads(x, name):
+def _heads(shape, name):
     """b, s, H, d of [b, s, H, d] or [b, s, d]."""
-    if x.ndim == 4:
-        return x.shape
-    if x.ndim == 3:
-        b, s, d = x.shape
+    if len(shape) == 4:
+        return shape
+    if len(shape) == 3:
+        b, s, d = shape
         return b, s, 1, d
     raise ValueError(f"{name} must be [b, s, H, d] or [b, s, d]")
 
@@ -275,16 +275,17 @@ def csa_norm(x: torch.Tensor, kind: int, weight: Optional[torch.Tensor] = None,
     if stream is not None and _elsewhere(stream, x):
         return _on(stream, csa_norm, x, kind, weight, bias, eps, out)
     dev, dt = _first(x, "x")
-    if x.ndim < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must be [..., n]")
-    n = x.shape[-1]
+    n = shape[-1]
     if out is None:
-        out = _new(x.shape, x.dtype, dev)
-    elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
-        _refuse(dev, out=(out, x.dtype, x.shape))
-    _call("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind,
-               _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), float(eps),
-               out.data_ptr(), _row_stride(out, "out"), x.numel() // n if n else 0, n)
+        out = _new(shape, x.dtype, dev)
+    elif out.dtype is not x.dtype or out.shape != shape or out.get_device() != dev:
+        _refuse(dev, out=(out, x.dtype, shape))
+    _call("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, kind,
+          _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), float(eps),
+          out.data_ptr(), _row_stride(out, "out", n), x.numel() // n if n else 0, n)
     return out
 
 
@@ -324,23 +325,24 @@ def csa_norm_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int,
         return _on(stream, csa_norm_bwd, x, dout, kind, weight, eps, has_bias, dx, dweight, dbias,
                    workspace)
     dev, dt = _first(x, "x")
-    if x.ndim < 1:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must be [..., n]")
-    n = x.shape[-1]
+    n = shape[-1]
     rows = x.numel() // n if n else 0
-    g_dt = _like(dout, "dout", x.shape, dev)
+    g_dt = _like(dout, "dout", shape, dev)
     if dx is None:
-        dx = _new(x.shape, x.dtype, dev)
-    dx_dt = _like(dx, "dx", x.shape, dev)
+        dx = _new(shape, x.dtype, dev)
+    dx_dt = _like(dx, "dx", shape, dev)
     w = _vector(weight, "weight", n, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, n, dev)
     nbytes = (csa_norm_bwd_workspace_size(rows, n, dweight is not None, dbias is not None)
               if workspace is None else 0)
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
-    _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x"), dt, kind, w,
-               float(eps), dout.data_ptr(), _row_stride(dout, "dout"), g_dt, dx.data_ptr(),
-               _row_stride(dx, "dx"), dx_dt, None if dweight is None else dweight.data_ptr(),
-               None if dbias is None else dbias.data_ptr(), rows, n, ws, nbytes)
+    _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, kind, w,
+          float(eps), dout.data_ptr(), _row_stride(dout, "dout", n), g_dt, dx.data_ptr(),
+          _row_stride(dx, "dx", n), dx_dt, None if dweight is None else dweight.data_ptr(),
+          None if dbias is None else dbias.data_ptr(), rows, n, ws, nbytes)
     return dx, dweight, dbias
 
 
@@ -354,15 +356,16 @@ def csa_rope(x: torch.Tensor, rope: CsaRope, pos: Optional[torch.Tensor] = None,
     if stream is not None and _elsewhere(stream, x):
         return _on(stream, csa_rope, x, rope, pos, inverse, out)
     dev, dt = _first(x, "x")
-    b, s, H, d = _heads(x, "x")
+    shape = x.shape
+    b, s, H, d = _heads(shape, "x")
     if out is None:
-        out = _new(x.shape, x.dtype, dev)
-    elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
-        _refuse(dev, out=(out, x.dtype, x.shape))
+        out = _new(shape, x.dtype, dev)
+    elif out.dtype is not x.dtype or out.shape != shape or out.get_device() != dev:
+        _refuse(dev, out=(out, x.dtype, shape))
     p, ps = _positions(pos, b, s, dev)
     _call("csa_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, p, ps,
-               _rope(rope, dev), 1 if inverse else 0, out.data_ptr(), _strides(out, "out"), b, s,
-               H, d)
+          _rope(rope, dev), 1 if inverse else 0, out.data_ptr(), _strides(out, "out"), b, s,
+          H, d)
     return out
 
 
@@ -374,14 +377,15 @@ def csa_rope_bwd(dout: torch.Tensor, rope: CsaRope, pos: Optional[torch.Tensor] 
     if stream is not None and _elsewhere(stream, dout):
         return _on(stream, csa_rope_bwd, dout, rope, pos, inverse, dx)
     dev, dt = _first(dout, "dout")
-    b, s, H, d = _heads(dout, "dout")
+    shape = dout.shape
+    b, s, H, d = _heads(shape, "dout")
     if dx is None:
-        dx = _new(dout.shape, dout.dtype, dev)
-    dx_dt = _like(dx, "dx", dout.shape, dev)
+        dx = _new(shape, dout.dtype, dev)
+    dx_dt = _like(dx, "dx", shape, dev)
     p, ps = _positions(pos, b, s, dev)
     _call("csa_rope_bwd", dev, stream, dout.data_ptr(), _strides(dout, "dout"), dt, p, ps,
-               _rope(rope, dev), 1 if inverse else 0, dx.data_ptr(), _strides(dx, "dx"), dx_dt, b,
-               s, H, d)
+          _rope(rope, dev), 1 if inverse else 0, dx.data_ptr(), _strides(dx, "dx"), dx_dt, b,
+          s, H, d)
     return dx
 
 
@@ -394,15 +398,16 @@ def csa_norm_rope(x: torch.Tensor, kind: int, rope: CsaRope, pos: Optional[torch
     if stream is not None and _elsewhere(stream, x):
         return _on(stream, csa_norm_rope, x, kind, rope, pos, weight, bias, eps, out)
     dev, dt = _first(x, "x")
-    b, s, H, d = _heads(x, "x")
+    shape = x.shape
+    b, s, H, d = _heads(shape, "x")
     if out is None:
-        out = _new(x.shape, x.dtype, dev)
-    elif out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
-        _refuse(dev, out=(out, x.dtype, x.shape))
+        out = _new(shape, x.dtype, dev)
+    elif out.dtype is not x.dtype or out.shape != shape or out.get_device() != dev:
+        _refuse(dev, out=(out, x.dtype, shape))
     p, ps = _positions(pos, b, s, dev)
     _call("csa_norm_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind,
-               _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), float(eps), p, ps,
-               _rope(rope, dev), out.data_ptr(), _strides(out, "out"), b, s, H, d)
+          _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), float(eps), p, ps,
+          _rope(rope, dev), out.data_ptr(), _strides(out, "out"), b, s, H, d)
     return out
 
 
@@ -419,11 +424,12 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
         return _on(stream, csa_norm_rope_bwd, x, dout, kind, rope, pos, weight, eps, has_bias, dx,
                    dweight, dbias, workspace)
     dev, dt = _first(x, "x")
-    b, s, H, d = _heads(x, "x")
-    g_dt = _like(dout, "dout", x.shape, dev)
+    shape = x.shape
+    b, s, H, d = _heads(shape, "x")
+    g_dt = _like(dout, "dout", shape, dev)
     if dx is None:
-        dx = _new(x.shape, x.dtype, dev)
-    dx_dt = _like(dx, "dx", x.shape, dev)
+        dx = _new(shape, x.dtype, dev)
+    dx_dt = _like(dx, "dx", shape, dev)
     w = _vector(weight, "weight", d, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, d, dev)
     nbytes = (csa_norm_bwd_workspace_size(b * s * H, d, dweight is not None, dbias is not None)
@@ -431,10 +437,10 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
     keep, ws, nbytes = _workspace(workspace, nbytes, dev)
     p, ps = _positions(pos, b, s, dev)
     _call("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind, w,
-               float(eps), p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
-               dx.data_ptr(), _strides(dx, "dx"), dx_dt,
-               None if dweight is None else dweight.data_ptr(),
-               None if dbias is None else dbias.data_ptr(), b, s, H, d, ws, nbytes)
+          float(eps), p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
+          dx.data_ptr(), _strides(dx, "dx"), dx_dt,
+          None if dweight is None else dweight.data_ptr(),
+          None if dbias is None else dbias.data_ptr(), b, s, H, d, ws, nbytes)
     return dx, dweight, dbias
 
 
