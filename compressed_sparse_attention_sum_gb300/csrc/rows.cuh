@@ -146,6 +146,13 @@ struct VecSlot {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p), "n"(kPiece) : "memory");
     }
   }
+  // places that nothing is ever asked for, so that they count as zeros
+  static __device__ __forceinline__ void zero(unsigned char* base, int i) {
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+#pragma unroll
+      for (int q = 0; q < kPiece / 4; ++q) reinterpret_cast<uint32_t*>(place(base, i, k))[q] = 0;
+  }
   static __device__ __forceinline__ void take(unsigned char* base, int i, VEC& v) {
 #pragma unroll
     for (int k = 0; k < kPieces; ++k) {

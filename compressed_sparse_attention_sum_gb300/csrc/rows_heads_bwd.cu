@@ -76,6 +76,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwd a, int la
   };
 #pragma unroll 1
   for (int i = 0; i < kStages; ++i) ask(i);
+#pragma unroll
+  for (int k = 0; k < NU; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (at[k][i] < 0)
+        for (int q = 0; q < kStages; ++q)
+          SlotX::zero(s_raw, (q * NU + k) * 2 + i), SlotG::zero(s_g, (q * NU + k) * 2 + i);
   float2 w[NU][2][V / 2], dw[NU][2][V / 2], db[DB ? NU : 1][2][V / 2];
   float cs[NU][V], sn[NU][V];
 #pragma unroll
@@ -116,8 +123,6 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwd a, int la
         VecG g;
         SlotX::take(s_raw, (stage * NU + k) * 2 + i, x[k][i]);
         SlotG::take(s_g, (stage * NU + k) * 2 + i, g);
-        // places that nothing was asked for hold anything
-        if (!live || at[k][i] < 0) x[k][i].clear(), g.clear();
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) dy[k][i][e] = g.two(e);
       }
@@ -187,11 +192,14 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwd a, int la
         for (int e = 0; e < V / 2; ++e) {
           float2 y = x[k][i].two(e);
           if (DB) y = add2(y, make_float2(mean[0], mean[0]));
-          // a row behind the last has dy = 0 but perhaps an infinite r
-          if (live) dw[k][i][e] = fma2(dy[k][i][e], mul2(y, make_float2(r, r)), dw[k][i][e]);
-          if (DB) db[k][i][e] = add2(db[k][i][e], dy[k][i][e]);
-          const float2 t = DB ? fma2(y, make_float2(cx, cx), make_float2(c0, c0)) : mul2(y, make_float2(cx, cx));
-          o[e] = fma2(mul2(dy[k][i][e], w[k][i][e]), make_float2(r, r), t);
+          const float2 rdy = mul2(dy[k][i][e], make_float2(r, r));
+          if (live) {                                   // (behind the last row: what the places held)
+            dw[k][i][e] = fma2(rdy, y, dw[k][i][e]);
+            if (DB) db[k][i][e] = add2(db[k][i][e], dy[k][i][e]);
+          }
+          const float2 t = DB ? fma2(y, make_float2(cx, cx), make_float2(c0, c0))
+                              : mul2(y, make_float2(cx, cx));
+          o[e] = fma2(rdy, w[k][i][e], t);
         }
         if (at[k][i] < 0 || !live) continue;
         if (a.dx_bf16) {

@@ -43,6 +43,10 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
   };
 #pragma unroll
   for (int i = 0; i < STAGES; ++i) ask(i);
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (!has(k))
+      for (int i = 0; i < STAGES * BATCH; ++i) Slot::zero(s_raw, i * NV + k);
   const auto affine = [&](int k, Pack<float, V>& w, Pack<float, V>& c) {
 #pragma unroll
     for (int e = 0; e < V; ++e) w.w[e] = __float_as_uint(1.f), c.w[e] = 0;
@@ -71,10 +75,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
 #pragma unroll
     for (int u = 0; u < BATCH; ++u)
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        Slot::take(s_raw, (stage * BATCH + u) * NV + k, raw[u][k]);
-        if (!has(k)) raw[u][k].clear();
-      }
+      for (int k = 0; k < NV; ++k) Slot::take(s_raw, (stage * BATCH + u) * NV + k, raw[u][k]);
     ask(stage);
     stage = stage + 1 == STAGES ? 0 : stage + 1;
     float m[BATCH], q[BATCH];

@@ -55,6 +55,10 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
   };
 #pragma unroll
   for (int i = 0; i < STAGES; ++i) ask(i);
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (!has(k))
+      for (int i = 0; i < STAGES * BATCH; ++i) SlotX::zero(s_raw, i * NV + k), SlotG::zero(s_g, i * NV + k);
   const auto weight = [&](int k, Pack<float, V>& w) {
 #pragma unroll
     for (int e = 0; e < V; ++e) w.w[e] = __float_as_uint(1.f);
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
     VecG g[BATCH][NV];
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
-      const bool live = row + (long long)u * row_step < rows;
+      const bool live = BATCH == 1 || row + (long long)u * row_step < rows;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         if constexpr (STAGES > 0) {
@@ -100,7 +104,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
           x[u][k].load((const TX*)a.x + (row + (long long)u * row_step) * a.xs.h + (v0 + k * threads) * V);
           g[u][k].load((const TG*)a.dout + (row + (long long)u * row_step) * a.gs.h + (v0 + k * threads) * V);
         }
-        if (!has(k) || !live) x[u][k].clear(), g[u][k].clear();
+        if (BATCH > 1 && !live) g[u][k].clear();
+        if (STAGES == 0 && !has(k)) x[u][k].clear(), g[u][k].clear();
       }
     }
     if constexpr (STAGES > 0) {
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
       const float cx = -r * r * r * (all[u * kSums + 1] * inv_n);
       const float c0 = DB ? -r * (all[u * kSums + kSums - 1] * inv_n) : 0.f;
       const long long at = row + (long long)u * row_step;
-      const bool live = at < rows;
+      const bool live = BATCH == 1 || at < rows;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         Pack<float, V> pw;
@@ -198,14 +203,13 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
         for (int e = 0; e < V / 2; ++e) {
           float2 y = x[u][k].two(e);
           if (DB) y = add2(y, make_float2(-mean[u], -mean[u]));
-          const float2 dy = g[u][k].two(e);
+          const float2 dy = g[u][k].two(e), rdy = mul2(dy, make_float2(r, r));
           // a row behind the last has dout = 0 but perhaps an infinite r
-          if (live) dw[k][e] = fma2(dy, mul2(y, make_float2(r, r)), dw[k][e]);
+          if (BATCH == 1 || live) dw[k][e] = fma2(rdy, y, dw[k][e]);
           if (DB) db[k][e] = add2(db[k][e], dy);
-          float2 t = make_float2(c0, c0);
-          if (!DB) t = mul2(y, make_float2(cx, cx));
-          if (DB) t = fma2(y, make_float2(cx, cx), t);
-          o[e] = fma2(mul2(dy, pw.two(e)), make_float2(r, r), t);
+          const float2 t = DB ? fma2(y, make_float2(cx, cx), make_float2(c0, c0))
+                              : mul2(y, make_float2(cx, cx));
+          o[e] = fma2(rdy, pw.two(e), t);
         }
         if (!has(k) || !live) continue;
         if (a.dx_bf16) {
