@@ -162,33 +162,43 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
   }
 }
 
-// A programmatic dependent of the kernel that wrote the parts: 32 columns a CTA,
-// the parts dealt to its warps and joined in a fixed order.
-constexpr int kSumWarps = 32;
-__global__ void __launch_bounds__(32 * kSumWarps) sum_parts_kernel(
+// A programmatic dependent of the kernel that wrote the parts: 32 columns a CTA, the parts
+// dealt to its WARPS warps and joined in a fixed order.
+template <int WARPS>
+__global__ void __launch_bounds__(32 * WARPS) sum_parts_kernel(
     const float* __restrict__ parts, int ctas, float* __restrict__ dweight,
     float* __restrict__ dbias, int n) {
-  __shared__ float s[kSumWarps][33];
+  __shared__ float s[WARPS][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cols = n * ((dweight != nullptr) + (dbias != nullptr)), c = blockIdx.x * 32 + lane;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float x = 0.f;
   if (c < cols) {
-#pragma unroll 8
-    for (int p = warp; p < ctas; p += kSumWarps) x += parts[(size_t)p * cols + c];
+    constexpr int kAtOnce = 10;                  // loads under way
+    for (int p0 = warp; p0 < ctas; p0 += kAtOnce * WARPS) {
+      float v[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        v[k] = p0 + k * WARPS < ctas ? parts[(size_t)(p0 + k * WARPS) * cols + c] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) x += v[k];
+    }
   }
   s[warp][lane] = x;
   __syncthreads();
-  // warp w sums column w
-  x = warp_sum(s[lane][warp]);
-  const int col = blockIdx.x * 32 + warp;
-  if (lane != 0 || col >= cols) return;
-  if (dweight == nullptr)
-    dbias[col] = x;
-  else if (col < n)
-    dweight[col] = x;
-  else
-    dbias[col - n] = x;
+  // warp w joins the columns w, w + WARPS, ...
+#pragma unroll
+  for (int k = 0; k < 32; k += WARPS) {
+    const int col = blockIdx.x * 32 + warp + k;
+    x = warp_sum(lane < WARPS ? s[lane][warp + k] : 0.f);
+    if (lane != 0 || col >= cols) continue;
+    if (dweight == nullptr)
+      dbias[col] = x;
+    else if (col < n)
+      dweight[col] = x;
+    else
+      dbias[col - n] = x;
+  }
 }
 
 // C channels a thread, BATCH rows together, STAGES batches under way, at most THREADS threads
@@ -239,7 +249,6 @@ cudaError_t launch_sum_parts(const float* parts, int ctas, float* dweight, float
   const int cols = n * ((dweight != nullptr) + (dbias != nullptr));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((cols + 31) / 32));
-  cfg.blockDim = dim3(32 * kSumWarps);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -247,7 +256,14 @@ cudaError_t launch_sum_parts(const float* parts, int ctas, float* dweight, float
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   count_launches(1);
-  return cudaLaunchKernelEx(&cfg, sum_parts_kernel, parts, ctas, dweight, dbias, n);
+  // as many warps as run at once: of few columns all of a CTA's (4 x 32 columns of 304 parts),
+  // of many eight (448 x 32 of 152 parts: 5.2 us, with 32 warps 9)
+  if (cols >= 4096) {
+    cfg.blockDim = dim3(32 * 8);
+    return cudaLaunchKernelEx(&cfg, sum_parts_kernel<8>, parts, ctas, dweight, dbias, n);
+  }
+  cfg.blockDim = dim3(32 * 32);
+  return cudaLaunchKernelEx(&cfg, sum_parts_kernel<32>, parts, ctas, dweight, dbias, n);
 }
 
 }  // namespace csa
