@@ -281,7 +281,9 @@ cudaError_t fwd_rope(const RowsFwd& a, cudaStream_t st) {
     if constexpr (KIND != kNormNone) return fwd<TI, TO, kRopeNone, V, KIND>(a, st);
     return cudaErrorInvalidValue;
   }
-  if (a.rope.half && !half_by(V, a.rope)) return fwd<TI, TO, kRopeHalf, 2, KIND>(a, st);
+  if (a.rope.half && !half_by(V, a.rope))
+    return V == 8 && half_by(4, a.rope) ? fwd<TI, TO, kRopeHalf, 4, KIND>(a, st)
+                                        : fwd<TI, TO, kRopeHalf, 2, KIND>(a, st);
   if constexpr (KIND == kNormRms && sizeof(TI) == 2) {
     if (a.H >= 4)
       return a.rope.half ? fwd<TI, TO, kRopeHalf, V, KIND, 3>(a, st)

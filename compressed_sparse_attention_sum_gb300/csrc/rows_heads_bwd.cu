@@ -277,6 +277,7 @@ cudaError_t bwd_rope(const RowsBwd& a, int ctas, cudaStream_t st) {
   if (a.rope.turns == nullptr) return bwd<TX, TG, kRopeNone, V, DB>(a, ctas, st);
   if (!a.rope.half) return bwd<TX, TG, kRopeInter, V, DB>(a, ctas, st);
   if (half_by(V, a.rope)) return bwd<TX, TG, kRopeHalf, V, DB>(a, ctas, st);
+  if (half_by(4, a.rope)) return bwd<TX, TG, kRopeHalf, 4, DB>(a, ctas, st);
   return bwd<TX, TG, kRopeHalf, 2, DB>(a, ctas, st);
 }
 
