@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_bwd_kernel(RowsBwd a, int la
     }
     group_sums(sums, lanes);
     const float r = rsqrtf(fmaf(sums[0], inv_n, a.eps));
-    const float cx = -r * r * r * (sums[1] * inv_n);
+    const float cx = -r * (r * (r * (sums[1] * inv_n)));   // (r^3 alone may overflow)
     const float c0 = DB && layer ? -r * (sums[kSums - 1] * inv_n) : 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k)

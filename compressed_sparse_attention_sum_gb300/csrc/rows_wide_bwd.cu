@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       const float r = rsqrtf(fmaf(all[u * kSums], inv_n, a.eps));
-      const float cx = -r * r * r * (all[u * kSums + 1] * inv_n);
+      const float cx = -r * (r * (r * (all[u * kSums + 1] * inv_n)));   // (r^3 alone may overflow)
       const float c0 = DB ? -r * (all[u * kSums + kSums - 1] * inv_n) : 0.f;
       const long long at = row + (long long)u * row_step;
       const bool live = BATCH == 1 || at < rows;

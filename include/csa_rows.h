@@ -26,12 +26,14 @@
  * order of their strides, each stride has to span what the smaller ones reach
  * (INVALID_ARG otherwise).  An output may be its input (same pointer, strides
  * and dtype; of the two inputs of a backward call, either); other overlaps of
- * inputs and outputs give unspecified values.
+ * inputs and outputs give unspecified values.  Gradients come for every row: those
+ * of rows that share an input's elements are the caller's to add.
  *
  * NaN and infinite inputs give unspecified values in their own row, and in the
  * weight and bias gradients of the channels that they reach; channels that a
  * rotation leaves out keep their bits.  Sums of squares are fp32: rows whose
- * magnitudes pass 2^63 / sqrt(width) overflow.
+ * magnitudes pass 2^63 / sqrt(width) overflow, and with eps 0 rows whose spread
+ * is below 2^-62 underflow.
  */
 #ifndef CSA_ROWS_H_
 #define CSA_ROWS_H_

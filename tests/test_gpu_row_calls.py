@@ -165,6 +165,27 @@ def test_norm_of_far_means_and_extreme_rows():
             assert torch.equal(dz[:5], rows.csa_norm_bwd(x, torch.ones_like(x), kind, None, EPS)[0][:5])
 
 
+@pytest.mark.parametrize("n", [64, 2056])
+@pytest.mark.parametrize("size", [1e-15, 1e-6, 1.0, 1e12])
+def test_rows_of_any_size_without_eps(n, size):
+    """eps = 0: the deviation is all that divides, and its cube would leave fp32."""
+    rng = np.random.default_rng(37)
+    x = torch.tensor((rng.standard_normal((5, n)) + 0.25) * size, dtype=F32, device="cuda")
+    dy, dy64 = draw(rng, 5, n)
+    w, w64 = draw(rng, n)
+    rope = plan(orc.freqs(16), 0, True)
+    for kind in (orc.RMS, orc.LAYER):
+        close(rows.csa_norm(x, kind, w, None, 0.0), *orc.norm(f64(x), kind, w64, None, 0.0))
+        want, err = orc.norm_bwd(f64(x), dy64, 0 * dy64, kind, w64, 0.0)
+        for has_bias in (False, True):
+            got = rows.csa_norm_bwd(x, dy, kind, w, 0.0, has_bias=has_bias)
+            close(got[0], want[0], err[0], what=kind)
+            close(got[1], want[1], err[1], what=kind)
+        if n == 64:
+            got = rows.csa_norm_rope_bwd(x[None], dy[None], kind, rope, torch.zeros(5, dtype=I32, device="cuda"), w, 0.0)
+            close(got[0][0], want[0], err[0] + 6 * orc.U * (np.abs(want[0]) + np.abs(dy64 * w64).max() / size), what=kind)
+
+
 @pytest.mark.parametrize("n", [128, 1024])
 def test_many_rows_sum_in_a_fixed_order(n):
     """Rows for every CTA several times over: the sums against fp64, and equal bits from equal calls."""
