@@ -18,6 +18,7 @@ namespace {
 template <typename T, int NV, int KIND, int BATCH, int STAGES, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
   constexpr int V = 16 / sizeof(T);
+  static_assert(THREADS <= 512, "a warp's share for each of 16 lanes");
   using Vec = Pack<T, V>;
   using Slot = VecSlot<Vec, 0>;                         // [stage][row][NV]
   extern __shared__ __align__(16) unsigned char s_raw[];
@@ -115,9 +116,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
         s_part[turn][u][threadIdx.x >> 5] = make_float2(KIND == kNormLayer ? m[u] : 0.f, q[u]);
     }
     __syncthreads();
-    // lane i has warp i's share; the row's sums are those over the lanes
+    // lanes i and 16 + i have warp i's share; the row's sums are those over 16 lanes
     float mean[BATCH], sq[BATCH];
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 15;
     const float cnt = lane < warps ? s_count[lane] : 0.f;
     float2 p[BATCH];
 #pragma unroll
@@ -127,14 +128,14 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
       sq[u] = p[u].y;
     }
     if constexpr (KIND == kNormLayer) {
-      group_sums(mean, 32);
+      group_sums(mean, 16);
 #pragma unroll
       for (int u = 0; u < BATCH; ++u) {
         mean[u] *= inv_n;
         sq[u] = fmaf((p[u].x - mean[u]) * (p[u].x - mean[u]), cnt, sq[u]);
       }
     }
-    group_sums(sq, 32);
+    group_sums(sq, 16);
     turn ^= 1;
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {

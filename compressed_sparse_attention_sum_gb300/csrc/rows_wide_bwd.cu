@@ -25,6 +25,7 @@ template <typename TX, typename TG, int C, bool DB, int BATCH, int STAGES, int T
 __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd a) {
   constexpr int V = sizeof(TX) == 2 && sizeof(TG) == 2 ? 8 : 4, NV = C / V;
   constexpr bool kKeep = C <= 16;
+  static_assert(THREADS <= 512, "a warp's share for each of 16 lanes");
   using VecX = Pack<TX, V>;
   using VecG = Pack<TG, V>;
   using SlotX = VecSlot<VecX, 0>;                       // [stage][row][NV]
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
     }
     constexpr int kSums = DB ? 3 : 2;                   // squares, g xc, g
     float sums[BATCH * kSums];
+    float2 xc[BATCH][NV][V / 2];                        // x less the warp's mean
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       float2 q = make_float2(0.f, 0.f), gx = q, gs = q;
@@ -145,6 +147,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
         for (int e = 0; e < V / 2; ++e) {
           float2 y = x[u][k].two(e);
           if (DB) y = add2(y, make_float2(-m[u], -m[u]));
+          xc[u][k][e] = y;
           const float2 gw = mul2(g[u][k].two(e), pw.two(e));
           if (!DB || has(k)) q = fma2(y, y, q);
           gx = fma2(gw, y, gx);
@@ -163,9 +166,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
             m[u], sums[u * kSums], sums[u * kSums + 1], DB ? sums[u * kSums + kSums - 1] : 0.f);
     }
     __syncthreads();
-    // lane i has warp i's share; the row's sums are those over the lanes
+    // lanes i and 16 + i have warp i's share; the row's sums are those over 16 lanes
     float mean[BATCH], all[BATCH * kSums];
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 15;
     const float cnt = lane < warps ? s_count[lane] : 0.f;
     float4 p[BATCH];
 #pragma unroll
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
       p[u] = lane < warps ? s_part[turn][u][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
       mean[u] = p[u].x * cnt;
     }
-    if (DB && layer) group_sums(mean, 32);
+    if (DB && layer) group_sums(mean, 16);
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
       mean[u] = DB && layer ? mean[u] * inv_n : 0.f;
@@ -182,7 +185,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
       all[u * kSums + 1] = DB ? fmaf(off, p[u].w, p[u].z) : p[u].z;
       if (DB) all[u * kSums + kSums - 1] = layer ? p[u].w : 0.f;
     }
-    group_sums(all, 32);
+    group_sums(all, 16);
     turn ^= 1;
 #pragma unroll
     for (int u = 0; u < BATCH; ++u) {
@@ -201,8 +204,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
         float2 o[V / 2];
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
-          float2 y = x[u][k].two(e);
-          if (DB) y = add2(y, make_float2(-mean[u], -mean[u]));
+          float2 y = xc[u][k][e];
+          if (DB) y = add2(y, make_float2(m[u] - mean[u], m[u] - mean[u]));
           const float2 dy = g[u][k].two(e), rdy = mul2(dy, make_float2(r, r));
           // a row behind the last has dout = 0 but perhaps an infinite r
           if (BATCH == 1 || live) dw[k][e] = fma2(rdy, y, dw[k][e]);
