@@ -128,9 +128,12 @@ struct Pack {
 // THREADS: of the CTA, 0: blockDim.x.
 template <typename VEC, int THREADS>
 struct VecSlot {
-  static constexpr int kPiece = sizeof(VEC) < 16 ? (int)sizeof(VEC) : 16, kPieces = sizeof(VEC) / kPiece;
+  static constexpr int kPiece = sizeof(VEC) < 16 ? (int)sizeof(VEC) : 16;
+  static constexpr int kPieces = sizeof(VEC) / kPiece;
 
-  static __device__ __forceinline__ uint32_t threads() { return THREADS > 0 ? THREADS : blockDim.x; }
+  static __device__ __forceinline__ uint32_t threads() {
+    return THREADS > 0 ? THREADS : blockDim.x;
+  }
   // piece k of slot i of this thread
   static __device__ __forceinline__ unsigned char* place(unsigned char* base, int i, int k) {
     return base + ((uint32_t)(i * kPieces + k) * threads() + threadIdx.x) * kPiece;
@@ -254,7 +257,8 @@ __device__ __forceinline__ void turn_unit(float2 (&v)[2][V / 2], const float (&c
     if (turns == 0) return;                       // all pairs of a unit turn, or none
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) {
-      const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]), s = make_float2(sn[2 * e], sn[2 * e + 1]);
+      const float2 c = make_float2(cs[2 * e], cs[2 * e + 1]);
+      const float2 s = make_float2(sn[2 * e], sn[2 * e + 1]);
       const float2 a = v[0][e], b = v[1][e];
       v[0][e] = fma2(a, c, mul2(b, make_float2(-s.x, -s.y)));
       v[1][e] = fma2(a, s, mul2(b, c));
@@ -315,7 +319,8 @@ struct Walk {
 inline Walk make_walk(int b, int s, int H, bool turned, int groups, int batch, int* ctas) {
   Walk best{};
   best.tokens = turned && H < 4;
-  const long long rows = (long long)b * s * H, inner = best.tokens ? s : H, most = (long long)*ctas * groups;
+  const long long rows = (long long)b * s * H, inner = best.tokens ? s : H;
+  const long long most = (long long)*ctas * groups;
   const double open = turned && !best.tokens ? 0.6 : 0.2;
   // one round: the shortest runs; very many: the longest
   const int longest = rows <= most ? batch : 16, shortest = rows > 64 * most ? 16 : batch;

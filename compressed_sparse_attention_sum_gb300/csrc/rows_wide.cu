@@ -221,12 +221,13 @@ cudaError_t wide_fwd(const RowsFwd& a, cudaStream_t st) {
 // Channels a thread by the width, measured for 64M bf16 channels (floor 39.6 us): more of them
 // mean fewer warps to join, fewer mean more CTAs that do not wait for one another's barriers.
 // 1024: 48.6 us (16 channels 48.8, one warp a row 57); 2048: 44.6 (8: 51, 32: 48);
-// 4096: 42.8 (16: 47, 8: 88); 8192: 42.8 (32: 44 to 50); 16384: 52.7 (16 with 1024 threads
+// 4096: 42.8 (16: 47, 8: 88); 8192: 42.8 (32: 44 to 50); 16384: 41.9 (16 with 1024 threads
 // 88, two CTAs of a cluster a row 114).
 template <typename T, int KIND>
 cudaError_t wide_fwd_width(const RowsFwd& a, cudaStream_t st) {
   constexpr bool half = sizeof(T) == 2;
   // rows for one CTA an SM, or two: nothing to overlap with, so as many threads as there are
+  // (16 x 4096: 1.9 us, without this rule 2.5; 304 x 4096: 2.9 and 3.5; 152 x 1024: 1.9 and 2.0)
   if (a.H <= 2 * 152 && a.d <= 4096) return wide_fwd<T, 8, KIND, 1, 1, 512, 1>(a, st);
   if (a.d <= 1024) return wide_fwd<T, 8, KIND, 2, 3, 128, 6>(a, st);
   if (a.d <= 2048) return wide_fwd<T, 16, KIND, 2, 3, 128, 4>(a, st);
@@ -242,7 +243,8 @@ cudaError_t launch_norm_wide(const RowsFwd& a, cudaStream_t st) {
   using bf = __nv_bfloat16;
   if (a.kind == kNormRms)
     return a.x_bf16 ? wide_fwd_width<bf, kNormRms>(a, st) : wide_fwd_width<float, kNormRms>(a, st);
-  return a.x_bf16 ? wide_fwd_width<bf, kNormLayer>(a, st) : wide_fwd_width<float, kNormLayer>(a, st);
+  return a.x_bf16 ? wide_fwd_width<bf, kNormLayer>(a, st)
+                  : wide_fwd_width<float, kNormLayer>(a, st);
 }
 
 cudaError_t launch_sum_parts(const float* parts, int ctas, float* dweight, float* dbias, int n,
