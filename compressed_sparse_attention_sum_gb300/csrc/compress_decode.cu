@@ -44,7 +44,8 @@ __device__ __forceinline__ void store_ring(const CompressDecodeArgs& a, int i, i
   const T* sc = (const T*)a.score + i * a.sc_bs;
   T* kr = (T*)a.kv_ring + (long long)i * a.R * a.d;
   T* sr = (T*)a.score_ring + (long long)i * a.R * a.sw;
-  const int per = a.d / 8, vecs = a.sw == 1 ? per + 1 : 2 * per;   // of a row (a score of width 1: one)
+  const int per = a.d / 8;
+  const int vecs = a.sw == 1 ? per + 1 : 2 * per;        // of a row (a score of width 1: one)
   constexpr int kAtOnce = 4;
   for (int x0 = (int)threadIdx.x; x0 < rows * vecs; x0 += kAtOnce * (int)blockDim.x) {
     Pack<T, 8> v[kAtOnce];
@@ -53,7 +54,8 @@ __device__ __forceinline__ void store_ring(const CompressDecodeArgs& a, int i, i
     for (int u = 0; u < kAtOnce; ++u) {
       // Padding is skipped here and not by a bound max(k0, -t0): nvcc 13.0 was seen to take
       // that maximum of t0 instead of -t0 (next to max(t0, 0)), and no token was stored.
-      const int x = x0 + u * (int)blockDim.x, row = x / vecs, e = x - row * vecs, k = k0 + row, t = t0 + k;
+      const int x = x0 + u * (int)blockDim.x, row = x / vecs, e = x - row * vecs;
+      const int k = k0 + row, t = t0 + k;
       to[u] = nullptr;
       if (x >= rows * vecs || t < 0) continue;
       const long long slot = t % a.R;
@@ -124,7 +126,10 @@ __global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecode
   const bool live = g < groups && b0 + g < p.count;
   if (live) {
     const int j = p.first + b0 + g;
-    const int lo = max(0, (j + 1 - a.coff) * a.ratio), hi = (j + 1) * a.ratio;
+    // tokens counted from the window's start: a sequence may end at 2^31 - 1, where the step
+    // past the last token would leave 32 bits
+    const int lo = max(0, (j + 1 - a.coff) * a.ratio), len = (j + 1) * a.ratio - lo;
+    const int held = p.t0 - lo;                  // tokens of the rings
     const T* kv = (const T*)a.kv + i * a.kv_bs;
     const T* sc = (const T*)a.score + i * a.sc_bs;
     const T* kr = (const T*)a.kv_ring + (long long)i * a.R * d;
@@ -134,15 +139,15 @@ __global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecode
     for (int e = 0; e < 8; ++e) { m[e] = -INFINITY; l[e] = o[e] = 0.f; }
     int slot = (lo + slice) % a.R;
 #pragma unroll 1
-    for (int t0 = lo + slice; t0 < hi; t0 += slices * kTokens) {
+    for (int t0 = slice; t0 < len; t0 += slices * kTokens) {
       Pack<T, 8> v[kTokens], z[kTokens];
 #pragma unroll
       for (int k = 0; k < kTokens; ++k) {
         const int t = t0 + k * slices;
-        if (t >= hi) continue;
-        const bool fresh = t >= p.t0;
-        const T* row = fresh ? kv + (t - p.t0) * a.kv_rs : kr + (long long)slot * d;
-        const T* srow = fresh ? sc + (t - p.t0) * a.sc_rs : sr + (long long)slot * a.sw;
+        if (t >= len) continue;
+        const bool fresh = t >= held;
+        const T* row = fresh ? kv + (t - held) * a.kv_rs : kr + (long long)slot * d;
+        const T* srow = fresh ? sc + (t - held) * a.sc_rs : sr + (long long)slot * a.sw;
         v[k].load(row + c0);
         if (a.sw == 1) {
           const float z1 = to_f(srow[0]);
@@ -159,7 +164,7 @@ __global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecode
         float2 top = make_float2(m[e], m[e + 1]);
 #pragma unroll
         for (int k = 0; k < kTokens; ++k)
-          if (t0 + k * slices < hi) {
+          if (t0 + k * slices < len) {
             const float2 x = z[k].two(e / 2);
             top.x = fmaxf(top.x, x.x);
             top.y = fmaxf(top.y, x.y);
@@ -171,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecode
         m[e] = top.x, m[e + 1] = top.y;
 #pragma unroll
         for (int k = 0; k < kTokens; ++k)
-          if (t0 + k * slices < hi) {
+          if (t0 + k * slices < len) {
             const float2 x = z[k].two(e / 2), y = v[k].two(e / 2);
             const float2 w = make_float2(weight_of(x.x, m2.x), weight_of(x.y, m2.y));
             l[e] += w.x, l[e + 1] += w.y;

@@ -247,6 +247,25 @@ def test_rings_beyond_32_bits():
     assert torch.equal(rings[0][:, :24], L.kv) and torch.equal(rings[1][:, :24], L.score)
 
 
+@pytest.mark.parametrize("d,ratio,coff,R,small", [(64, 4, 2, 8, 23), (64, 4, 1, 8, 31), (512, 1, 1, 8, 15), (64, 1, 2, 4, 11)])
+def test_the_longest_sequences(d, ratio, coff, R, small):
+    """Sequences that end at 2^31 - 1: the same rows, bit for bit, as of a short one that ends at the same place of its block and
+    of its ring (nothing turned: the rotation alone would tell them apart)."""
+    top = 2 ** 31 - 1
+    assert top % R == small % R and top % ratio == small % ratio
+    for s in (1, 2, 5):
+        L = Layer(79, 2, small, d, ratio, coff, "d", BF, orc.RMS, 0)
+        rings = L.rings(R)
+        L.run(rings, [small - s])
+        far = tuple(t.clone() for t in rings)
+        out, first, counts = L.call(rings, small - s, s)
+        got, far_first, far_counts = L.call(far, small - s, s, lens=ints([top] * 2))
+        k = top // ratio - (top - s) // ratio
+        assert far_first.tolist() == [(top - s) // ratio] * 2 and far_counts.tolist() == counts.tolist() == [k] * 2
+        assert torch.equal(got[:, :k], out[:, :k])
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(rings, far))
+
+
 def test_the_binding_refuses():
     L = Layer(67, 2, 8, 64, 4, 1, "d", BF)
     kr, sr = L.rings(8)
