@@ -164,6 +164,10 @@ def _new(shape, dtype, dev):
     return _empty(tuple(shape), tuple(reversed(strides)), dtype, dev)
 
 
+def _zeros(shape, strides, dtype, dev):
+    return torch.zeros(shape, dtype=dtype, device=f"cuda:{dev}")
+
+
 def _first(t, name):
     dev = t.get_device()
     if dev < 0:
@@ -461,7 +465,8 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
     the tokens complete are pooled (coff blocks a window), normalised (kind CSA_NORM_RMS or
     CSA_NORM_LAYER, 0: not) and turned (rope).  Returns
     (out [b, ceil(s_q / ratio), d], first [b], counts [b]): x, pos0 and counts of
-    csa_cache_write; rows of out from counts on are left as they were.
+    csa_cache_write; rows of out from counts on are left as they were.  Without new tokens
+    (s_q 0) nothing is written; first and counts are zeros unless they were given.
     """
     if stream is not None and _elsewhere(stream, kv):
         return _on(stream, csa_compress_decode, kv, score, kv_ring, score_ring, seq_lens, ratio,
@@ -499,12 +504,13 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
         ob, orow, oc = out.stride()
         if blocks and b and (oc != 1 or (blocks > 1 and orow != d)):
             raise ValueError("out rows must be packed")
+    made = _empty if s_q else _zeros
     if first is None:
-        first = _empty((b,), (1,), _I32, dev)
+        first = made((b,), (1,), _I32, dev)
     else:
         _optional(first, "first", _I32, (b,), dev)
     if counts is None:
-        counts = _empty((b,), (1,), _I32, dev)
+        counts = made((b,), (1,), _I32, dev)
     else:
         _optional(counts, "counts", _I32, (b,), dev)
     _call("csa_compress_decode", dev, stream, kv.data_ptr(), kb, kr, score.data_ptr(),

@@ -247,6 +247,21 @@ def test_rings_beyond_32_bits():
     assert torch.equal(rings[0][:, :24], L.kv) and torch.equal(rings[1][:, :24], L.score)
 
 
+def test_no_new_tokens():
+    L = Layer(83, 3, 8, 64, 4, 2, "d", BF)
+    rings = L.rings(8)
+    L.run(rings, [8])
+    held = [t.clone() for t in rings]
+    torch.full((3,), 77, dtype=I32, device="cuda")     # (what the next tensors of this size would find)
+    torch.full((3,), 77, dtype=I32, device="cuda")
+    out, first, counts = L.call(rings, 8, 0, lens=ints([8, 3, 0]))
+    assert out.shape == (3, 0, 64) and first.tolist() == counts.tolist() == [0] * 3
+    mine = [ints([5] * 3), ints([6] * 3)]
+    L.call(rings, 8, 0, lens=ints([8, 3, 0]), first=mine[0], counts=mine[1])
+    assert mine[0].tolist() == [5] * 3 and mine[1].tolist() == [6] * 3
+    assert all(torch.equal(a, b) for a, b in zip(rings, held))
+
+
 @pytest.mark.parametrize("d,ratio,coff,R,small", [(64, 4, 2, 8, 23), (64, 4, 1, 8, 31), (512, 1, 1, 8, 15), (64, 1, 2, 4, 11)])
 def test_the_longest_sequences(d, ratio, coff, R, small):
     """Sequences that end at 2^31 - 1: the same rows, bit for bit, as of a short one that ends at the same place of its block and
