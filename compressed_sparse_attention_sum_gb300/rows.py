@@ -164,6 +164,14 @@ def _new(shape, dtype, dev):
     return _empty(tuple(shape), tuple(reversed(strides)), dtype, dev)
 
 
+_INT_MAX = 2 ** 31 - 1     # ctypes would pass a larger int's low 32 bits
+
+
+def _fits(name, largest):
+    if largest > _INT_MAX:
+        raise ValueError(f"{name} has a size of 2^31 or more")
+
+
 def _zeros(shape, strides, dtype, dev):
     return torch.zeros(shape, dtype=dtype, device=f"cuda:{dev}")
 
@@ -255,8 +263,10 @@ def _positions(pos, b, s, dev):
 def _heads(shape, name):
     """b, s, H, d of [b, s, H, d] or [b, s, d]."""
     if len(shape) == 4:
+        _fits(name, max(shape))
         return shape
     if len(shape) == 3:
+        _fits(name, max(shape))
         b, s, d = shape
         return b, s, 1, d
     raise ValueError(f"{name} must be [b, s, H, d] or [b, s, d]")
@@ -283,6 +293,7 @@ def csa_norm(x: torch.Tensor, kind: int, weight: Optional[torch.Tensor] = None,
     if not shape:
         raise ValueError("x must be [..., n]")
     n = shape[-1]
+    _fits("x", n)
     if out is None:
         out = _new(shape, x.dtype, dev)
     elif out.dtype is not x.dtype or out.shape != shape or out.get_device() != dev:
@@ -296,6 +307,7 @@ def csa_norm(x: torch.Tensor, kind: int, weight: Optional[torch.Tensor] = None,
 def csa_norm_bwd_workspace_size(rows: int, n: int, want_dweight: bool = True,
                                 want_dbias: bool = False) -> int:
     """Workspace bytes of csa_norm_bwd, and of csa_norm_rope_bwd with b * s * H rows."""
+    _fits("a row", n)
     return int(load_library().csa_norm_bwd_workspace_size(rows, n, int(want_dweight),
                                                           int(want_dbias)))
 
@@ -333,6 +345,7 @@ def csa_norm_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int,
     if not shape:
         raise ValueError("x must be [..., n]")
     n = shape[-1]
+    _fits("x", n)
     rows = x.numel() // n if n else 0
     g_dt = _like(dout, "dout", shape, dev)
     if dx is None:
@@ -478,6 +491,7 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
     if score.ndim != 3 or kv_ring.ndim != 3 or ratio < 1:
         raise ValueError("score and kv_ring must have three dimensions, ratio be at least 1")
     dtype, sw, R = kv.dtype, score.shape[2], kv_ring.shape[1]
+    _fits("kv, a ring or a block", max(b, s_q, d, sw, R, ratio, coff))
     if not (score.dtype is dtype and kv_ring.dtype is dtype and score_ring.dtype is dtype
             and seq_lens.dtype is _I32 and score.get_device() == dev
             and kv_ring.get_device() == dev and score_ring.get_device() == dev

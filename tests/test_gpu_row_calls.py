@@ -209,6 +209,32 @@ def test_many_rows_sum_in_a_fixed_order(n):
     assert torch.equal(only, got[2])
 
 
+def test_sizes_beyond_32_bits_are_refused():
+    """2^32 more than a size that a call takes: nothing of it may count as the small size."""
+    far = 2 ** 32
+    one = torch.ones(1, 1, 1, 64, device="cuda")
+    before = one.clone()
+    rope = plan(orc.freqs(64), 0, False)
+    for axis in range(3):
+        shape = [1, 1, 1, 64]
+        shape[axis] += far
+        x = one.expand(shape)
+        for call in (lambda: rows.csa_rope(x, rope, out=x), lambda: rows.csa_rope_bwd(x, rope, dx=x),
+                     lambda: rows.csa_norm_rope(x, orc.RMS, rope, out=x), lambda: rows.csa_norm_rope_bwd(x, x, orc.RMS, rope, dx=x)):
+            with pytest.raises(ValueError, match="2\\^31"):
+                call()
+    wide = one.view(1, 64).as_strided((1, 64 + far), (1, 0))
+    for call in (lambda: rows.csa_norm(wide, orc.RMS, out=wide), lambda: rows.csa_norm_bwd(wide, wide, orc.RMS, dx=wide),
+                 lambda: rows.csa_norm_bwd_workspace_size(1, 64 + far)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
+    kv, ring, n = torch.ones(1, 1, 64, device="cuda"), torch.ones(1, 8, 64, device="cuda"), torch.ones(1, dtype=I32, device="cuda")
+    for bad in (dict(ratio=4 + far), dict(coff=1 + far)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            rows.csa_compress_decode(kv, kv, ring, ring.clone(), n, **{**dict(ratio=4), **bad})
+    assert torch.equal(one, before)
+
+
 # ---------------------------------------------------------------- rotation
 
 # d, dim, first, half
