@@ -218,6 +218,22 @@ def test_scores_of_minus_infinity():
         assert np.abs(f64(got[0, j]) - want).max() <= 64 * orc.U * np.abs(f64(L.kv)).max()
 
 
+@pytest.mark.parametrize("ratio,coff", [(8, 1), (8, 2), (128, 1)])
+def test_a_block_of_minus_infinities(ratio, coff):
+    """A channel whose scores are all -inf has no weights: NaN there, and nowhere else."""
+    n = 3 * ratio
+    L = Layer(89, 2, n, 64, ratio, coff, "d", F32, 0, 0)
+    want = L.run(L.rings(coff * ratio), [n])
+    L.score[1, :2 * ratio, 5] = float("-inf")
+    got = L.run(L.rings(coff * ratio), [n])
+    none = torch.zeros_like(got, dtype=torch.bool)
+    none[1, :2, 5] = True
+    assert torch.equal(got.isnan(), none)
+    keep = ~none
+    keep[1, :, 5] = False
+    assert torch.equal(got[keep], want[keep])
+
+
 def test_strided_inputs_and_streams():
     L = Layer(61, 3, 30, 64, 4, 2, "d", BF)
     want = L.run(L.rings(8), [30])
