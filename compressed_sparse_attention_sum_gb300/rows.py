@@ -76,11 +76,16 @@ def load_library():
 _entries = {}
 
 
-def _call(name, dev, stream, *args):
-    """Call an entry point with device dev current, on `stream` or on dev's current stream."""
+def _entry(name):
     fn = _entries.get(name)
     if fn is None:
         fn = _entries[name] = getattr(load_library(), name)
+    return fn
+
+
+def _call(name, dev, stream, *args):
+    """Call an entry point with device dev current, on `stream` or on dev's current stream."""
+    fn = _entries.get(name) or _entry(name)
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _call(name, dev, stream, *args)
@@ -201,6 +206,8 @@ def _row_stride(t, name, n):
     if t.is_contiguous():
         return n
     strides, shape = t.stride(), t.shape
+    if len(strides) == 2 and strides[1] == 1:
+        return strides[0]
     if t.numel() == 0:
         return n
     if strides[-1] != 1:
@@ -308,8 +315,21 @@ def csa_norm_bwd_workspace_size(rows: int, n: int, want_dweight: bool = True,
                                 want_dbias: bool = False) -> int:
     """Workspace bytes of csa_norm_bwd, and of csa_norm_rope_bwd with b * s * H rows."""
     _fits("a row", n)
-    return int(load_library().csa_norm_bwd_workspace_size(rows, n, int(want_dweight),
-                                                          int(want_dbias)))
+    return _entry("csa_norm_bwd_workspace_size")(rows, n, 1 if want_dweight else 0,
+                                                 1 if want_dbias else 0)
+
+
+def _bwd_workspace(workspace, rows, n, dweight, dbias, dev):
+    """The tensor, pointer and size of a backward call's workspace."""
+    if workspace is not None:
+        return _workspace(workspace, 0, dev)
+    if dweight is None and dbias is None:
+        return None, None, 0
+    nbytes = csa_norm_bwd_workspace_size(rows, n, dweight is not None, dbias is not None)
+    if nbytes == 0:
+        return None, None, 0
+    ws = _empty((nbytes,), (1,), torch.uint8, dev)
+    return ws, ws.data_ptr(), nbytes
 
 
 def _sums(weight, has_bias, dweight, dbias, n, dev):
@@ -353,9 +373,7 @@ def csa_norm_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int,
     dx_dt = _like(dx, "dx", shape, dev)
     w = _vector(weight, "weight", n, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, n, dev)
-    nbytes = (csa_norm_bwd_workspace_size(rows, n, dweight is not None, dbias is not None)
-              if workspace is None else 0)
-    keep, ws, nbytes = _workspace(workspace, nbytes, dev)
+    keep, ws, nbytes = _bwd_workspace(workspace, rows, n, dweight, dbias, dev)
     _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, kind, w,
           float(eps), dout.data_ptr(), _row_stride(dout, "dout", n), g_dt, dx.data_ptr(),
           _row_stride(dx, "dx", n), dx_dt, None if dweight is None else dweight.data_ptr(),
@@ -449,9 +467,7 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
     dx_dt = _like(dx, "dx", shape, dev)
     w = _vector(weight, "weight", d, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, d, dev)
-    nbytes = (csa_norm_bwd_workspace_size(b * s * H, d, dweight is not None, dbias is not None)
-              if workspace is None else 0)
-    keep, ws, nbytes = _workspace(workspace, nbytes, dev)
+    keep, ws, nbytes = _bwd_workspace(workspace, b * s * H, d, dweight, dbias, dev)
     p, ps = _positions(pos, b, s, dev)
     _call("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind, w,
           float(eps), p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
