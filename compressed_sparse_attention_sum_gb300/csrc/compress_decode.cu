@@ -73,13 +73,17 @@ __device__ __forceinline__ void store_ring(const CompressDecodeArgs& a, int i, i
   }
 }
 
-// 2^((z - m) log2 e); m = -inf (nothing but scores of -inf so far) counts as 0, so that
-// such scores have no weight.
-__device__ __forceinline__ float minus_log2(float m) { return m == -INFINITY ? 0.f : -m * kLog2e; }
+// e^(z - m) of two channels' scores z under maxima m: the difference is formed first, so that a
+// token at the maximum has weight 1 whatever the scores' common offset, also at the lowest values of
+// the type (z log2 e - m log2 e leaves a residue of m's rounding, and infinity where that overflows).
+// m = -inf (nothing but scores of -inf so far) counts as 0, so that such scores have no weight.
 // (ex2.approx is within 2^-22 of itself; weights below 2^-126 are 0)
-__device__ __forceinline__ float weight_of(float z, float m2) {
-  float w;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(z, kLog2e, m2)));
+__device__ __forceinline__ float minus_max(float m) { return m == -INFINITY ? 0.f : -m; }
+__device__ __forceinline__ float2 weight_of(float2 z, float2 minus_m) {
+  const float2 x = mul2(add2(z, minus_m), make_float2(kLog2e, kLog2e));
+  float2 w;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w.y) : "f"(x.y));
   return w;
 }
 
@@ -169,16 +173,15 @@ __global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecode
             top.x = fmaxf(top.x, x.x);
             top.y = fmaxf(top.y, x.y);
           }
-        const float2 m2 = make_float2(minus_log2(top.x), minus_log2(top.y));
-        const float2 old = make_float2(weight_of(m[e], m2.x), weight_of(m[e + 1], m2.y));
+        const float2 minus = make_float2(minus_max(top.x), minus_max(top.y));
+        const float2 old = weight_of(make_float2(m[e], m[e + 1]), minus);
         l[e] *= old.x, l[e + 1] *= old.y;
         o[e] *= old.x, o[e + 1] *= old.y;
         m[e] = top.x, m[e + 1] = top.y;
 #pragma unroll
         for (int k = 0; k < kTokens; ++k)
           if (t0 + k * slices < len) {
-            const float2 x = z[k].two(e / 2), y = v[k].two(e / 2);
-            const float2 w = make_float2(weight_of(x.x, m2.x), weight_of(x.y, m2.y));
+            const float2 y = v[k].two(e / 2), w = weight_of(z[k].two(e / 2), minus);
             l[e] += w.x, l[e + 1] += w.y;
             o[e] = fmaf(w.x, y.x, o[e]), o[e + 1] = fmaf(w.y, y.y, o[e + 1]);
           }
@@ -211,12 +214,14 @@ __global__ void __launch_bounds__(THREADS) compress_decode_kernel(CompressDecode
       float top = -INFINITY, l = 0.f, o = 0.f;
 #pragma unroll 8
       for (int s = 0; s < slices; ++s) top = fmaxf(top, from[s * d]);
-      const float m2 = minus_log2(top);
-#pragma unroll 8
-      for (int s = 0; s < slices; ++s) {
-        const float w = weight_of(from[s * d], m2);
-        l = fmaf(from[part + s * d], w, l);
-        o = fmaf(from[2 * part + s * d], w, o);
+      const float2 minus = make_float2(minus_max(top), minus_max(top));
+#pragma unroll 4
+      for (int s = 0; s < slices; s += 2) {      // (2 slices or more are an even number)
+        const float2 w = weight_of(make_float2(from[s * d], from[(s + 1) * d]), minus);
+        l = fmaf(from[part + s * d], w.x, l);
+        o = fmaf(from[2 * part + s * d], w.x, o);
+        l = fmaf(from[part + (s + 1) * d], w.y, l);
+        o = fmaf(from[2 * part + (s + 1) * d], w.y, o);
       }
       s_row[x] = to_f(from_f<T>(o / l));         // the pooled row's one cast
     }

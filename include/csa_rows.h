@@ -208,7 +208,9 @@ csa_status_t csa_norm_rope_bwd(const void* x, const csa_row_strides_t* x_strides
  * counts[i] new:
  *   pooled row: csa_compress_overlap's entry j, over the positions
  *     max(0, (j + 1 - coff) * ratio) .. (j + 1) * ratio - 1, cast once to dt
- *     (scores of -inf have no weight; a channel of nothing else is NaN)
+ *     (only the scores' distances to the largest of the window count: any finite
+ *     ones, the type's lowest among them, may mask; scores of -inf have no weight, a
+ *     channel of nothing else is NaN)
  *   norm kind csa_norm_kind_t (0: none; weight, bias and eps are then not read)
  *   rotation of position (j + 1) * ratio - 1 (rope NULL: none), as csa_rope
  *   out[i, j - first[i]] = the result, cast once to dt

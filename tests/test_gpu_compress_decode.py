@@ -398,3 +398,60 @@ def test_a_captured_decode_step_matches_the_whole_sequence_calls(bits):
     # logits of at most 1.5^2 |x||y| d scale = 25, summed in 16 steps on each side
     assert (L - ref_l).abs().max().item() <= 25 * 16 * 2 * 2.0 ** -22
     assert torch.equal(Z, rows.csa_rope(O, rope, None, inverse=True))
+
+
+LOWEST = "lowest of the type"
+MASKED = [
+    # dtype, ratio, coff, d, masked tokens, tokens
+    (BF, 128, 1, 512, range(64), 128),                 # whole slices, and a thread's first group
+    (BF, 128, 1, 128, range(120), 128),                # all but the last slice's last tokens
+    (BF, 128, 1, 128, range(8, 256), 256),             # most of a block; a block of nothing else
+    (F32, 4, 2, 64, range(4), 12),                     # the block before a sequence's first real one
+    (F32, 4, 1, 64, range(8), 12),                     # blocks of nothing else
+    (F32, 8, 1, 72, [0, 1, 2, 3, 9, 15, 16, 23], 24),  # a thread's first group; single tokens
+    (BF, 4, 2, 512, [0, 1, 2, 3, 5, 8, 11], 16),
+    (F32, 128, 2, 512, range(100, 260), 384),
+]
+
+
+@pytest.mark.parametrize("value", [-1e4, -1e10, -1e20, -1e30, LOWEST])
+@pytest.mark.parametrize("case", MASKED, ids=str)
+def test_scores_masked_by_a_finite_value(case, value):
+    """Tokens with scores far below the others have no weight, wherever a block has them; a block of nothing else is their mean."""
+    dtype, ratio, coff, d, masked, n = case
+    for sw in ("d", 1):
+        L = Layer(97, 2, n, d, ratio, coff, sw, dtype, 0, 0)
+        L.score[1, list(masked)] = torch.finfo(dtype).min if value is LOWEST else value
+        got = L.run(L.rings(coff * ratio), [n])
+        assert torch.equal(L.run(L.rings(coff * ratio), [1] * n), got)
+        for i in range(2):
+            close(got[i], *L.oracle(i, n), dtype)
+        # the whole-sequence call, where a window has a token that is not masked
+        whole = csa.csa_compress_overlap(L.kv, L.score, ratio, coff)
+        want, err = L.oracle(1, n)
+        off = np.abs(f64(got[1]) - f64(whole[1])) - 2 * (err + orc.STEP[NAME[dtype]] * (np.abs(want) + err)) - 1e-37
+        for j in range(n // ratio):
+            if not set(range(max(0, (j + 1 - coff) * ratio), (j + 1) * ratio)) <= set(masked):
+                assert (off[j] <= 0).all(), j
+
+
+@pytest.mark.parametrize("ratio,coff,d", [(4, 2, 64), (8, 1, 512), (128, 1, 128), (100, 2, 80)])
+@pytest.mark.parametrize("offset", [0.0, 300.0, -3000.0, 30000.0, 1e9, -1e30])
+def test_a_common_offset_of_the_scores(ratio, coff, d, offset):
+    """The softmax does not depend on it; what fp32 leaves of the scores is what both sides are given."""
+    n = 3 * ratio
+    L = Layer(101, 1, n, d, ratio, coff, "d", F32, 0, 0)
+    L.score += offset
+    close(L.run(L.rings(coff * ratio), [n])[0], *L.oracle(0, n), F32)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_token_far_above_the_others(dtype):
+    """It alone has weight: its row, to the bit, also where the difference of two scores leaves the type."""
+    for ratio, coff, top in ((4, 1, 1e4), (16, 1, 1e30), (128, 1, torch.finfo(dtype).max), (4, 2, torch.finfo(dtype).max)):
+        L = Layer(103, 1, 2 * ratio, 64, ratio, coff, "d", dtype, 0, 0)
+        for at in (0, ratio // 2, ratio - 1):
+            L.score.clamp_(-4, 4)
+            L.score[0, ratio + at] = top
+            L.score[0, ratio + (at + 1) % ratio] = torch.finfo(dtype).min
+            assert torch.equal(L.run(L.rings(coff * ratio), [2 * ratio])[0, 1], L.kv[0, ratio + at])
