@@ -15,6 +15,7 @@
 #include "compress_pool.cuh"
 #include "csa_common.cuh"
 #include "csa_kernels.h"
+#include "rows.cuh"
 #include "tcgen05.cuh"
 
 namespace csa {
@@ -212,8 +213,10 @@ __global__ void __launch_bounds__(64) compress_overlap_bwd_kernel(
 // one memory latency covers the block.  The softmax statistics then come from
 // two reductions, each over a warp's lanes by shuffles and over the CTA's
 // warps in shared memory: the block maximum M per channel, then the sums of
-// e_t = 2^(s_t log2(e) - M log2(e)) and of e_t kv_t under that common maximum
-// (one exponential per element, no rescaling of partial sums).
+// e_t = 2^((s_t - M) log2(e)) and of e_t kv_t under that common maximum (one
+// exponential per element, no rescaling of partial sums).  The difference is
+// formed first: s_t log2(e) - M log2(e) leaves a residue of the rounding of
+// M log2(e), of which scores below -1e10 make infinity.
 constexpr int kSplitThreads = 256;
 constexpr int kSplitWarps = kSplitThreads / 32;
 constexpr int kSplitCache = 4;
@@ -227,8 +230,15 @@ int split_slice_groups(int groups) {
 
 struct SplitShared {
   float red[kSplitWarps][2][64];   // per-warp partial maxima / sums of the C channels
-  float M2[64], L[64], P[64];      // M log2(e), sum of e_t, pooled value
+  float M[64], inv[64], P[64];     // maximum (0 for -inf), 1 / sum of e_t, pooled value
 };
+
+// e_t of two channels' scores s under their maxima m
+__device__ __forceinline__ float2 split_weight(const float* s, const float* m) {
+  const float2 x = mul2(add2(make_float2(s[0], s[1]), make_float2(-m[0], -m[1])),
+                        make_float2(kLog2e, kLog2e));
+  return make_float2(umma::ex2(x.x), umma::ex2(x.y));
+}
 
 template <typename T>
 __device__ __forceinline__ void load_score8(const T* scp, int t, int score_width, int c0, float* s) {
@@ -283,31 +293,27 @@ __device__ __forceinline__ void split_block_stats(const T* kvp, const T* scp, in
     float m = S.red[0][0][tid];
 #pragma unroll
     for (int w = 1; w < kSplitWarps; ++w) m = fmaxf(m, S.red[w][0][tid]);
-    S.M2[tid] = m * kLog2e;
+    S.M[tid] = m == -INFINITY ? 0.f : m;
   }
   __syncthreads();
-  float m2[8], l[8], a[8];
+  float m[8], l[8], a[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { m2[i] = S.M2[cgl * 8 + i]; l[i] = 0.f; a[i] = 0.f; }
+  for (int i = 0; i < 8; ++i) { m[i] = S.M[cgl * 8 + i]; l[i] = 0.f; a[i] = 0.f; }
+  auto add = [&](const float* vt, const float* st) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 e = split_weight(st + i, m + i);
+      l[i] += e.x, l[i + 1] += e.y;
+      a[i] = fmaf(e.x, vt[i], a[i]), a[i + 1] = fmaf(e.y, vt[i + 1], a[i + 1]);
+    }
+  };
 #pragma unroll
   for (int k = 0; k < kSplitCache; ++k)
-    if (k < n_my) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float e = umma::ex2(fmaf(sc[k][i], kLog2e, -m2[i]));
-        l[i] += e;
-        a[i] = fmaf(e, vc[k][i], a[i]);
-      }
-    }
+    if (k < n_my) add(vc[k], sc[k]);
   for (int k = kSplitCache; k < n_my; ++k) {
     float vt[8], st[8];
     load_token(kvp, scp, ts + k * TS, d, score_width, c0, vt, st);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float e = umma::ex2(fmaf(st[i], kLog2e, -m2[i]));
-      l[i] += e;
-      a[i] = fmaf(e, vt[i], a[i]);
-    }
+    add(vt, st);
   }
   for (int o = G; o < 32; o <<= 1) {
 #pragma unroll
@@ -328,8 +334,9 @@ __device__ __forceinline__ void split_block_stats(const T* kvp, const T* scp, in
     float L = 0.f, A = 0.f;
 #pragma unroll
     for (int w = 0; w < kSplitWarps; ++w) { L += S.red[w][0][tid]; A += S.red[w][1][tid]; }
-    S.L[tid] = L;
-    S.P[tid] = A / L;
+    const float inv = 1.f / L;
+    S.inv[tid] = inv;
+    S.P[tid] = A * inv;
   }
   __syncthreads();
 }
@@ -387,13 +394,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) compress_bwd_split_kernel(
   const T* scp = score + ((long long)bi * sq + (long long)j * ratio) * score_width;
   float vc[kSplitCache][8], sc[kSplitCache][8];
   split_block_stats(kvp, scp, d, score_width, TS, G, ts, cgl, c0, n_my, vc, sc, S);
-  // w_t = 2^(s_t log2(e) - b2) with b2 = M log2(e) + log2(L)
-  float b2[8], P[8];
+  // w_t = e_t / L
+  const float* m = S.M + cgl * 8;
+  const float* P = S.P + cgl * 8;
+  float gl[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    b2[i] = S.M2[cgl * 8 + i] + log2f(S.L[cgl * 8 + i]);
-    P[i] = S.P[cgl * 8 + i];
-  }
+  for (int i = 0; i < 8; ++i) gl[i] = gv[i] * S.inv[cgl * 8 + i];
   umma::cp_async_wait_all_();
   const unsigned gmask = ((1u << G) - 1u) << (lane & ~(G - 1));
   float* dsp = dscore + ((long long)bi * sq + (long long)j * ratio) * score_width;
@@ -401,9 +407,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) compress_bwd_split_kernel(
     float ds[8], dsum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float w = umma::ex2(fmaf(st[i], kLog2e, -b2[i]));
-      dt[i] = fmaf(w, gv[i], dt[i]);
-      ds[i] = w * gv[i] * (vt[i] - P[i]);
+      const float2 e = split_weight(st + (i & ~1), m + (i & ~1));
+      const float wg = (i & 1 ? e.y : e.x) * gl[i];
+      dt[i] += wg;
+      ds[i] = wg * (vt[i] - P[i]);
       dsum += ds[i];
     }
     store8(dkp + (long long)t * d, dt);
