@@ -4,6 +4,8 @@
 // attention", compressor review).
 #pragma once
 
+#include <cfloat>
+
 #include "csa_common.cuh"
 
 namespace csa {
@@ -48,16 +50,17 @@ __device__ __forceinline__ void pool_block(const T* kvp, const T* scp, int ratio
       pooled[i] = acc / sum;
     }
   } else {
+    // the maximum starts at the lowest finite value, under which scores of -inf have no weight
     float acc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { m[i] = -INFINITY; l[i] = 0.f; acc[i] = 0.f; }
+    for (int i = 0; i < 8; ++i) { m[i] = -FLT_MAX; l[i] = 0.f; acc[i] = 0.f; }
     for (int t = 0; t < ratio; ++t) {
       float vt[8], st[8];
       load_token(kvp, scp, t, d, score_width, c0, vt, st);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float mn = fmaxf(m[i], st[i]);
-        const float alpha = expf(m[i] - mn);  // 0 on the first token (m = -inf)
+        const float alpha = expf(m[i] - mn);
         const float e = expf(st[i] - mn);
         l[i] = l[i] * alpha + e;
         acc[i] = acc[i] * alpha + e * vt[i];

@@ -100,6 +100,7 @@ unsigned long long csa_kernel_launches(void);
  *   out[b, j, c] = sum_t weights_t * kv[b, t, c],
  * with c' = c when score_width == d and c' = 0 when score_width == 1.
  * The softmax, products and sum run in fp32; the result is cast once to dt.
+ * Scores of -inf have no weight (a channel of nothing else is NaN).
  * Tokens past the last complete block (sq % r of them) are not pooled.
  *
  *   kv      in   [b, sq, d] rows of dt; batch stride kv_batch_stride elements

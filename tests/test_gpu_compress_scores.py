@@ -97,3 +97,35 @@ def test_scores_masked_by_a_finite_value(ratio, coff, d, dtype, value):
 @pytest.mark.parametrize("ratio,coff,d", SHAPES)
 def test_a_common_offset_of_the_scores(ratio, coff, d, offset):
     check(ratio, coff, F32, "d", d, 3 * ratio, lambda score: score.add_(offset))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ratio,coff,d", SHAPES)
+def test_scores_of_minus_infinity(ratio, coff, d, dtype):
+    """The start of a block, tokens in the middle, all but one."""
+    n = 4 * ratio
+    mask = torch.zeros(n, dtype=torch.bool)
+    for j in range(4):
+        at = slice(j * ratio, (j + 1) * ratio)
+        mask[at] = torch.tensor([(t < ratio // 2, t % 2 == 0, t != ratio - 1, t != 0)[j] for t in range(ratio)])
+    for sw in ("d", 1):
+        check(ratio, coff, dtype, sw, d, n, lambda score: score[1].masked_fill_(mask.cuda()[:, None], float("-inf")))
+
+
+@pytest.mark.parametrize("ratio,coff,d", SHAPES)
+def test_a_window_of_minus_infinities(ratio, coff, d):
+    """A channel whose scores are all -inf has no weights: NaN there, and nowhere else."""
+    n = (coff + 2) * ratio
+    g = torch.Generator().manual_seed(3)
+    kv, score = torch.randn(1, n, d, generator=g).cuda(), torch.randn(1, n, d, generator=g).cuda()
+    want = csa.csa_compress_overlap(kv, score, ratio, coff)
+    score[:, :coff * ratio, 5] = float("-inf")
+    got = csa.csa_compress_overlap(kv, score, ratio, coff)
+    none = torch.zeros_like(got, dtype=torch.bool)
+    none[:, :coff, 5] = True
+    assert torch.equal(got.isnan(), none)
+    none[:, :, 5] = True
+    assert torch.equal(got[~none], want[~none])
+    w = torch.ones(d, device="cuda")
+    rows = csa.csa_compress_norm_rope(kv, score, ratio, w, 1e-6, 0, 1e4)
+    assert bool(rows[:, :coff].isnan().all()) and bool(rows[:, coff:].isfinite().all())
