@@ -31,7 +31,8 @@
  *
  * NaN and infinite inputs give unspecified values in their own row, and in the
  * weight and bias gradients of the channels that they reach; channels that a
- * rotation leaves out keep their bits.  Sums of squares are fp32: rows whose
+ * rotation leaves out keep their values (infinities and signed zeros among them; a NaN
+ * stays a NaN, in bf16 perhaps another one).  Sums of squares are fp32: rows whose
  * magnitudes pass 2^63 / sqrt(width) overflow, and with eps 0 rows whose spread
  * is below 2^-62 underflow.
  */

@@ -524,3 +524,29 @@ def test_the_binding_refuses():
             pytest.fail(f"call {i} was not refused")
     with pytest.raises(AttributeError):
         rope.first = 8
+
+
+def test_channels_that_are_not_turned_keep_their_values():
+    """Any bits: infinities, zeros of both signs and subnormal values stay as they are, NaNs stay NaNs; out of place, in place and
+    turned back, in vectors that turn in part, in whole or not at all."""
+    rng = np.random.default_rng(41)
+    for dtype, bits in ((BF, torch.int16), (F32, torch.int32)):
+        top = 1 << 8 * dtype.itemsize
+        for d, dim, first, half in TURNS:
+            rest = [c for c in range(d) if not first <= c < first + dim]
+            rope = plan(orc.freqs(dim), first, half)
+            for b, s, H in ((1, 3, 1), (2, 5, 6)):
+                odd = torch.tensor(rng.integers(-top // 2, top // 2, (b, s, H, d)), dtype=bits, device="cuda")
+                odd[0, 0, 0, :4] = torch.tensor([float("inf"), float("-inf"), 0.0, -0.0], dtype=dtype).view(bits).cuda()
+                odd[..., first:first + dim] = draw(rng, b, s, H, dim, dtype=dtype)[0].view(bits)
+                x = odd.view(dtype)
+                nan = x[..., rest].isnan()
+                for inverse in (False, True):
+                    outs = [rows.csa_rope(x, rope, inverse=inverse), rows.csa_rope_bwd(x, rope, inverse=inverse)]
+                    z = x.clone()
+                    outs.append(rows.csa_rope(z, rope, inverse=inverse, out=z))
+                    for y in outs:
+                        at = (dtype, d, dim, first, half, inverse)
+                        assert torch.equal(y[..., rest].isnan(), nan), at
+                        assert torch.equal(y.view(bits)[..., rest][~nan], odd[..., rest][~nan]), at
+                        assert bool(y[..., first:first + dim].isfinite().all()), at
