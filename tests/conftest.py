@@ -11,3 +11,15 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
     config.addinivalue_line("markers", "slow: long-running parity case at full workload size")
+
+
+# This one gives csa_norm_rope_bwd, which without rows writes zeros to dweight, an address that is made up: an error on
+# a machine without a GPU, and a memory fault on one with.
+HOST_ONLY = ("test_row_calls_cpu.py::test_rope_calls_refuse[csa_norm_rope_bwd]",)
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        if item.nodeid.endswith(HOST_ONLY):
+            item.add_marker(pytest.mark.skipif("__import__('torch').cuda.is_available()",
+                                               reason="hands a made-up address to a kernel where there is a GPU"))

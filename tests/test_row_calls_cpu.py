@@ -188,3 +188,23 @@ def test_oracle_gradients_are_those_of_autograd(kind, half):
     got, _ = orc.norm_bwd(x, back, e, kind, w, 1e-5)
     for g, t in zip(got, want):
         assert np.abs(g - t.numpy()).max() < 1e-11
+
+
+def test_gradients_without_rows_look_at_no_pointer_but_the_sums(lib):
+    """... and at none where these are not wanted; misaligned ones are refused before they are written."""
+    def call(dweight, dbias, **size):
+        at = dict(dict(b=2, s=16, H=32), **size)
+        return lib.csa_norm_rope_bwd(None, None, 1, 1, None, 1e-6, None, 0, None, None, None, 0, None, None, 1, dweight, dbias, at["b"],
+                                     at["s"], at["H"], 128, None, 0, None)
+    for none in (dict(b=0), dict(s=0), dict(H=0)):
+        assert call(None, None, **none) == 0
+        assert call(FAKE + 4, None, **none) == call(None, FAKE + 8, **none) == INVALID
+    assert call(None, None) == INVALID
+
+
+def test_made_up_addresses_meet_no_gpu(request):
+    """The one test whose made-up address a kernel would write to is skipped where there is a GPU."""
+    import conftest
+    assert conftest.HOST_ONLY == ("test_row_calls_cpu.py::test_rope_calls_refuse[csa_norm_rope_bwd]",)
+    item = [i for i in request.session.items if i.nodeid.endswith(conftest.HOST_ONLY)]
+    assert all([m.args for m in i.iter_markers("skipif")] == [("__import__('torch').cuda.is_available()",)] for i in item)
