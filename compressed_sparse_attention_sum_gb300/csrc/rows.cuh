@@ -33,10 +33,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 
 // cos and sin of the angles that `turn` (2^-64 turns a position) makes at position pos,
-// of two pairs.  The product modulo 2^64 is exact: whole turns drop out, for any int32
-// position.  Its top 32 bits are the angle to 2^-32 turns; the nearest quarter turn is
-// split off in integers, so the rest x is within pi / 4 and rounds to fp32 with an error
-// below 2^-25 of it.  Minimax polynomials (Remez exchange over that range) of
+// of two pairs.  angle_of gives the angle to 2^-32 turns; the nearest quarter turn is split
+// off in integers, so the rest x is within pi / 4 and rounds to fp32 with an error below
+// 2^-25 of it.  Minimax polynomials (Remez exchange over that range) of
 // (sin x / x - 1) / x^2 and (cos x - 1 + x^2 / 2) / x^4: 1.8e-9 and 1e-10; with all
 // roundings sine and cosine are within 1.7 x 2^-24.
 __device__ __forceinline__ void turn_cos_sin(const long long (&turn)[2], int pos, float2* c,
@@ -45,7 +44,7 @@ __device__ __forceinline__ void turn_cos_sin(const long long (&turn)[2], int pos
   float2 x;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t u = (uint32_t)((unsigned long long)(turn[i] * (long long)pos) >> 32);
+    const uint32_t u = angle_of(turn[i], pos);
     q[i] = (u + 0x20000000u) >> 30;                     // quarter turns, mod 4
     (i ? x.y : x.x) = (float)(int32_t)(u - (q[i] << 30));
   }

@@ -20,6 +20,13 @@ struct RopeArgs {
   bool half, back;        // back: by the negative angle
 };
 
+// The angle that `turn` (2^-64 turns a position) makes at position pos, in 2^-32 turns: the
+// top half of the product modulo 2^64, which is exact, as whole turns drop out.  The factors
+// are unsigned: signed ones would overflow at most positions.
+__host__ __device__ constexpr uint32_t angle_of(int64_t turn, int pos) {
+  return (uint32_t)(((uint64_t)turn * (uint64_t)(int64_t)pos) >> 32);
+}
+
 struct RowStrides {
   long long b, t, h;      // elements
 };

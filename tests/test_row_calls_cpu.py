@@ -5,6 +5,7 @@ the oracle against torch's autograd."""
 import ctypes
 import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -208,3 +209,17 @@ def test_made_up_addresses_meet_no_gpu(request):
     assert conftest.HOST_ONLY == ("test_row_calls_cpu.py::test_rope_calls_refuse[csa_norm_rope_bwd]",)
     item = [i for i in request.session.items if i.nodeid.endswith(conftest.HOST_ONLY)]
     assert all([m.args for m in i.iter_markers("skipif")] == [("__import__('torch').cuda.is_available()",)] for i in item)
+
+
+def test_angles_are_products_modulo_a_turn(tmp_path):
+    """The kernels' angle against whole numbers of any size, as constant expressions: those may not overflow."""
+    top = 2 ** 31
+    cases = [(t, p) for t in (0, 1, 2 ** 62 + 12345, 2 ** 63 - 1, -1, -2 ** 63 + 1, -2 ** 63, 0x123456789abcdef) for p in (0, 1, -1, 3, 1 << 20, top - 1, -top)]
+    lines = [f"static_assert(csa::angle_of((int64_t){t % 2 ** 64}ull, {p if p > -top else '-2147483647 - 1'}) == {t * p % 2 ** 64 >> 32}u, \"\");"
+             for t, p in cases]
+    src = tmp_path / "angles.cpp"
+    src.write_text('#include "rows.h"\n' + "\n".join(lines) + "\n")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc()))), "include")
+    r = subprocess.run(["g++", "-std=c++17", "-fsyntax-only", "-I", build.CSRC, "-I", cuda, "-I", "/usr/local/cuda/include", str(src)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
