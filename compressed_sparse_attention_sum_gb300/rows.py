@@ -100,6 +100,21 @@ def _call(name, dev, stream, *args):
         raise CSAError(name, code)
 
 
+_INT_MAX = 2 ** 31 - 1     # ctypes would pass a larger int's low 32 bits
+
+
+def _fits(name, largest):
+    if largest > _INT_MAX:
+        raise ValueError(f"{name} has a size of 2^31 or more")
+
+
+def _kind(kind):
+    """A norm's kind as the entry points take it (0: none), which refuse the other small ones."""
+    if kind >> 2:
+        raise ValueError("kind must be CSA_NORM_RMS or CSA_NORM_LAYER")
+    return kind
+
+
 class CsaRope:
     """A rotation: `turns` (csa_rope_turns, one of each channel pair) on the device, the
     first turned channel, the pairs' layout ("interleaved" or "half") and a factor on
@@ -115,6 +130,9 @@ class CsaRope:
             raise TypeError("turns must be a contiguous int64 vector (csa_rope_turns)")
         if layout not in _LAYOUTS:
             raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
+        if not 0 <= int(first) <= _INT_MAX:
+            raise ValueError("first must be a channel of the row")
+        _fits("turns", 2 * turns.shape[0])
         put = super().__setattr__
         put("turns", turns)
         put("first", int(first))
@@ -138,6 +156,7 @@ def csa_rope_freqs(dim: int, base: float = 10000.0, scaling: str = "plain", fact
     kept; contexts of original_len positions stretched by factor)."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}")
+    _fits("dim", abs(int(dim)))
     out = torch.empty(max(0, int(dim) // 2), dtype=torch.float64)
     code = load_library().csa_rope_freqs(int(dim), float(base), _SCALINGS[scaling], float(factor),
                                          float(original_len), float(beta_fast), float(beta_slow),
@@ -149,9 +168,11 @@ def csa_rope_freqs(dim: int, base: float = 10000.0, scaling: str = "plain", fact
 
 def csa_rope_turns(freqs, device="cuda") -> torch.Tensor:
     """Frequencies (radians a position) as int64 parts of a turn on `device`."""
-    freqs = torch.as_tensor(freqs, dtype=torch.float64, device="cpu").contiguous()
+    freqs = torch.as_tensor(freqs, dtype=torch.float64, device="cpu")
     if freqs.ndim != 1:
         raise ValueError("freqs must be a vector")
+    _fits("freqs", freqs.shape[0])
+    freqs = freqs.contiguous()
     out = torch.empty(freqs.shape[0], dtype=torch.int64)
     code = load_library().csa_rope_turns(freqs.data_ptr() or None, freqs.shape[0],
                                          out.data_ptr() or None)
@@ -167,14 +188,6 @@ def _new(shape, dtype, dev):
         strides.append(n)
         n *= size
     return _empty(tuple(shape), tuple(reversed(strides)), dtype, dev)
-
-
-_INT_MAX = 2 ** 31 - 1     # ctypes would pass a larger int's low 32 bits
-
-
-def _fits(name, largest):
-    if largest > _INT_MAX:
-        raise ValueError(f"{name} has a size of 2^31 or more")
 
 
 def _zeros(shape, strides, dtype, dev):
@@ -305,7 +318,7 @@ def csa_norm(x: torch.Tensor, kind: int, weight: Optional[torch.Tensor] = None,
         out = _new(shape, x.dtype, dev)
     elif out.dtype is not x.dtype or out.shape != shape or out.get_device() != dev:
         _refuse(dev, out=(out, x.dtype, shape))
-    _call("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, kind,
+    _call("csa_norm", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, _kind(kind),
           _vector(weight, "weight", n, dev), _vector(bias, "bias", n, dev), float(eps),
           out.data_ptr(), _row_stride(out, "out", n), x.numel() // n if n else 0, n)
     return out
@@ -374,7 +387,7 @@ def csa_norm_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int,
     w = _vector(weight, "weight", n, dev)
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, n, dev)
     keep, ws, nbytes = _bwd_workspace(workspace, rows, n, dweight, dbias, dev)
-    _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, kind, w,
+    _call("csa_norm_bwd", dev, stream, x.data_ptr(), _row_stride(x, "x", n), dt, _kind(kind), w,
           float(eps), dout.data_ptr(), _row_stride(dout, "dout", n), g_dt, dx.data_ptr(),
           _row_stride(dx, "dx", n), dx_dt, None if dweight is None else dweight.data_ptr(),
           None if dbias is None else dbias.data_ptr(), rows, n, ws, nbytes)
@@ -440,7 +453,7 @@ def csa_norm_rope(x: torch.Tensor, kind: int, rope: CsaRope, pos: Optional[torch
     elif out.dtype is not x.dtype or out.shape != shape or out.get_device() != dev:
         _refuse(dev, out=(out, x.dtype, shape))
     p, ps = _positions(pos, b, s, dev)
-    _call("csa_norm_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind,
+    _call("csa_norm_rope", dev, stream, x.data_ptr(), _strides(x, "x"), dt, _kind(kind),
           _vector(weight, "weight", d, dev), _vector(bias, "bias", d, dev), float(eps), p, ps,
           _rope(rope, dev), out.data_ptr(), _strides(out, "out"), b, s, H, d)
     return out
@@ -469,7 +482,7 @@ def csa_norm_rope_bwd(x: torch.Tensor, dout: torch.Tensor, kind: int, rope: CsaR
     dweight, dbias = _sums(weight, has_bias, dweight, dbias, d, dev)
     keep, ws, nbytes = _bwd_workspace(workspace, b * s * H, d, dweight, dbias, dev)
     p, ps = _positions(pos, b, s, dev)
-    _call("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, kind, w,
+    _call("csa_norm_rope_bwd", dev, stream, x.data_ptr(), _strides(x, "x"), dt, _kind(kind), w,
           float(eps), p, ps, _rope(rope, dev), dout.data_ptr(), _strides(dout, "dout"), g_dt,
           dx.data_ptr(), _strides(dx, "dx"), dx_dt,
           None if dweight is None else dweight.data_ptr(),
@@ -544,7 +557,7 @@ def csa_compress_decode(kv: torch.Tensor, score: torch.Tensor, kv_ring: torch.Te
     else:
         _optional(counts, "counts", _I32, (b,), dev)
     _call("csa_compress_decode", dev, stream, kv.data_ptr(), kb, kr, score.data_ptr(),
-          sb, sr, sw, kv_ring.data_ptr(), score_ring.data_ptr(), R, seq_lens.data_ptr(), kind, w,
+          sb, sr, sw, kv_ring.data_ptr(), score_ring.data_ptr(), R, seq_lens.data_ptr(), _kind(kind), w,
           bp, float(eps), turned, out.data_ptr(), ob, first.data_ptr(),
           counts.data_ptr(), b, s_q, d, ratio, coff, dt)
     return out, first, counts

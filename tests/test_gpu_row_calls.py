@@ -550,3 +550,19 @@ def test_channels_that_are_not_turned_keep_their_values():
                         assert torch.equal(y[..., rest].isnan(), nan), at
                         assert torch.equal(y.view(bits)[..., rest][~nan], odd[..., rest][~nan]), at
                         assert bool(y[..., first:first + dim].isfinite().all()), at
+
+
+def test_numbers_beyond_32_bits_are_not_cut():
+    """A kind and a first channel that are a good one and 2^32."""
+    x, ring, lens = torch.ones(1, 8, 64, device="cuda"), torch.ones(1, 8, 64, device="cuda"), torch.ones(1, dtype=I32, device="cuda")
+    turns, far = rows.csa_rope_turns(orc.freqs(64)), 2 ** 32
+    rope = rows.CsaRope(turns)
+    for first in (far, -far, -2):
+        with pytest.raises(ValueError, match="first"):
+            rows.CsaRope(turns, first)
+    for kind in (1 + far, 2 - far):
+        for call in (lambda: rows.csa_norm(x, kind), lambda: rows.csa_norm_bwd(x, x, kind), lambda: rows.csa_norm_rope(x, kind, rope),
+                     lambda: rows.csa_norm_rope_bwd(x, x, kind, rope),
+                     lambda: rows.csa_compress_decode(x, x, ring, ring.clone(), lens, 4, kind=kind)):
+            with pytest.raises(ValueError, match="kind"):
+                call()

@@ -211,6 +211,20 @@ def test_made_up_addresses_meet_no_gpu(request):
     assert all([m.args for m in i.iter_markers("skipif")] == [("__import__('torch').cuda.is_available()",)] for i in item)
 
 
+def test_numbers_beyond_32_bits_are_not_cut(lib):
+    """2^32 more than a size that a call takes: nothing of it may count as the small size."""
+    far = 2 ** 32
+    for dim in (64 + far, 64 - far, 2 ** 31):
+        with pytest.raises(ValueError, match="2\\^31"):
+            rows.csa_rope_freqs(dim)
+    with pytest.raises(ValueError, match="2\\^31"):
+        rows.csa_rope_turns(torch.zeros(1, dtype=torch.float64).expand(1 + far), "cpu")
+    for kind in (1 + far, 2 + far, 1 - far, far, -1, 4):
+        with pytest.raises(ValueError, match="kind"):
+            rows._kind(kind)
+    assert [rows._kind(k) for k in (0, 1, 2, 3)] == [0, 1, 2, 3]
+
+
 def test_angles_are_products_modulo_a_turn(tmp_path):
     """The kernels' angle against whole numbers of any size, as constant expressions: those may not overflow."""
     top = 2 ** 31
