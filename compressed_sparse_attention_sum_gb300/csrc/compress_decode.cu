@@ -309,7 +309,7 @@ cudaError_t launch_pool(const CompressDecodeArgs& a, int slices, cudaStream_t st
   const auto k = compress_decode_kernel<T, kTokens, THREADS>;
   const cudaError_t e = once(k, (size_t)(3 * kMaxHeadWidth + THREADS * (8 + 24)) * sizeof(float));
   if (e != cudaSuccess) return e;
-  const int pool = (blocks + groups - 1) / groups, rows = store_rows(a.d);
+  const int pool = (blocks - 1) / groups + 1, rows = store_rows(a.d);   // (blocks may be 2^31 - 1)
   const int store = a.store_here ? (a.s_q + rows - 1) / rows : 0;
   k<<<dim3((unsigned)(pool + store), (unsigned)a.b), threads, smem, st>>>(a, slices, groups, pool, rows);
   count_launches(1);

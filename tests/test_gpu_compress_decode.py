@@ -455,3 +455,19 @@ def test_one_token_far_above_the_others(dtype):
             L.score[0, ratio + at] = top
             L.score[0, ratio + (at + 1) % ratio] = torch.finfo(dtype).min
             assert torch.equal(L.run(L.rings(coff * ratio), [2 * ratio])[0, 1], L.kv[0, ratio + at])
+
+
+@pytest.mark.parametrize("s_q", [2 ** 31 - 1, 2 ** 31 - 300])
+def test_the_longest_call(s_q):
+    """As many new tokens as there can be, each a block: every row of out is its token's."""
+    d = 8
+    row = torch.arange(1, d + 1, device="cuda").to(BF).view(1, 1, d)
+    kv, score = row.expand(1, s_q, d), torch.zeros(1, 1, 1, dtype=BF, device="cuda").expand(1, s_q, 1)
+    kr, sr = torch.zeros(1, 4, d, dtype=BF, device="cuda"), torch.zeros(1, 4, 1, dtype=BF, device="cuda")
+    out, first, counts = rows.csa_compress_decode(kv, score, kr, sr, ints([s_q]), 1)
+    assert out.shape == (1, s_q, d) and first.tolist() == [0] and counts.tolist() == [s_q]
+    for i in range(0, s_q, 1 << 28):
+        assert bool((out[:, i:i + (1 << 28)] == row).all()), i
+    assert bool((kr == row).all())
+    del out
+    torch.cuda.empty_cache()
