@@ -164,11 +164,11 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_kernel(RowsFwd a) {
 }
 
 // A programmatic dependent of the kernel that wrote the parts: 32 columns a CTA, the parts
-// dealt to its WARPS warps and joined in a fixed order.
+// dealt to its WARPS warps and joined in a fixed order.  (No __restrict__: parts are written
+// while this kernel already runs, so they may not be read as constant data.)
 template <int WARPS>
-__global__ void __launch_bounds__(32 * WARPS) sum_parts_kernel(
-    const float* __restrict__ parts, int ctas, float* __restrict__ dweight,
-    float* __restrict__ dbias, int n) {
+__global__ void __launch_bounds__(32 * WARPS) sum_parts_kernel(const float* parts, int ctas,
+                                                               float* dweight, float* dbias, int n) {
   __shared__ float s[WARPS][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cols = n * ((dweight != nullptr) + (dbias != nullptr)), c = blockIdx.x * 32 + lane;

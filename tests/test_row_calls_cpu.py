@@ -3,6 +3,7 @@ exports what include/csa_rows.h declares, refuses invalid arguments before any C
 call, the binding refuses host tensors; frequencies and turns against their formulas;
 the oracle against torch's autograd."""
 import ctypes
+import glob
 import os
 import re
 import subprocess
@@ -237,3 +238,17 @@ def test_angles_are_products_modulo_a_turn(tmp_path):
     r = subprocess.run(["g++", "-std=c++17", "-fsyntax-only", "-I", build.CSRC, "-I", cuda, "-I", "/usr/local/cuda/include", str(src)],
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_dependent_kernels_read_what_their_predecessor_wrote():
+    """A kernel that starts before its predecessor's end and waits for it: its pointers are not __restrict__, of which a const one
+    may be read through the cache of data that no kernel writes meanwhile, and before the wait."""
+    seen = 0
+    for path in glob.glob(os.path.join(build.CSRC, "*.cu")):
+        src = re.sub(r"//[^\n]*", "", open(path).read())
+        starts = [m.start() for m in re.finditer(r"__global__", src)] + [len(src)]
+        for a, b in zip(starts, starts[1:]):
+            if "griddepcontrol.wait" in src[a:b]:
+                seen += 1
+                assert "__restrict__" not in src[a:src.index("{", a)], (os.path.basename(path), src[a:a + 120])
+    assert seen >= 3
