@@ -6,8 +6,8 @@
 //
 // A CTA goes through rows; its threads keep their channels' sums of dweight and dbias in
 // registers to the end.  The next rows of x and dout are on their way into the threads' own
-// places of shared memory.  BATCH rows share a barrier: of a warp's share of a row, its mean,
-// its squares and its sum of g xc about that mean and its sum of g go to shared memory, from
+// places of shared memory.  A row takes one barrier: of a warp's share of it, its mean, its
+// squares and its sum of g xc about that mean and its sum of g go to shared memory, from
 // which every thread joins the row's (exactly, at any mean: sum g (x - mean) = sum g (x - m_w)
 // + (m_w - mean) sum g).
 #include <algorithm>
@@ -21,37 +21,34 @@ namespace {
 
 // DB: whether dbias may be wanted and the norm may be a layer norm; RMS norms without a bias
 // have a kernel of their own, with fewer sums.
-template <typename TX, typename TG, int C, bool DB, int BATCH, int STAGES, int THREADS, int PER_SM>
+template <typename TX, typename TG, int C, bool DB, int STAGES, int THREADS, int PER_SM>
 __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd a) {
   constexpr int V = sizeof(TX) == 2 && sizeof(TG) == 2 ? 8 : 4, NV = C / V;
   constexpr bool kKeep = C <= 16;
   static_assert(THREADS <= 512, "a warp's share for each of 16 lanes");
   using VecX = Pack<TX, V>;
   using VecG = Pack<TG, V>;
-  using SlotX = VecSlot<VecX, 0>;                       // [stage][row][NV]
+  using SlotX = VecSlot<VecX, 0>;                       // [stage][NV]
   using SlotG = VecSlot<VecG, 0>;
   extern __shared__ __align__(16) unsigned char s_raw[];
-  __shared__ __align__(16) float4 s_part[2][BATCH][THREADS / 32];
+  __shared__ __align__(16) float4 s_part[2][THREADS / 32];
   __shared__ float s_count[THREADS / 32];               // elements of each warp
   const int nv = a.d / V, threads = blockDim.x, warps = threads / 32, v0 = threadIdx.x;
-  unsigned char* s_g = s_raw + (size_t)STAGES * BATCH * C * sizeof(TX) * threads;
+  unsigned char* s_g = s_raw + (size_t)STAGES * C * sizeof(TX) * threads;
   const int rows = a.H, row_step = gridDim.x;
   const bool layer = DB && a.kind == kNormLayer;
   const auto has = [&](int k) { return v0 + k * threads < nv; };
   long long asked = blockIdx.x;                         // the next row to ask for
   const auto ask = [&](int stage) {
+    const TX* x = (const TX*)a.x + asked * a.xs.h;
+    const TG* g = (const TG*)a.dout + asked * a.gs.h;
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const TX* x = (const TX*)a.x + asked * a.xs.h;
-      const TG* g = (const TG*)a.dout + asked * a.gs.h;
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (asked < rows && has(k)) {
-          SlotX::ask(s_raw, (stage * BATCH + u) * NV + k, x + (v0 + k * threads) * V);
-          SlotG::ask(s_g, (stage * BATCH + u) * NV + k, g + (v0 + k * threads) * V);
-        }
-      asked += row_step;
-    }
+    for (int k = 0; k < NV; ++k)
+      if (asked < rows && has(k)) {
+        SlotX::ask(s_raw, stage * NV + k, x + (v0 + k * threads) * V);
+        SlotG::ask(s_g, stage * NV + k, g + (v0 + k * threads) * V);
+      }
+    asked += row_step;
     copies_commit();
   };
 #pragma unroll
@@ -59,7 +56,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if (!has(k))
-      for (int i = 0; i < STAGES * BATCH; ++i) SlotX::zero(s_raw, i * NV + k), SlotG::zero(s_g, i * NV + k);
+      for (int i = 0; i < STAGES; ++i) SlotX::zero(s_raw, i * NV + k), SlotG::zero(s_g, i * NV + k);
   const auto weight = [&](int k, Pack<float, V>& w) {
 #pragma unroll
     for (int e = 0; e < V; ++e) w.w[e] = __float_as_uint(1.f);
@@ -89,52 +86,41 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
   const float inv_mine = mine > 0.f ? 1.f / mine : 0.f;
   int stage = 0, turn = 0;
 #pragma unroll 1
-  for (long long row = blockIdx.x; row < rows; row += (long long)BATCH * row_step) {
+  for (long long row = blockIdx.x; row < rows; row += row_step) {
     if constexpr (STAGES > 0) copies_wait<STAGES - 1>();
-    VecX x[BATCH][NV];
-    VecG g[BATCH][NV];
+    VecX x[NV];
+    VecG g[NV];
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const bool live = BATCH == 1 || row + (long long)u * row_step < rows;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if constexpr (STAGES > 0) {
-          SlotX::take(s_raw, (stage * BATCH + u) * NV + k, x[u][k]);
-          SlotG::take(s_g, (stage * BATCH + u) * NV + k, g[u][k]);
-        } else if (has(k) && live) {
-          x[u][k].load((const TX*)a.x + (row + (long long)u * row_step) * a.xs.h + (v0 + k * threads) * V);
-          g[u][k].load((const TG*)a.dout + (row + (long long)u * row_step) * a.gs.h + (v0 + k * threads) * V);
-        }
-        if (BATCH > 1 && !live) g[u][k].clear();
-        if (STAGES == 0 && !has(k)) x[u][k].clear(), g[u][k].clear();
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (STAGES > 0) {
+        SlotX::take(s_raw, stage * NV + k, x[k]);
+        SlotG::take(s_g, stage * NV + k, g[k]);
+      } else if (has(k)) {
+        x[k].load((const TX*)a.x + row * a.xs.h + (v0 + k * threads) * V);
+        g[k].load((const TG*)a.dout + row * a.gs.h + (v0 + k * threads) * V);
+      } else {
+        x[k].clear(), g[k].clear();
       }
     }
     if constexpr (STAGES > 0) {
       ask(stage);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
-    float m[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) m[u] = 0.f;
+    float m[1] = {0.f};
     if (DB && layer) {
+      float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        float2 t = make_float2(0.f, 0.f);
+      for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) t = add2(t, x[u][k].two(e));
-        m[u] = t.x + t.y;
-      }
+        for (int e = 0; e < V / 2; ++e) t = add2(t, x[k].two(e));
+      m[0] = t.x + t.y;
       group_sums(m, 32);
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) m[u] *= inv_mine;
+      m[0] *= inv_mine;
     }
     constexpr int kSums = DB ? 3 : 2;                   // squares, g xc, g
-    float sums[BATCH * kSums];
-    float2 xc[BATCH][NV][V / 2];                        // x less the warp's mean
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
+    float sums[kSums];
+    float2 xc[NV][V / 2];                               // x less the warp's mean
+    {
       float2 q = make_float2(0.f, 0.f), gx = q, gs = q;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -145,87 +131,70 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
           weight(k, pw);
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {
-          float2 y = x[u][k].two(e);
-          if (DB) y = add2(y, make_float2(-m[u], -m[u]));
-          xc[u][k][e] = y;
-          const float2 gw = mul2(g[u][k].two(e), pw.two(e));
+          float2 y = x[k].two(e);
+          if (DB) y = add2(y, make_float2(-m[0], -m[0]));
+          xc[k][e] = y;
+          const float2 gw = mul2(g[k].two(e), pw.two(e));
           if (!DB || has(k)) q = fma2(y, y, q);
           gx = fma2(gw, y, gx);
           if (DB) gs = add2(gs, gw);
         }
       }
-      sums[u * kSums] = q.x + q.y;
-      sums[u * kSums + 1] = gx.x + gx.y;
-      if (DB) sums[u * kSums + kSums - 1] = gs.x + gs.y;
+      sums[0] = q.x + q.y;
+      sums[1] = gx.x + gx.y;
+      if (DB) sums[kSums - 1] = gs.x + gs.y;
     }
     group_sums(sums, 32);
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u)
-        s_part[turn][u][threadIdx.x >> 5] = make_float4(
-            m[u], sums[u * kSums], sums[u * kSums + 1], DB ? sums[u * kSums + kSums - 1] : 0.f);
-    }
+    if ((threadIdx.x & 31) == 0)
+      s_part[turn][threadIdx.x >> 5] =
+          make_float4(m[0], sums[0], sums[1], DB ? sums[kSums - 1] : 0.f);
     __syncthreads();
     // lanes i and 16 + i have warp i's share; the row's sums are those over 16 lanes
-    float mean[BATCH], all[BATCH * kSums];
     const int lane = threadIdx.x & 15;
     const float cnt = lane < warps ? s_count[lane] : 0.f;
-    float4 p[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      p[u] = lane < warps ? s_part[turn][u][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
-      mean[u] = p[u].x * cnt;
-    }
+    const float4 p = lane < warps ? s_part[turn][lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float mean[1] = {p.x * cnt}, all[kSums];
     if (DB && layer) group_sums(mean, 16);
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      mean[u] = DB && layer ? mean[u] * inv_n : 0.f;
-      const float off = DB ? p[u].x - mean[u] : 0.f;
-      all[u * kSums] = DB ? fmaf(off * off, cnt, p[u].y) : p[u].y;
-      all[u * kSums + 1] = DB ? fmaf(off, p[u].w, p[u].z) : p[u].z;
-      if (DB) all[u * kSums + kSums - 1] = layer ? p[u].w : 0.f;
-    }
+    mean[0] = DB && layer ? mean[0] * inv_n : 0.f;
+    const float off = DB ? p.x - mean[0] : 0.f;
+    all[0] = DB ? fmaf(off * off, cnt, p.y) : p.y;
+    all[1] = DB ? fmaf(off, p.w, p.z) : p.z;
+    if (DB) all[kSums - 1] = layer ? p.w : 0.f;
     group_sums(all, 16);
     turn ^= 1;
+    const float r = rsqrtf(fmaf(all[0], inv_n, a.eps));
+    const float cx = -r * (r * (r * (all[1] * inv_n)));   // (r^3 alone may overflow)
+    const float c0 = DB ? -r * (all[kSums - 1] * inv_n) : 0.f;
 #pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const float r = rsqrtf(fmaf(all[u * kSums], inv_n, a.eps));
-      const float cx = -r * (r * (r * (all[u * kSums + 1] * inv_n)));   // (r^3 alone may overflow)
-      const float c0 = DB ? -r * (all[u * kSums + kSums - 1] * inv_n) : 0.f;
-      const long long at = row + (long long)u * row_step;
-      const bool live = BATCH == 1 || at < rows;
+    for (int k = 0; k < NV; ++k) {
+      Pack<float, V> pw;
+      if constexpr (kKeep)
+        pw = w[k];
+      else
+        weight(k, pw);
+      float2 o[V / 2];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        Pack<float, V> pw;
-        if constexpr (kKeep)
-          pw = w[k];
-        else
-          weight(k, pw);
-        float2 o[V / 2];
+      for (int e = 0; e < V / 2; ++e) {
+        float2 y = xc[k][e];
+        if (DB) y = add2(y, make_float2(m[0] - mean[0], m[0] - mean[0]));
+        const float2 dy = g[k].two(e), rdy = mul2(dy, make_float2(r, r));
+        dw[k][e] = fma2(rdy, y, dw[k][e]);
+        if (DB) db[k][e] = add2(db[k][e], dy);
+        const float2 t = DB ? fma2(y, make_float2(cx, cx), make_float2(c0, c0))
+                            : mul2(y, make_float2(cx, cx));
+        o[e] = fma2(rdy, pw.two(e), t);
+      }
+      if (!has(k)) continue;
+      if (a.dx_bf16) {
+        Pack<__nv_bfloat16, V> p;
 #pragma unroll
-        for (int e = 0; e < V / 2; ++e) {
-          float2 y = xc[u][k][e];
-          if (DB) y = add2(y, make_float2(m[u] - mean[u], m[u] - mean[u]));
-          const float2 dy = g[u][k].two(e), rdy = mul2(dy, make_float2(r, r));
-          // a row behind the last has dout = 0 but perhaps an infinite r
-          if (BATCH == 1 || live) dw[k][e] = fma2(rdy, y, dw[k][e]);
-          if (DB) db[k][e] = add2(db[k][e], dy);
-          const float2 t = DB ? fma2(y, make_float2(cx, cx), make_float2(c0, c0))
-                              : mul2(y, make_float2(cx, cx));
-          o[e] = fma2(rdy, pw.two(e), t);
-        }
-        if (!has(k) || !live) continue;
-        if (a.dx_bf16) {
-          Pack<__nv_bfloat16, V> p;
+        for (int e = 0; e < V / 2; ++e) p.set(e, o[e]);
+        p.store((__nv_bfloat16*)a.dx + row * a.ds.h + (v0 + k * threads) * V);
+      } else {
+        Pack<float, V> p;
 #pragma unroll
-          for (int e = 0; e < V / 2; ++e) p.set(e, o[e]);
-          p.store((__nv_bfloat16*)a.dx + at * a.ds.h + (v0 + k * threads) * V);
-        } else {
-          Pack<float, V> p;
-#pragma unroll
-          for (int e = 0; e < V / 2; ++e) p.set(e, o[e]);
-          p.store((float*)a.dx + at * a.ds.h + (v0 + k * threads) * V);
-        }
+        for (int e = 0; e < V / 2; ++e) p.set(e, o[e]);
+        p.store((float*)a.dx + row * a.ds.h + (v0 + k * threads) * V);
       }
     }
   }
@@ -266,11 +235,11 @@ int wide_threads(int n) {
   return (n + c * 32 - 1) / (c * 32) * 32;
 }
 
-template <typename TX, typename TG, int C, bool DB, int BATCH, int STAGES, int THREADS, int PER_SM>
+template <typename TX, typename TG, int C, bool DB, int STAGES, int THREADS, int PER_SM>
 cudaError_t bwd(const RowsBwd& a, int ctas, cudaStream_t st) {
-  constexpr size_t a_thread = (size_t)STAGES * BATCH * C * (sizeof(TX) + sizeof(TG));
+  constexpr size_t a_thread = (size_t)STAGES * C * (sizeof(TX) + sizeof(TG));
   static SmemOnce once;
-  const auto k = norm_wide_bwd_kernel<TX, TG, C, DB, BATCH, STAGES, THREADS, PER_SM>;
+  const auto k = norm_wide_bwd_kernel<TX, TG, C, DB, STAGES, THREADS, PER_SM>;
   const cudaError_t e = once(k, a_thread * THREADS);
   if (e != cudaSuccess) return e;
   const int threads = wide_threads(a.d);
@@ -282,12 +251,12 @@ cudaError_t bwd(const RowsBwd& a, int ctas, cudaStream_t st) {
 template <typename TX, typename TG, bool DB>
 cudaError_t bwd_width(const RowsBwd& a, int ctas, cudaStream_t st) {
   constexpr int bytes = sizeof(TX) + sizeof(TG);        // a channel: 4, 6 or 8
-  if (a.d <= 2048) return bwd<TX, TG, 16, DB, 1, 3, 128, 4>(a, ctas, st);
-  if (a.d <= 4096) return bwd<TX, TG, 16, DB, 1, 3, 256, 2>(a, ctas, st);
-  if (a.d <= 8192) return bwd<TX, TG, 16, DB, 1, bytes == 4 ? 4 : 3, 512, 1>(a, ctas, st);
-  if (a.d <= 16384) return bwd<TX, TG, 32, DB, 1, bytes == 8 ? 1 : 2, 512, 1>(a, ctas, st);
+  if (a.d <= 2048) return bwd<TX, TG, 16, DB, 3, 128, 4>(a, ctas, st);
+  if (a.d <= 4096) return bwd<TX, TG, 16, DB, 3, 256, 2>(a, ctas, st);
+  if (a.d <= 8192) return bwd<TX, TG, 16, DB, bytes == 4 ? 4 : 3, 512, 1>(a, ctas, st);
+  if (a.d <= 16384) return bwd<TX, TG, 32, DB, bytes == 8 ? 1 : 2, 512, 1>(a, ctas, st);
   // two fp32 rows of 32768 channels are more than shared memory: read where they are used
-  return bwd<TX, TG, 64, DB, 1, bytes == 8 ? 0 : 1, 512, 1>(a, ctas, st);
+  return bwd<TX, TG, 64, DB, bytes == 8 ? 0 : 1, 512, 1>(a, ctas, st);
 }
 
 template <typename TX, typename TG>
