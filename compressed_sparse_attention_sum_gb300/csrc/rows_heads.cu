@@ -271,9 +271,19 @@ cudaError_t fwd(const RowsFwd& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// Whether three CTAs an SM go through bf16 rows that are normed and turned, RMS, interleaved.  They
+// hide more latency but read the weight from shared memory and share an SM's issue, and are faster
+// only for long calls whose runs are 16 heads of a token, on all lanes, half of them turned at most
+// (us, two CTAs / three; 64 of 512 channels turned): 64 heads, 2^26 channels 44.2 / 52.4, 1.5 x 2^26
+// 80.8 / 77.6, 2^28 198 / 175, 2^29 377 / 343; 64 of 128 at 2^28 196 / 182.  Others, at 2^28 channels: 8
+// heads 180 / 190, 5 heads 176 / 209, 16 x 192 183 / 227, all 512 turned 183 / 191, half layout 198 / 195
+// (at 2^29 378 / 383); 16 x 2 tokens of 32 x 128 2.9 / 3.2.
+bool three_ctas(const RowsFwd& a, int lanes) {
+  return !a.rope.half && a.H % 16 == 0 && a.d == 16 * lanes && 2 * a.rope.dim <= a.d &&
+         (long long)a.b * a.s * a.H * a.d > 1ll << 26;
+}
+
 // Vectors of 16 bytes; the half layout's pairs on smaller ones where dim or first ask for it.
-// bf16 rows of many heads, normed and turned, are bound by the warps' latency: three CTAs an SM
-// (2 x 8192 tokens of 64 heads x 512 in 343 us, two CTAs 377; one head 44.7, two 38.6).
 template <typename TI, typename TO, int KIND>
 cudaError_t fwd_rope(const RowsFwd& a, cudaStream_t st) {
   constexpr int V = 16 / sizeof(TI);
@@ -285,9 +295,7 @@ cudaError_t fwd_rope(const RowsFwd& a, cudaStream_t st) {
     return V == 8 && half_by(4, a.rope) ? fwd<TI, TO, kRopeHalf, 4, KIND>(a, st)
                                         : fwd<TI, TO, kRopeHalf, 2, KIND>(a, st);
   if constexpr (KIND == kNormRms && sizeof(TI) == 2) {
-    if (a.H >= 4)
-      return a.rope.half ? fwd<TI, TO, kRopeHalf, V, KIND, 3>(a, st)
-                         : fwd<TI, TO, kRopeInter, V, KIND, 3>(a, st);
+    if (three_ctas(a, row_lanes<V>(a.d))) return fwd<TI, TO, kRopeInter, V, KIND, 3>(a, st);
   }
   return a.rope.half ? fwd<TI, TO, kRopeHalf, V, KIND>(a, st)
                      : fwd<TI, TO, kRopeInter, V, KIND>(a, st);

@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) norm_wide_bwd_kernel(RowsBwd 
 // Channels a thread, and the most threads and CTAs an SM, by the width.  16384 x 4096 bf16
 // (floor 59 us), RMS / layer norm with a bias: 66 / 78 us; 8 channels a thread 66 / 115 (twice
 // the warps, whose joins cost as much as their channels), 32 channels 80 / 143 (the layer norm's
-// sums no longer fit the registers), two rows a barrier 88 / 98.
+// sums no longer fit the registers), two rows a barrier 88 / 98.  Other widths of 64M channels:
+// 2048 68 / 78, 8192 68 / 82, 16384 77 / 133 (layer norms and biases spill 200 to 264 bytes a thread),
+// 32768 149 / 251 (all spill); fp32 (floor 119) 2048 to 8192 130 / 141 to 145, 16384 130 / 211, 32768 295 / 444.
 struct WideShape { int c, threads, per_sm; };
 WideShape wide_shape(int n) {
   if (n <= 2048) return {16, 128, 4};

@@ -135,7 +135,7 @@ def test_gradient_of_many_rows(n, count, kind):
 # of two or three; pairs on vectors of 16 bytes and on smaller ones
 TURNED = [(2, 4097, 32, 128, 128, 0, True), (3, 3001, 5, 512, 64, 448, False), (1, 1801, 64, 512, 64, 448, False), (1, 60013, 1, 128, 128, 0, True),
           (2, 20011, 3, 64, 22, 42, False), (2, 9001, 2, 80, 40, 0, True), (1, 3001, 8, 192, 40, 2, True), (5, 8003, 1, 512, 64, 448, False),
-          (2, 1001, 20, 256, 256, 0, False)]
+          (2, 1001, 20, 256, 256, 0, False), (1, 2113, 64, 512, 64, 448, False), (3, 3001, 64, 128, 64, 64, False)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
