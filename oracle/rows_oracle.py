@@ -119,7 +119,7 @@ def compress(kv, score, ratio, coff, kind, weight, bias, eps, f, first, half, sc
         # A weight: its exponent is the distance to the maximum times log2 e, three roundings (of the difference, the
         # constant and the product), in the numerator and in the sum that divides it; a common offset of the scores has
         # no part in it.  8 more roundings and 16 of rescaling; the sums.
-        far = np.where(w > 0, w * (z.max(0) - z), 0.0)
+        far = w * np.where(w > 0, z.max(0) - z, 0.0)
         size = (w * np.abs(kv[t])).sum(0)
         off = (24 + 2 * D) * U * size + 3 * U * ((far * np.abs(kv[t])).sum(0) + far.sum(0) * size)
         e = off + STEP["fp32"] * np.abs(x)
