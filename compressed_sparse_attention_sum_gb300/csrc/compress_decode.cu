@@ -52,8 +52,7 @@ __device__ __forceinline__ void store_ring(const CompressDecodeArgs& a, int i, i
     T* to[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      // Padding is skipped here and not by a bound max(k0, -t0): nvcc 13.0 was seen to take
-      // that maximum of t0 instead of -t0 (next to max(t0, 0)), and no token was stored.
+      // (rows of padding, before the sequence's first token, are skipped one by one)
       const int x = x0 + u * (int)blockDim.x, row = x / vecs, e = x - row * vecs;
       const int k = k0 + row, t = t0 + k;
       to[u] = nullptr;
