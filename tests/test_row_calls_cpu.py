@@ -241,14 +241,15 @@ def test_angles_are_products_modulo_a_turn(tmp_path):
 
 
 def test_dependent_kernels_read_what_their_predecessor_wrote():
-    """A kernel that starts before its predecessor's end and waits for it: its pointers are not __restrict__, of which a const one
-    may be read through the cache of data that no kernel writes meanwhile, and before the wait."""
-    seen = 0
-    for path in glob.glob(os.path.join(build.CSRC, "*.cu")):
+    """A row call's kernel that starts before its predecessor's end and waits for it: its pointers are not __restrict__, of which a
+    const one may be read through the cache of data that no kernel writes meanwhile, and before the wait."""
+    seen = set()
+    for path in glob.glob(os.path.join(build.CSRC, "rows_*.cu")):
         src = re.sub(r"//[^\n]*", "", open(path).read())
         starts = [m.start() for m in re.finditer(r"__global__", src)] + [len(src)]
         for a, b in zip(starts, starts[1:]):
             if "griddepcontrol.wait" in src[a:b]:
-                seen += 1
-                assert "__restrict__" not in src[a:src.index("{", a)], (os.path.basename(path), src[a:a + 120])
-    assert seen >= 3
+                head = src[a:src.index("{", a)]
+                seen.add(re.search(r"(\w+_kernel)\(", head).group(1))
+                assert "__restrict__" not in head, (os.path.basename(path), head)
+    assert seen == {"sum_parts_kernel"}
